@@ -10,11 +10,11 @@ cannot do without.
 
 Definitions (t: token, j: slot, e: expert, l: adapter)
   route    score s[t, e] = softmax over e or 1 / (1 + exp(-logit));  the key of an
-           expert is s + bias[e] where there is a bias, else its logit (the score is
-           monotone in it);  with groups, the `topk_groups` groups with the largest
-           sum of their two largest keys stay;  the top_k experts by key, largest
-           first, ties to the lower index;  weights[t, j] = s / (sum of the chosen s
-           if renormalized) * scale.
+           expert is s + bias[e] where there is a bias, else s, and without groups its
+           logit (the score is monotone in it);  with groups, the `topk_groups` groups
+           with the largest sum of their `group_top` largest keys stay;  the top_k
+           experts by key, largest first, ties to the lower index;  weights[t, j] =
+           s / (sum of the chosen s if renormalized) * scale.
   experts  per token: int8 codes q = rne(x * (127 / amax)), scale amax / 127;
            (g, u) = rows of W13[e] . x;  h = bf16(g / (1 + exp(-g)) * u), quantized
            per row like x;  y = W2[e] . h;  out[t] = sum_j weights[t, j] y[t, j].
@@ -41,16 +41,19 @@ def listed():
     return [
         # one token of a decode step: a launch's latency is all there is
         dict(name="route t1 e64", op="route", tokens=1, experts=64, top_k=8, score="softmax",
-             bias=False, groups=1, topk_groups=1, renorm=True, dtype="bf16"),
+             bias=False, groups=1, topk_groups=1, group_top=1, renorm=True, dtype="bf16"),
         # a serving batch with a balance bias and limited groups
         dict(name="route t64 e256 groups", op="route", tokens=64, experts=256, top_k=8,
-             score="sigmoid", bias=True, groups=8, topk_groups=4, renorm=True, dtype="f32"),
+             score="sigmoid", bias=True, groups=8, topk_groups=4, group_top=2,
+             renorm=True, dtype="f32"),
         # a prompt of ordinary length, an odd number of experts
         dict(name="route t4096 e129", op="route", tokens=4096, experts=129, top_k=6,
-             score="softmax", bias=True, groups=1, topk_groups=1, renorm=False, dtype="f32"),
+             score="softmax", bias=True, groups=1, topk_groups=1, group_top=1,
+             renorm=False, dtype="f32"),
         # the largest prefill batch
         dict(name="route t16384 e256 groups", op="route", tokens=16384, experts=256, top_k=8,
-             score="sigmoid", bias=True, groups=8, topk_groups=4, renorm=True, dtype="f32"),
+             score="sigmoid", bias=True, groups=8, topk_groups=4, group_top=2,
+             renorm=True, dtype="f32"),
         # one token of a decode step: the chosen experts' weights stream from HBM once
         dict(name="experts t1", op="experts", tokens=1, experts=64, top_k=8, hidden=2048,
              inter=768, half=False, out="bf16"),
@@ -100,7 +103,8 @@ def _draw(rng):
         top_k = rng.randint(1, min(8, topk_groups * (experts // groups)))
         return dict(op="route", tokens=_log_int(rng, 1, 16384), experts=experts, top_k=top_k,
                     score=rng.choice(["softmax", "sigmoid"]), bias=rng.random() < 0.6,
-                    groups=groups, topk_groups=topk_groups, renorm=rng.random() < 0.7,
+                    groups=groups, topk_groups=topk_groups, group_top=rng.randint(1, 2),
+                    renorm=rng.random() < 0.7,
                     dtype=rng.choice(["f32", "bf16"]))
     if op == "experts":
         while True:
@@ -230,12 +234,12 @@ def _plain_route(st):
         s = p / p.sum(1, keepdim=True, dtype=torch.float64).float()
     else:
         s = 1.0 / (1.0 + torch.exp(-x))
-    key = s + st["bias"] if st["bias"] is not None else x
+    key = s + st["bias"] if st["bias"] is not None else s if c["groups"] > 1 else x
     if c["groups"] > 1:
         t, per = x.shape[0], c["experts"] // c["groups"]
-        two = torch.sort(key.view(t, c["groups"], per), dim=2, descending=True).values[..., :2]
+        best = torch.sort(key.view(t, c["groups"], per), dim=2, descending=True).values
         keep = torch.zeros((t, c["groups"]), dtype=torch.bool, device=x.device)
-        keep.scatter_(1, _top(two.sum(2), c["topk_groups"]), True)
+        keep.scatter_(1, _top(best[..., :c["group_top"]].sum(2), c["topk_groups"]), True)
         key = torch.where(keep.repeat_interleave(per, 1), key, float("-inf"))
     ids = _top(key, c["top_k"])
     w = s.gather(1, ids)
@@ -323,8 +327,8 @@ def run(state):
         if c["op"] == "route":
             return binding.moe_route(state["logits"], c["top_k"], bias=state["bias"],
                                      score=c["score"], groups=c["groups"],
-                                     topk_groups=c["topk_groups"], renormalize=c["renorm"],
-                                     scale=_scale(c))
+                                     topk_groups=c["topk_groups"], group_top=c["group_top"],
+                                     renormalize=c["renorm"], scale=_scale(c))
         if c["op"] == "experts":
             return binding.w4a8_moe_ffn(state["x"], state["ids"], state["weights"],
                                         state["w13"]["packed"], state["w2"]["packed"],
@@ -347,11 +351,13 @@ def exact(case, seed):
     if case["op"] == "route":
         x = st["logits"].to(f64)
         s = torch.softmax(x, 1) if case["score"] == "softmax" else torch.sigmoid(x)
-        key = x if st["bias"] is None else s + st["bias"].to(f64)
+        key = s if st["bias"] is None and case["groups"] > 1 else x
+        if st["bias"] is not None:
+            key = s + st["bias"].to(f64)
         if case["groups"] > 1:
             per = case["experts"] // case["groups"]
-            rank2 = torch.topk(key.view(len(x), case["groups"], per), min(2, per), 2).values
-            order = torch.argsort(rank2.sum(2), dim=1, descending=True, stable=True)
+            best = torch.topk(key.view(len(x), case["groups"], per), case["group_top"], 2)
+            order = torch.argsort(best.values.sum(2), dim=1, descending=True, stable=True)
             drop = order[:, case["topk_groups"]:]
             member = torch.arange(case["experts"], device=x.device) // per
             lost = (member[None, :, None] == drop[:, None, :]).any(2)
