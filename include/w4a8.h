@@ -397,6 +397,129 @@ w4a8_status dequant_add_requant(const int8_t *q_in, const float *s_in, const voi
                                 hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Rows that choose their weights: routing rows to experts, the experts'
+ * products on stacks of packed weights, and low-rank adapters beside a shared
+ * projection.  Row t of a batch names its experts or its adapter by index in a
+ * device array; the host needs to know only the sizes.
+ * ------------------------------------------------------------------------ */
+
+typedef enum {
+    W4A8_SCORE_SOFTMAX = 0,  /* s[t, e] = exp(x[t, e] - max_e x) / sum_e exp(x[t, e] - max_e x) */
+    W4A8_SCORE_SIGMOID = 1   /* s[t, e] = 1 / (1 + exp(-x[t, e])) */
+} w4a8_score;
+
+#define W4A8_MAX_EXPERTS 1024
+#define W4A8_MAX_TOP_K 32
+#define W4A8_MAX_ROUTE_GROUPS 64
+
+/*
+ * Routing: the top_k experts of every token and their weights.
+ *   logits  [tokens, experts], rows `ld` elements apart (ld >= experts):
+ *           binary32 (W4A8_F32) or bf16 bits (W4A8_BF16)
+ *   bias    [experts] binary32, or NULL: a bias for balance, in the choice only
+ *   ids     [tokens, top_k] int32 (output), largest key first
+ *   weights [tokens, top_k] binary32 (output)
+ * All in binary32, every step rounded once; the softmax's sum is taken in 64
+ * bits and rounded once, so no order of its terms shows in the scores.
+ *   key[t, e] = s[t, e] + bias[e] with a bias, s[t, e] with groups and no bias,
+ *               else x[t, e] itself (the score is monotone in it)
+ *   groups > 1: the experts are `groups` equal runs; only the topk_groups groups
+ *               with the largest sum of their group_top (1 or 2) largest keys
+ *               stay (ties to the lower group)
+ *   ids[t, j]   the top_k largest keys, ties to the lower expert
+ *   weights[t, j] = s / (sum of the chosen s) * scale with renormalize (0 where
+ *               that sum is 0), else s * scale
+ * An expert whose logit is -inf or NaN, or whose bias makes its key so, is never
+ * chosen; +inf counts as the largest finite value.  Slots left over (fewer such
+ * experts than top_k, none at all in a fully masked row) get id -1 and weight 0.
+ * Requires 1 <= top_k <= topk_groups * experts / groups, experts % groups == 0
+ * and 1 <= topk_groups <= groups (W4A8_ERR_SHAPE); at most W4A8_MAX_EXPERTS
+ * experts, W4A8_MAX_TOP_K choices, W4A8_MAX_ROUTE_GROUPS groups, and fewer than
+ * 2^31 tokens (W4A8_ERR_UNSUPPORTED).
+ */
+w4a8_status w4a8_moe_route(const void *logits, w4a8_dtype logits_dtype, int64_t ld,
+                           const float *bias, int64_t tokens, int32_t experts, int32_t top_k,
+                           w4a8_score score, int32_t groups, int32_t topk_groups,
+                           int32_t group_top, int32_t renormalize, float scale, int32_t *ids,
+                           float *weights, hipStream_t stream);
+
+/* Bytes of workspace w4a8_moe_ffn needs (0 for sizes it refuses). */
+size_t w4a8_moe_ffn_workspace_bytes(int64_t tokens, int32_t experts, int32_t top_k,
+                                    int64_t hidden, int64_t inter, w4a8_dtype out_dtype);
+
+/*
+ * Gated feed-forward layer of routed experts on packed 4-bit weights.
+ *   x       [tokens, hidden] bf16
+ *   ids     [tokens, top_k] int32: the expert of each slot; any value outside
+ *           [0, experts) is an unused slot (an expert on another device, a masked
+ *           row), and the same expert may appear twice
+ *   weights [tokens, top_k] binary32
+ *   w13_*   pack_w4_grouped output of the [experts * 2 * inter, hidden] matrix
+ *           whose rows are, expert after expert, inter gate rows and inter up rows
+ *   w2_*    pack_w4_grouped output of the [experts * hidden, inter] matrix
+ *   out     [tokens, hidden] binary32 or bf16 (W4A8_I32 is W4A8_ERR_UNSUPPORTED)
+ * Per used slot (t, j) with e = ids[t, j]:
+ *   q, s    = per-row codes and scale of x[t]: amax = max |x|, inv = 127 * (1 /
+ *             amax), q = rne(x * inv), s = amax * (1 / 127), each operation
+ *             rounded to binary32 (quantize_act_blockwise with block == hidden
+ *             but for the two divisions, taken as products with the rounded
+ *             reciprocal as array programs take them; codes at a half may differ)
+ *   g, u    = the w4a8_gemm outputs (binary32) of the gate and up rows of e
+ *   h       = bf16((g / (1 + exp(-g))) * u), its steps in binary32
+ *   hq, hs  = codes and scale of the row h, as for x
+ *   y       = the w4a8_gemm output of w2 of e, in out's type
+ *   out[t]  = sum over used slots, in order, of weights[t, j] * y  (binary32),
+ *             rounded to out's type; 0 for a token without used slots.
+ * With bf16 outputs each y is thus rounded to bf16 before the sum.
+ * The result does not depend on timing (no sum is taken by atomics).
+ * Requires hidden > 0, inter > 0, both multiples of 64, 1 <= top_k and
+ * 1 <= experts (W4A8_ERR_SHAPE); experts <= W4A8_MAX_EXPERTS, top_k <=
+ * W4A8_MAX_TOP_K, hidden and inter <= W4A8_K_MAX, tokens * hidden, inter *
+ * hidden and tokens * top_k below 2^31, group == 64 (W4A8_ERR_UNSUPPORTED).
+ * The workspace is caller memory, 16-byte aligned, of at least
+ * w4a8_moe_ffn_workspace_bytes(...) bytes (W4A8_ERR_SHAPE); calls that share it
+ * must be ordered.  out may not alias x.
+ */
+w4a8_status w4a8_moe_ffn(const uint16_t *x, const int32_t *ids, const float *weights,
+                         const uint8_t *w13_packed, const uint8_t *w13_grp_scale,
+                         const float *w13_ch_scale, const uint8_t *w2_packed,
+                         const uint8_t *w2_grp_scale, const float *w2_ch_scale, int64_t tokens,
+                         int32_t experts, int32_t top_k, int64_t hidden, int64_t inter,
+                         int32_t group, void *out, w4a8_dtype out_dtype, void *workspace,
+                         size_t ws_bytes, hipStream_t stream);
+
+#define W4A8_LORA_RANK_MAX 128
+#define W4A8_LORA_ADAPTERS_MAX 4095
+
+/* Bytes of workspace w4a8_lora_add needs (0 for sizes it refuses). */
+size_t w4a8_lora_workspace_bytes(int64_t tokens, int32_t adapters, int32_t rank, int64_t k);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection:
+ *   out[t] = y[t] + scale[l] * (b[l] (a[l] x[t])),  l = ids[t]
+ *   x     [tokens, k] bf16, rows ldx elements apart
+ *   a     [adapters, rank, k] bf16;  b [adapters, n, rank] bf16
+ *   scale [adapters] binary32, or NULL (all 1)
+ *   ids   [tokens] int32; outside [0, adapters): no adapter, out[t] = y[t]
+ *   y, out [tokens, n], rows ldy / ldo elements apart, both bf16 (W4A8_BF16) or
+ *         both binary32 (W4A8_F32); out may be y itself (same pointer and stride)
+ * a[l] x[t] is summed in binary32 (parts of k, added in order) and kept so: the
+ * product with b takes it as bf16 terms that hold it to 2^-16 (bf16 out) or
+ * 2^-24 (binary32 out); the sum with y is binary32, rounded once to out's type.
+ * Adapters of lower rank are padded with zero rows of a and columns of b.
+ * Requires rank, k, n > 0, rank, k, n, ldx multiples of 8, ldy and ldo multiples
+ * of 8 (bf16) or 4 (binary32), ldx >= k, ldy, ldo >= n, adapters >= 1
+ * (W4A8_ERR_SHAPE); rank <= W4A8_LORA_RANK_MAX, adapters <=
+ * W4A8_LORA_ADAPTERS_MAX, k <= 2^30, tokens below 2^31, n below 2^24
+ * (W4A8_ERR_UNSUPPORTED).  Workspace rules as for w4a8_moe_ffn.
+ */
+w4a8_status w4a8_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, const uint16_t *b,
+                          const float *scale, const int32_t *ids, int64_t tokens,
+                          int32_t adapters, int32_t rank, int64_t k, int64_t n, const void *y,
+                          int64_t ldy, void *out, int64_t ldo, w4a8_dtype dtype,
+                          void *workspace, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Measurement aid (not part of the method): the int8 matrix-core reference
  * that the GEMMs' utilisation is compared with, and the shader clock.
  * ------------------------------------------------------------------------ */

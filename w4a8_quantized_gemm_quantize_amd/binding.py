@@ -64,6 +64,15 @@ _SIGS = {
     "dequant_add_requant": ([_P, _P, _P, ctypes.c_int, _I64, _I64, _I32, _P, _P, _P, _P],
                             ctypes.c_int),
     "w4a8_probe_mfma_i8": ([_I64, _I32, _P, _P, _P], ctypes.c_int),
+    "w4a8_moe_route": ([_P, ctypes.c_int, _I64, _P, _I64, _I32, _I32, ctypes.c_int, _I32, _I32,
+                        _I32, _I32, ctypes.c_float, _P, _P, _P], ctypes.c_int),
+    "w4a8_moe_ffn_workspace_bytes": ([_I64, _I32, _I32, _I64, _I64, ctypes.c_int],
+                                     ctypes.c_size_t),
+    "w4a8_moe_ffn": ([_P] * 9 + [_I64, _I32, _I32, _I64, _I64, _I32, _P, ctypes.c_int, _P,
+                                 ctypes.c_size_t, _P], ctypes.c_int),
+    "w4a8_lora_workspace_bytes": ([_I64, _I32, _I32, _I64], ctypes.c_size_t),
+    "w4a8_lora_add": ([_P, _I64, _P, _P, _P, _P, _I64, _I32, _I32, _I64, _I64, _P, _I64, _P,
+                       _I64, ctypes.c_int, _P, ctypes.c_size_t, _P], ctypes.c_int),
     "w4a8_gemm_bf16act_noalloc": ([_P, _P, _P, _P, _I64, _I64, _I64, _I32, _P, ctypes.c_int, _P],
                                   ctypes.c_int),
 }
@@ -512,6 +521,142 @@ def dequant_add_requant(q_in, s_in, x, block: int, want_sum: bool = False, q_out
                                     block, _ptr(sum_out), _ptr(q_out), _ptr(s_out),
                                     _stream(stream)))
     return q_out, s_out, sum_out
+
+
+# ------------------------------------------------ rows that choose weights --
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _rows(fn, t, dtypes, cols, name):
+    """A 2-D CUDA tensor of one of `dtypes` and `cols` columns whose rows are
+    contiguous; returns the elements from one row to the next."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2):
+        raise ValueError(f"{fn}: {name} must be a 2-D CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{fn}: {name} must be of dtype {' or '.join(map(str, dtypes))}, "
+                         f"not {t.dtype}")
+    if t.shape[1] != cols:
+        raise W4A8SizeError(fn, f"a row of {name}", t.shape[1], cols)
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{fn}: rows of {name} must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else cols
+
+
+def moe_route(logits, top_k: int, bias=None, score: str = "softmax", groups: int = 1,
+              topk_groups: int = 1, group_top: int = 2, renormalize: bool = True,
+              scale: float = 1.0, ids=None, weights=None, stream=None):
+    """logits float32 or bfloat16 [tokens, experts] (rows may be strided) ->
+    (ids int32 [tokens, top_k], weights float32 [tokens, top_k]): the experts of each
+    token, largest key first, -1 with weight 0 where none is left."""
+    fn = "moe_route"
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError(f"{fn}: logits must be a 2-D CUDA tensor")
+    if score not in _SCORES:
+        raise ValueError(f"{fn}: score must be 'softmax' or 'sigmoid', not {score!r}")
+    tokens, experts = logits.shape
+    ld = _rows(fn, logits, tuple(_FLOATS), experts, "logits")
+    if ids is None:
+        ids = _empty(stream, (tokens, top_k), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = _empty(stream, (tokens, top_k), dtype=torch.float32, device=logits.device)
+    _sized(fn, bias, _F32, experts, "bias")
+    _sized(fn, ids, (torch.int32,), tokens * top_k, "ids")
+    _sized(fn, weights, _F32, tokens * top_k, "weights")
+    _check(fn, _lib.w4a8_moe_route(_ptr(logits), _FLOATS[logits.dtype], ld, _ptr(bias), tokens,
+                                   experts, top_k, _SCORES[score], groups, topk_groups,
+                                   group_top, int(renormalize), scale, _ptr(ids), _ptr(weights),
+                                   _stream(stream)))
+    return ids, weights
+
+
+def moe_ffn_workspace_bytes(tokens: int, experts: int, top_k: int, hidden: int, inter: int,
+                            out_dtype=torch.bfloat16) -> int:
+    return int(_lib.w4a8_moe_ffn_workspace_bytes(tokens, experts, top_k, hidden, inter,
+                                                 _FLOATS[out_dtype]))
+
+
+def w4a8_moe_ffn(x, ids, weights, w13, w2, inter: int, out_dtype=torch.bfloat16,
+                 group: int = GROUP, out=None, workspace=None, stream=None):
+    """Gated feed-forward layer of routed experts.
+
+    x bf16 [tokens, hidden]; ids int32 and weights float32 [tokens, top_k] (moe_route's;
+    an id outside the experts is an unused slot); w13 and w2 the (w_packed, grp_scale,
+    ch_scale) of pack_w4_grouped for the stacked matrices [experts * 2 * inter, hidden]
+    (per expert inter gate rows, then inter up rows) and [experts * hidden, inter]
+    -> out [tokens, hidden] (bfloat16 or float32)."""
+    fn = "w4a8_moe_ffn"
+    _dev(x, torch.bfloat16, "x")
+    _dev(ids, torch.int32, "ids")
+    tokens, hidden = x.shape
+    if ids.dim() != 2 or ids.shape[0] != tokens:
+        raise ValueError(f"{fn}: ids must be [tokens, top_k]")
+    if out is None and out_dtype not in _FLOATS:
+        raise ValueError(f"{fn}: out_dtype must be float32 or bfloat16")
+    top_k = ids.shape[1]
+    c13 = w13[2]
+    if inter <= 0 or c13.numel() % (2 * inter):
+        raise W4A8SizeError(fn, "w13 ch_scale", c13.numel(), 2 * inter)
+    experts = c13.numel() // (2 * inter)
+    if out is None:
+        out = _empty(stream, (tokens, hidden), dtype=out_dtype, device=x.device)
+    _sized(fn, out, tuple(_FLOATS), tokens * hidden, "out")
+    need = moe_ffn_workspace_bytes(tokens, experts, top_k, hidden, inter, out.dtype)
+    if workspace is None:
+        workspace = _empty(stream, (max(need, 16),), dtype=torch.uint8, device=x.device)
+    _sized(fn, weights, _F32, tokens * top_k, "weights")
+    for name, (wp, gs, cs), n, k in (("w13", w13, experts * 2 * inter, hidden),
+                                     ("w2", w2, experts * hidden, inter)):
+        _sized(fn, wp, _U8, n * k // 2, name + " w_packed")
+        _sized(fn, gs, _U8, n * _per(k, group), name + " grp_scale")
+        _sized(fn, cs, _F32, n, name + " ch_scale")
+    _sized(fn, workspace, _U8, 0, "workspace")
+    _check(fn, _lib.w4a8_moe_ffn(_ptr(x), _ptr(ids), _ptr(weights), _ptr(w13[0]), _ptr(w13[1]),
+                                 _ptr(c13), _ptr(w2[0]), _ptr(w2[1]), _ptr(w2[2]), tokens,
+                                 experts, top_k, hidden, inter, group, _ptr(out),
+                                 _FLOATS[out.dtype], _ptr(workspace), workspace.numel(),
+                                 _stream(stream)))
+    return out
+
+
+def lora_workspace_bytes(tokens: int, adapters: int, rank: int, k: int) -> int:
+    return int(_lib.w4a8_lora_workspace_bytes(tokens, adapters, rank, k))
+
+
+def lora_add(x, a, b, ids, y, scale=None, out=None, workspace=None, stream=None):
+    """out = y + scale[l] * ((x a[l]^T) b[l]^T) with l = ids[t] for each row t (outside the
+    adapters: out = y).  x bf16 [tokens, k] and y, out [tokens, n] (both bfloat16 or both
+    float32) may have strided rows; a bf16 [adapters, rank, k], b bf16 [adapters, n, rank],
+    ids int32 [tokens], scale float32 [adapters] or None.  out may be y."""
+    fn = "lora_add"
+    _dev(a, torch.bfloat16, "a")
+    _dev(b, torch.bfloat16, "b")
+    if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+        raise ValueError(f"{fn}: a must be [adapters, rank, k] and b [adapters, n, rank]")
+    adapters, rank, k = a.shape
+    n = b.shape[1]
+    ldx = _rows(fn, x, (torch.bfloat16,), k, "x")
+    ldy = _rows(fn, y, tuple(_FLOATS), n, "y")
+    tokens = x.shape[0]
+    if y.shape[0] != tokens:
+        raise W4A8SizeError(fn, "y (rows)", y.shape[0], tokens)
+    if out is None:
+        out = _empty(stream, (tokens, n), dtype=y.dtype, device=y.device)
+    ldo = _rows(fn, out, (y.dtype,), n, "out")
+    if out.shape[0] != tokens:
+        raise W4A8SizeError(fn, "out (rows)", out.shape[0], tokens)
+    _sized(fn, ids, (torch.int32,), tokens, "ids")
+    _sized(fn, scale, _F32, adapters, "scale")
+    if workspace is None:
+        need = lora_workspace_bytes(tokens, adapters, rank, k)
+        workspace = _empty(stream, (max(need, 16),), dtype=torch.uint8, device=x.device)
+    _sized(fn, workspace, _U8, 0, "workspace")
+    _check(fn, _lib.w4a8_lora_add(_ptr(x), ldx, _ptr(a), _ptr(b), _ptr(scale), _ptr(ids), tokens,
+                                  adapters, rank, k, n, _ptr(y), ldy, _ptr(out), ldo,
+                                  _FLOATS[y.dtype], _ptr(workspace), workspace.numel(),
+                                  _stream(stream)))
+    return out
 
 
 # -------------------------------------------------------- measurement aid --

@@ -130,6 +130,35 @@ w4a8_status check_gemm_args(const void *a, const float *a_scale, bool need_a_sca
     return W4A8_OK;
 }
 
+w4a8_status check_moe_shape(int64_t tokens, int32_t experts, int32_t top_k, int64_t hidden,
+                            int64_t inter, int32_t group, w4a8_dtype out_dtype) {
+    if (tokens < 0 || experts < 1 || top_k < 1 || hidden <= 0 || inter <= 0)
+        return W4A8_ERR_SHAPE;
+    if (group != W4A8_GROUP) return W4A8_ERR_UNSUPPORTED;
+    if (hidden % W4A8_GROUP != 0 || inter % W4A8_GROUP != 0) return W4A8_ERR_SHAPE;
+    if (out_dtype != W4A8_F32 && out_dtype != W4A8_BF16) return W4A8_ERR_UNSUPPORTED;
+    // 32-bit offsets inside one expert's weights, x and the row indices
+    if (experts > W4A8_MAX_EXPERTS || top_k > W4A8_MAX_TOP_K || hidden > W4A8_K_MAX ||
+        inter > W4A8_K_MAX || inter * hidden > INT32_MAX || tokens > INT32_MAX / hidden ||
+        tokens > INT32_MAX / top_k)
+        return W4A8_ERR_UNSUPPORTED;
+    // workgroups of the products: row tiles x 256-column tiles
+    const int64_t cols = (2 * inter > hidden ? 2 * inter : hidden) / 256 + 1;
+    if ((tokens * top_k / 16 + experts) * cols > INT32_MAX) return W4A8_ERR_UNSUPPORTED;
+    return W4A8_OK;
+}
+
+w4a8_status check_lora_shape(int64_t tokens, int32_t adapters, int32_t rank, int64_t k,
+                             int64_t n) {
+    if (tokens < 0 || adapters < 1 || rank < 1 || k < 1 || n < 1 || rank % 8 != 0 || k % 8 != 0 ||
+        n % 8 != 0)
+        return W4A8_ERR_SHAPE;
+    if (rank > W4A8_LORA_RANK_MAX || adapters > W4A8_LORA_ADAPTERS_MAX ||
+        k > ((int64_t)1 << 30) || n >= ((int64_t)1 << 24) || tokens > INT32_MAX)
+        return W4A8_ERR_UNSUPPORTED;
+    return W4A8_OK;
+}
+
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // Workspace checks of the fused entry points; on success sets the code and
@@ -475,6 +504,112 @@ w4a8_status w4a8_probe_mfma_i8(int64_t workgroups, int32_t iters, int32_t *sink,
     if (!sink || !clocks) return W4A8_ERR_NULL;
     if (!aligned16(sink) || !aligned16(clocks)) return W4A8_ERR_MISALIGNED;
     return finish(w4a8::launch_mfma_probe(workgroups, iters, sink, clocks, stream), stream);
+}
+
+/* ------------------------------------------- rows that choose their weights */
+
+w4a8_status w4a8_moe_route(const void *logits, w4a8_dtype logits_dtype, int64_t ld,
+                           const float *bias, int64_t tokens, int32_t experts, int32_t top_k,
+                           w4a8_score score, int32_t groups, int32_t topk_groups,
+                           int32_t group_top, int32_t renormalize, float scale, int32_t *ids,
+                           float *weights, hipStream_t stream) {
+    if (tokens < 0 || experts < 1 || top_k < 1 || groups < 1 || topk_groups < 1 ||
+        topk_groups > groups || experts % groups != 0 || ld < experts ||
+        (int64_t)top_k > (int64_t)topk_groups * (experts / groups))
+        return W4A8_ERR_SHAPE;
+    if (experts > W4A8_MAX_EXPERTS || top_k > W4A8_MAX_TOP_K || groups > W4A8_MAX_ROUTE_GROUPS ||
+        tokens > INT32_MAX || (group_top != 1 && group_top != 2) ||
+        (logits_dtype != W4A8_F32 && logits_dtype != W4A8_BF16) ||
+        (score != W4A8_SCORE_SOFTMAX && score != W4A8_SCORE_SIGMOID))
+        return W4A8_ERR_UNSUPPORTED;
+    if (tokens == 0) return W4A8_OK;
+    if (!logits || !ids || !weights) return W4A8_ERR_NULL;
+    if (!aligned16(logits) || !aligned16(ids) || !aligned16(weights) || !aligned16(bias))
+        return W4A8_ERR_MISALIGNED;
+    return finish(w4a8::launch_route(logits, logits_dtype == W4A8_BF16, ld, bias, tokens, experts,
+                                     top_k, score == W4A8_SCORE_SIGMOID, groups, topk_groups,
+                                     group_top, renormalize != 0, scale, ids, weights, stream),
+                  stream);
+}
+
+size_t w4a8_moe_ffn_workspace_bytes(int64_t tokens, int32_t experts, int32_t top_k,
+                                    int64_t hidden, int64_t inter, w4a8_dtype out_dtype) {
+    if (tokens <= 0 || check_moe_shape(tokens, experts, top_k, hidden, inter, W4A8_GROUP,
+                                       out_dtype) != W4A8_OK)
+        return 0;
+    return w4a8::moe_workspace_bytes(tokens, experts, top_k, hidden, inter, (int)out_dtype);
+}
+
+w4a8_status w4a8_moe_ffn(const uint16_t *x, const int32_t *ids, const float *weights,
+                         const uint8_t *w13_packed, const uint8_t *w13_grp_scale,
+                         const float *w13_ch_scale, const uint8_t *w2_packed,
+                         const uint8_t *w2_grp_scale, const float *w2_ch_scale, int64_t tokens,
+                         int32_t experts, int32_t top_k, int64_t hidden, int64_t inter,
+                         int32_t group, void *out, w4a8_dtype out_dtype, void *workspace,
+                         size_t ws_bytes, hipStream_t stream) {
+    w4a8_status st = check_moe_shape(tokens, experts, top_k, hidden, inter, group, out_dtype);
+    if (st != W4A8_OK) return st;
+    if (tokens == 0) return W4A8_OK;
+    const void *needed[] = {x, ids, weights, w13_packed, w13_grp_scale, w13_ch_scale,
+                            w2_packed, w2_grp_scale, w2_ch_scale, out, workspace};
+    for (const void *p : needed)
+        if (!p) return W4A8_ERR_NULL;
+    for (const void *p : needed)
+        if (!aligned16(p)) return W4A8_ERR_MISALIGNED;
+    if (ws_bytes < w4a8::moe_workspace_bytes(tokens, experts, top_k, hidden, inter,
+                                             (int)out_dtype))
+        return W4A8_ERR_SHAPE;
+    st = debug_check_inputs(stream, {{x, (size_t)(tokens * hidden), true},
+                                     {weights, (size_t)(tokens * top_k), false},
+                                     {w13_ch_scale, (size_t)(experts * 2 * inter), false},
+                                     {w2_ch_scale, (size_t)(experts * hidden), false}});
+    if (st != W4A8_OK) return st;
+    return finish(w4a8::launch_moe_ffn(x, ids, weights, w13_packed, w13_grp_scale, w13_ch_scale,
+                                       w2_packed, w2_grp_scale, w2_ch_scale, tokens, experts,
+                                       top_k, hidden, inter, out, (int)out_dtype, workspace,
+                                       stream),
+                  stream);
+}
+
+size_t w4a8_lora_workspace_bytes(int64_t tokens, int32_t adapters, int32_t rank, int64_t k) {
+    if (tokens <= 0 || check_lora_shape(tokens, adapters, rank, k, 8) != W4A8_OK) return 0;
+    return w4a8::lora_workspace_bytes(tokens, adapters, rank, k);
+}
+
+w4a8_status w4a8_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, const uint16_t *b,
+                          const float *scale, const int32_t *ids, int64_t tokens,
+                          int32_t adapters, int32_t rank, int64_t k, int64_t n, const void *y,
+                          int64_t ldy, void *out, int64_t ldo, w4a8_dtype dtype,
+                          void *workspace, size_t ws_bytes, hipStream_t stream) {
+    w4a8_status st = check_lora_shape(tokens, adapters, rank, k, n);
+    if (st != W4A8_OK) return st;
+    if (dtype != W4A8_F32 && dtype != W4A8_BF16) return W4A8_ERR_UNSUPPORTED;
+    const int64_t step = dtype == W4A8_BF16 ? 8 : 4;
+    if (ldx < k || ldy < n || ldo < n || ldx % 8 != 0 || ldy % step != 0 || ldo % step != 0)
+        return W4A8_ERR_SHAPE;
+    if (y == out && ldy != ldo) return W4A8_ERR_SHAPE;
+    if (tokens == 0) return W4A8_OK;
+    const void *needed[] = {x, a, b, ids, y, out, workspace};
+    for (const void *p : needed)
+        if (!p) return W4A8_ERR_NULL;
+    for (const void *p : needed)
+        if (!aligned16(p)) return W4A8_ERR_MISALIGNED;
+    if (!aligned16(scale)) return W4A8_ERR_MISALIGNED;
+    if (ws_bytes < w4a8::lora_workspace_bytes(tokens, adapters, rank, k)) return W4A8_ERR_SHAPE;
+    if (debug_sync_enabled()) {
+        st = debug_check_inputs(stream, {{a, (size_t)adapters * rank * k, true},
+                                         {b, (size_t)adapters * rank * n, true},
+                                         {scale, (size_t)adapters, false}});
+        for (int64_t t = 0; t < tokens && st == W4A8_OK; ++t)
+            st = debug_check_inputs(
+                stream, {{x + t * ldx, (size_t)k, true},
+                         {(const uint8_t *)y + t * ldy * (dtype == W4A8_BF16 ? 2 : 4), (size_t)n,
+                          dtype == W4A8_BF16}});
+        if (st != W4A8_OK) return st;
+    }
+    return finish(w4a8::launch_lora_add(x, ldx, a, b, ids, scale, tokens, adapters, rank, k, n, y,
+                                        ldy, out, ldo, dtype == W4A8_BF16, workspace, stream),
+                  stream);
 }
 
 }  // extern "C"

@@ -122,6 +122,17 @@ __device__ __forceinline__ void act_scale_pair(float amax, float &s, float &inv)
     inv = (amax > 0.0f) ? (127.0f / amax) : 0.0f;
 }
 
+// The same pair as an array program rounds it, where a scalar over an array and an
+// array over a scalar are products with a rounded reciprocal: inv = 127 * (1 /
+// amax), s = amax * (1 / 127).  A code differs from the pair's above only where
+// x * inv lands within an ulp of a half, which bf16 rows do often enough (x =
+// amax / 2 is exactly 63.5) to matter to a layer that is compared code by code
+// with its array form.
+__device__ __forceinline__ void act_scale_pair_rcp(float amax, float &s, float &inv) {
+    s = amax * (1.0f / 127.0f);
+    inv = (amax > 0.0f) ? 127.0f * (1.0f / amax) : 0.0f;
+}
+
 // Maximum of a non-negative 32-bit value over the 64 lanes of a wavefront with
 // DPP row operations (quad swaps, half-row and row mirrors, then row broadcasts
 // into rows 1-3); lane 63 ends with the total, which is returned to all lanes.
@@ -223,6 +234,11 @@ __device__ __forceinline__ uint32_t buffer_load4(__amdgpu_buffer_rsrc_t r, int v
 __device__ __forceinline__ void buffer_to_lds16(__amdgpu_buffer_rsrc_t r, void *lds_block,
                                                 int voff, int soff) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_vptr)lds_block, 16, voff, soff, 0, 0);
+}
+// 4 bytes per lane straight into LDS at lds_block + 4 * lane (m0 = lds_block).
+__device__ __forceinline__ void buffer_to_lds4(__amdgpu_buffer_rsrc_t r, void *lds_block,
+                                               int voff, int soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_vptr)lds_block, 4, voff, soff, 0, 0);
 }
 
 // Byte offset of chunk j of n-tile t in the packed weights.

@@ -126,6 +126,35 @@ __device__ __forceinline__ u32x4 buffer_load16_nt(__amdgpu_buffer_rsrc_t r, int 
     return __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 2);
 }
 
+// ------------------------------------------------- rows that choose weights --
+// SEL forms of the kernels below: the weights are a stack of equal matrices
+// ("experts") and the rows, sorted by expert, come in tiles of at most one row
+// block, each of one expert (the tile table: expert, first sorted row, rows; 0
+// rows: an unused entry).  The weight pointers move to the tile's expert and m
+// becomes the tile's last row, so the K loops are those of the plain product.
+//   kSelGateUp  the rows of A are gathered (sorted row i reads row src[i]) and
+//               the matrices hold 2 `inter` channels, first the gate's, then
+//               the up projection's; a workgroup's even 16-channel tiles are
+//               gate tiles, its odd ones the up tiles of the same channels, so
+//               both products of an output meet in one lane and it stores
+//               bf16(silu(gate) * up) to sorted row i of [rows, inter].
+//   kSelScatter the rows of A are the sorted rows; sorted row i is stored to
+//               row dst[i].
+enum Sel : int { kSelNone = 0, kSelGateUp = 1, kSelScatter = 2 };
+struct SelArgs {
+    const int4 *tiles;       // [slots] {expert, first sorted row, rows, 0}
+    const int32_t *map;      // src (kSelGateUp) or dst (kSelScatter) of a sorted row
+    uint32_t a_bytes;        // bytes of A (kSelGateUp: gathered through 32-bit offsets)
+    int32_t slots;
+    int64_t inter;
+};
+
+// silu(g) * u in binary32, every step rounded on its own.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+    const float d = 1.0f + expf(-g);
+    return (g / d) * u;
+}
+
 // ---------------------------------------------------------------- skinny --
 constexpr int kSkinnyMaxVec = 8;    // fused prologue: 16-byte vectors held per thread
 // Row vectors (8 activations each) per thread of the fused prologue with
@@ -181,18 +210,37 @@ struct WeightBatch {
 // KF: the fused prologue keeps the widened activations in registers between its
 // maximum and its codes (fewer VALU instructions, more registers: used when one
 // workgroup per CU is all the grid has, so occupancy does not matter).
+// SEL: rows that choose weights (see above; non-fused, per-token scales only):
+// workgroup (x, y) takes tile y of the table.
 template <int WF, int MT, int NT, int WAVES, int D, bool FUSED, int AV, int AB = 0,
-          bool KF = false>
+          bool KF = false, int SEL = kSelNone>
 __global__ __launch_bounds__(64 * WAVES) void gemm_skinny_kernel(
     const void *__restrict__ act, const float *__restrict__ a_scale,
     const uint8_t *__restrict__ w_packed, const uint8_t *__restrict__ grp_scale,
     const float *__restrict__ ch_scale, int m, int64_t n, int64_t k,
     void *__restrict__ out, int out_dtype, int8_t *__restrict__ ws_q,
-    float *__restrict__ ws_s, int64_t first_wave) {
+    float *__restrict__ ws_s, int64_t first_wave, SelArgs sel) {
     constexpr int THREADS = 64 * WAVES;
     constexpr int ROWS = MT * 16;
     extern __shared__ __attribute__((aligned(16))) uint8_t act_lds[];  // FUSED: [m][k + 16]
     static_assert(AB == 0 || !FUSED, "per-block scales only in the non-fused form");
+    static_assert(SEL == kSelNone || (!FUSED && AB == 0), "rows that choose weights");
+    static_assert(SEL != kSelGateUp || NT == 2, "a gate tile and its up tile");
+    int first_row = 0;                       // the tile's first sorted row
+    if constexpr (SEL != kSelNone) {
+        const int4 tile = sel.tiles[blockIdx.y];
+        if (tile.z == 0) return;
+        first_row = tile.y;
+        m = tile.z;
+        w_packed += (int64_t)tile.x * (n * k / 2);
+        grp_scale += (int64_t)tile.x * (n * (k / kGroup)) * (WF == kW4Lqq ? 2 : 1);
+        ch_scale += (int64_t)tile.x * n;
+        sel.map += first_row;
+        if constexpr (SEL == kSelScatter) {
+            act = (const int8_t *)act + (int64_t)first_row * k;
+            a_scale += first_row;
+        }
+    }
     __shared__ int red[AB ? 1 : NT][16][AB ? 1 : ROWS + 4];
     __shared__ float redf[AB ? WAVES : 1][AB ? NT : 1][16][AB ? ROWS + 1 : 1];
     __shared__ float sa_lds[ROWS];
@@ -204,7 +252,9 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_skinny_kernel(
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int c = lane & 15, kq = lane >> 4;
     const int64_t ntiles = n / kNTile;
-    const int64_t t0 = (int64_t)blockIdx.x * NT;
+    const int64_t t0 = (int64_t)blockIdx.x * (SEL == kSelGateUp ? 1 : NT);
+    // tiles from one of this workgroup's to the next
+    const int tstep = SEL == kSelGateUp ? (int)(sel.inter / kNTile) : 1;
     // k <= K_MAX: the K-derived counts fit 32 bits (shorter scalar code ahead
     // of the first loads: 150 -> 123 instructions before the decode kernel's
     // last prologue request, decode 6.52 -> 6.46 us, 4 x 4096 x 4096 5.67 ->
@@ -245,19 +295,24 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_skinny_kernel(
     constexpr int kPSize = WF == kW4Lqq ? 2 : 1;                 // bytes per group parameter
     const int wtile = kWTileMul * (int)k;
     const int ptile = kNTile * (int)G * kPSize;
-    const int tiles_here = (int)(ntiles - t0 < NT ? ntiles - t0 : NT);
+    const int tiles_here = (int)(SEL == kSelGateUp ? tstep + 1
+                                                   : ntiles - t0 < NT ? ntiles - t0 : NT);
+    const int wstep = tstep * wtile, pstep = tstep * ptile;
     const __amdgpu_buffer_rsrc_t rw =
         buffer_rsrc(w_packed + t0 * (int64_t)wtile, (uint32_t)tiles_here * wtile);
     const __amdgpu_buffer_rsrc_t rp =
         WF == kW8 ? rw : buffer_rsrc(grp_scale + t0 * (int64_t)ptile, (uint32_t)tiles_here * ptile);
-    const __amdgpu_buffer_rsrc_t ra = buffer_rsrc(act, FUSED ? (uint32_t)(m * k32 * 2) : (uint32_t)(m * k));
+    const __amdgpu_buffer_rsrc_t ra =
+        buffer_rsrc(act, SEL == kSelGateUp ? sel.a_bytes
+                                           : FUSED ? (uint32_t)(m * k32 * 2) : (uint32_t)(m * k));
     const WParamSel psel = wparam_selectors<WF>(c);
     const int poff_c = WF == kW4Lqq ? (c & ~1) * 2 : (c & ~3);
     int aoff[FUSED ? 1 : MT];                    // activation row offsets (rows past m: row m - 1)
 #pragma unroll
     for (int mt = 0; mt < (FUSED ? 1 : MT); ++mt) {
         const int row = (mt * 16 + c < m) ? mt * 16 + c : m - 1;
-        aoff[mt] = row * (int)k + kq * 16;
+        if constexpr (SEL == kSelGateUp) aoff[mt] = sel.map[row] * k32 + kq * 16;
+        else aoff[mt] = row * (int)k + kq * 16;
     }
 
     // Weights (+ non-fused activation fragments) of D chunks, requested together.
@@ -279,10 +334,10 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_skinny_kernel(
                                                   j * (2 * kChunkBytes) + kChunkBytes);
                     b.s[d][nt][0] = b.s[d][nt][1] = 0u;
                 } else {
-                    b.w[d][nt].r = buffer_load16_nt(rw, nt * wtile + lane * 16, j * kChunkBytes);
+                    b.w[d][nt].r = buffer_load16_nt(rw, nt * wstep + lane * 16, j * kChunkBytes);
                     const int so = j * (2 * kNTile * kPSize);
-                    b.s[d][nt][0] = buffer_load4(rp, nt * ptile + poff_c, so);
-                    b.s[d][nt][1] = buffer_load4(rp, nt * ptile + poff_c, so + kNTile * kPSize);
+                    b.s[d][nt][0] = buffer_load4(rp, nt * pstep + poff_c, so);
+                    b.s[d][nt][1] = buffer_load4(rp, nt * pstep + poff_c, so + kNTile * kPSize);
                 }
             }
             if constexpr (!FUSED) {
@@ -532,10 +587,11 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_skinny_kernel(
         uint32_t sv[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int64_t t = (t0 + nt < ntiles) ? t0 + nt : tlast;
+            const int64_t tt = t0 + nt * (int64_t)tstep;
+            const int64_t t = (tt < ntiles) ? tt : tlast;
             wp[nt] = load_wrec_half<WF>(w_packed, t, j, k, lane);
             sv[nt] = WF == kW8 ? 0u
-                               : buffer_load4(rp, nt * ptile + poff_c,
+                               : buffer_load4(rp, nt * pstep + poff_c,
                                               (int)(2 * j) * kNTile * kPSize);
         }
         v4i av[MT];
@@ -546,7 +602,10 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_skinny_kernel(
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 const int row = (mt * 16 + c < m) ? mt * 16 + c : m - 1;
-                av[mt] = *(const v4i *)(a_q + (int64_t)row * k + kk);
+                if constexpr (SEL == kSelGateUp)
+                    av[mt] = __builtin_bit_cast(v4i, buffer_load16(ra, aoff[mt], (int)j * kChunkK));
+                else
+                    av[mt] = *(const v4i *)(a_q + (int64_t)row * k + kk);
             }
         }
         SaStep sa_half = {};
@@ -595,6 +654,25 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_skinny_kernel(
 #pragma unroll
             for (int i = 0; i < 4; ++i) atomicAdd(&red[nt][4 * kq + i][mt * 16 + c], acc[nt][mt][i]);
     __syncthreads();
+    if constexpr (SEL == kSelGateUp) {
+        for (int idx = tid; idx < m * 4; idx += THREADS) {
+            const int row = idx >> 2, quad = idx & 3;
+            const int64_t nn = t0 * kNTile + 4 * quad;
+            const float sa = a_scale[sel.map[row]];
+            const f32x4 sg = *(const f32x4 *)(ch_scale + nn);
+            const f32x4 su = *(const f32x4 *)(ch_scale + sel.inter + nn);
+            float y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float g = (float)red[0][4 * quad + i][row] * sa * sg[i];
+                const float u = (float)red[1][4 * quad + i][row] * sa * su[i];
+                y[i] = silu_mul(g, u);
+            }
+            *(u32x2 *)((uint16_t *)out + (first_row + row) * sel.inter + nn) =
+                u32x2{bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3])};
+        }
+        return;
+    }
     for (int idx = tid; idx < NT * m * 4; idx += THREADS) {
         const int nt = idx / (m * 4);
         const int rem = idx - nt * m * 4;
@@ -605,7 +683,8 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_skinny_kernel(
                         red[nt][4 * quad + 2][row], red[nt][4 * quad + 3][row]};
         const int64_t nn = t * kNTile + 4 * quad;
         const float sa = FUSED ? sa_lds[row] : a_scale[row];
-        store4(out, out_dtype, row, n, nn, a4, sa, *(const f32x4 *)(ch_scale + nn));
+        const int64_t orow = SEL == kSelScatter ? sel.map[row] : row;
+        store4(out, out_dtype, orow, n, nn, a4, sa, *(const f32x4 *)(ch_scale + nn));
     }
 }
 
@@ -649,12 +728,15 @@ __device__ __forceinline__ int act_lds_off(int row, int c16) {
 // [gridDim.y][m][ldo]; one slice (kslice >= k) is the whole product.  Per-token
 // scales only when split.  first_wave: workgroups the device starts before the
 // rest (one per CU); with two per CU the later one of each pair is second.
-template <int WF, int BM, int BN, int WAVES_M, int WAVES_N, int AB = 0>
+// SEL: rows that choose weights (see above): the row tiles are the entries of
+// the tile table; per-token scales, K not split.
+template <int WF, int BM, int BN, int WAVES_M, int WAVES_N, int AB = 0, int SEL = kSelNone>
 __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, AB == 64 || AB == 128 ? 2 : 1) void gemm_tiled_kernel(
     const int8_t *__restrict__ a_q, const float *__restrict__ a_scale,
     const uint8_t *__restrict__ w_packed, const uint8_t *__restrict__ grp_scale,
     const float *__restrict__ ch_scale, int64_t m, int64_t n, int64_t k,
-    void *__restrict__ out, int64_t ldo, int out_dtype, int64_t kslice, int64_t first_wave) {
+    void *__restrict__ out, int64_t ldo, int out_dtype, int64_t kslice, int64_t first_wave,
+    SelArgs sel) {
     using L = TiledLds<BM, BN>;
     constexpr int WAVES = WAVES_M * WAVES_N;
     constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
@@ -700,7 +782,8 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, AB == 64 || AB == 128 ? 2 :
     // Tile order: consecutive workgroup ids go round-robin over the 8 XCDs, so
     // each XCD gets a contiguous slice of a grouped traversal (4 row tiles per
     // group) and the workgroups sharing an L2 share activation rows and weights.
-    const int64_t mtiles = (m + BM - 1) / BM;
+    static_assert(SEL == kSelNone || AB == 0, "rows that choose weights: per-token scales");
+    const int64_t mtiles = SEL != kSelNone ? sel.slots : (m + BM - 1) / BM;
     const int64_t ntb = (n + BN - 1) / BN;
     const int64_t nwg = mtiles * ntb;
     int64_t id = blockIdx.x;
@@ -710,10 +793,21 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, AB == 64 || AB == 128 ? 2 :
     const int64_t first_m = group * GM;
     const int64_t gsize = (mtiles - first_m < GM) ? (mtiles - first_m) : GM;
     const int64_t within = id - group * GM * ntb;
-    const int64_t m0 = (first_m + within % gsize) * BM;
+    int64_t m0 = (first_m + within % gsize) * BM;
     const int64_t n0 = (within / gsize) * BN;
-    const int64_t t0 = n0 / kNTile;
+    // kSelGateUp: n0 counts the workgroup's BN channels of both products, the
+    // output columns are half of them
+    const int64_t t0 = n0 / kNTile / (SEL == kSelGateUp ? 2 : 1);
     const int64_t ntiles = n / kNTile;
+    if constexpr (SEL != kSelNone) {
+        const int4 tile = sel.tiles[first_m + within % gsize];
+        if (tile.z == 0) return;
+        m0 = tile.y;
+        m = m0 + tile.z;
+        w_packed += (int64_t)tile.x * (n * k / 2);
+        grp_scale += (int64_t)tile.x * (n * (k / kGroup)) * (WF == kW4Lqq ? 2 : 1);
+        ch_scale += (int64_t)tile.x * n;
+    }
 
     // This workgroup's K slice: the operand pointers move to its first chunk
     // (strides stay those of the whole K), its partials to slice blockIdx.y.
@@ -721,7 +815,8 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, AB == 64 || AB == 128 ? 2 :
     a_q += k0;
     w_packed += (k0 / kChunkK) * (WF == kW8 ? 2 * kChunkBytes : kChunkBytes);
     if (WF != kW8) grp_scale += (k0 / kGroup) * kNTile * (WF == kW4Lqq ? 2 : 1);
-    out = (uint8_t *)out + (int64_t)blockIdx.y * m * ldo * (out_dtype == 1 ? 2 : 4);
+    if constexpr (SEL == kSelNone)
+        out = (uint8_t *)out + (int64_t)blockIdx.y * m * ldo * (out_dtype == 1 ? 2 : 4);
     // K in whole 128-wide chunks plus at most one trailing 64-wide chunk (only
     // in the last slice).  All indices and offsets below fit 32 bits: k <=
     // K_MAX, and one workgroup reads at most BM k activation bytes and 16 BN k
@@ -742,10 +837,14 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, AB == 64 || AB == 128 ? 2 :
     constexpr int kWTileMul = WF == kW8 ? 16 : 8;                // weight bytes per tile = mul * k
     constexpr int kPSize = WF == kW4Lqq ? 2 : 1;                 // bytes per group parameter
     const int rows_here = (int)(m - m0 < BM ? m - m0 : BM);
-    const int tiles_here = (int)(ntiles - t0 < NTB ? ntiles - t0 : NTB);
+    // kSelGateUp: up to the last up tile (the host keeps n k / 2 below 2^32)
+    const int tiles_here =
+        (int)(SEL == kSelGateUp || ntiles - t0 < NTB ? ntiles - t0 : NTB);
     const int wtile = kWTileMul * kfull;
     const int ptile = kNTile * gk * kPSize;
-    const __amdgpu_buffer_rsrc_t ra = buffer_rsrc(a_q + m0 * k, (uint32_t)rows_here * kfull);
+    const __amdgpu_buffer_rsrc_t ra =
+        SEL == kSelGateUp ? buffer_rsrc(a_q, sel.a_bytes)
+                          : buffer_rsrc(a_q + m0 * k, (uint32_t)rows_here * kfull);
     const __amdgpu_buffer_rsrc_t rw =
         buffer_rsrc(w_packed + t0 * (int64_t)wtile, (uint32_t)tiles_here * wtile);
     const __amdgpu_buffer_rsrc_t rp =
@@ -759,7 +858,24 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, AB == 64 || AB == 128 ? 2 :
     // that issue them, so every wait below covers them.
     if constexpr (kSclLds) {
         static_assert(WAVES >= kSclA + kSclC, "one scale block per wavefront");
-        if (wave < kSclA) {
+        if constexpr (SEL == kSelGateUp) {
+            // row scales gathered, four bytes a lane; channel scales: the gate's
+            // BN / 2, then the up projection's (past the end: zero, not stored)
+            static_assert(BM % 64 == 0 && BM / 64 < WAVES && BN <= 256, "scale blocks");
+            if (wave < BM / 64) {
+                const int r = wave * 64 + lane;
+                const int64_t row = m0 + (r < rows_here ? r : rows_here - 1);
+                const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(a_scale, 0xffffffffu);
+                buffer_to_lds4(rs, scl_a + wave * 256, sel.map[row] * 4, 0);
+            } else if (wave == BM / 64) {
+                const int64_t h0 = t0 * kNTile;
+                const __amdgpu_buffer_rsrc_t rs =
+                    buffer_rsrc(ch_scale + h0, (uint32_t)(2 * sel.inter - h0) * 4);
+                const int cg = lane * 4;            // of BN: gate, then up
+                buffer_to_lds16(rs, scl_c,
+                                (cg < BN / 2 ? cg : (int)sel.inter + cg - BN / 2) * 4, 0);
+            }
+        } else if (wave < kSclA) {
             const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(a_scale + m0, (uint32_t)rows_here * 4);
             buffer_to_lds16(rs, scl_a + wave * 1024, wave * 1024 + lane * 16, 0);
         } else if (wave < kSclA + kSclC) {
@@ -778,7 +894,11 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, AB == 64 || AB == 128 ? 2 :
 #pragma unroll
     for (int i = 0; i < ACT_I; ++i) {
         const int row = (i * WAVES + wave) * 8 + (lane >> 3);
-        aoff[i] = row * kfull + (act_swz(row, lane & 7) << 4);
+        if constexpr (SEL == kSelGateUp)        // rows past the tile's: its last one
+            aoff[i] = sel.map[m0 + (row < rows_here ? row : rows_here - 1)] * kfull +
+                      (act_swz(row, lane & 7) << 4);
+        else
+            aoff[i] = row * kfull + (act_swz(row, lane & 7) << 4);
     }
     // Stage and register-set selection by a compile-time tag (0, 1 or 2).
     auto act_of = [&](auto st) -> uint8_t * {
@@ -812,7 +932,9 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, AB == 64 || AB == 128 ? 2 :
     int woff[TPW], woff_half[TPW], poff[TPW];
 #pragma unroll
     for (int i = 0; i < TPW; ++i) {
-        const int tr = wave * TPW + i;
+        int tr = wave * TPW + i;
+        // even tiles: gate, odd ones: the up tile of the same channels
+        if constexpr (SEL == kSelGateUp) tr = (tr >> 1) + (tr & 1) * (int)(sel.inter / kNTile);
         woff[i] = tr * wtile + lane * 16;
         woff_half[i] = tr * wtile + (lane * 8 < 496 ? lane * 8 : 496);
         poff[i] = tr * ptile + (WF == kW4Lqq ? (c & ~1) * 2 : (c & ~3));
@@ -1164,9 +1286,11 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, AB == 64 || AB == 128 ? 2 :
     {
         constexpr int PER_ARRAY = WAVES / 4;
         static_assert(WAVES % 4 == 0, "four stage arrays share the epilogue");
-        const int esize = (out_dtype == 1) ? 2 : 4;
+        // kSelGateUp: bf16, half as many output columns
+        constexpr int WNO = SEL == kSelGateUp ? WN / 2 : WN;
+        const int esize = (SEL == kSelGateUp || out_dtype == 1) ? 2 : 4;
         const int rows_pass = (esize == 2) ? WM : WM / 2;
-        const int row_bytes = WN * esize;
+        const int row_bytes = WNO * esize;
         const int segs = row_bytes / 16;                 // 16-byte segments per row
         // kRegW: the weight stages held no operands; half the wavefronts use each
         constexpr int PER_W = WAVES / 2;
@@ -1188,7 +1312,9 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, AB == 64 || AB == 128 ? 2 :
         f32x4 scv[TN];
 #pragma unroll
         for (int tn = 0; tn < TN; ++tn) {
-            const int col = wn * WN + tn * 16 + 4 * kq;
+            const int col = SEL == kSelGateUp
+                                ? (tn & 1) * (BN / 2) + wn * WNO + (tn >> 1) * 16 + 4 * kq
+                                : wn * WN + tn * 16 + 4 * kq;
             if constexpr (kSclLds) {
                 scv[tn] = *(const f32x4 *)(scl_c + col * 4);
             } else {
@@ -1204,6 +1330,21 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, AB == 64 || AB == 128 ? 2 :
                 if (r < 0 || r >= rows_pass) continue;
                 const float sa =
                     AB ? 1.0f : *(const float *)(scl_a + (wm * WM + tm * 16 + c) * 4);
+                if constexpr (SEL == kSelGateUp) {
+#pragma unroll
+                    for (int tp = 0; tp < TN / 2; ++tp) {
+                        const int byte = (tp * 16 + 4 * kq) * 2;
+                        const v4i ag = acc[2 * tp][tm], au = acc[2 * tp + 1][tm];
+                        float y[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            y[i] = silu_mul((float)ag[i] * sa * scv[2 * tp][i],
+                                            (float)au[i] * sa * scv[2 * tp + 1][i]);
+                        *(u32x2 *)(ebuf + seg_off(r, byte >> 4) + (byte & 15)) =
+                            u32x2{bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3])};
+                    }
+                    continue;
+                }
 #pragma unroll
                 for (int tn = 0; tn < TN; ++tn) {
                     const int col = tn * 16 + 4 * kq;             // within the wavefront tile
@@ -1241,10 +1382,13 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, AB == 64 || AB == 128 ? 2 :
                 const int r = r0 + lane / lanes_per_row;
                 const int seg = lane % lanes_per_row;
                 const int64_t row = m0 + wm * WM + pass * rows_pass + r;
-                const int64_t nn = n0 + wn * WN + (seg * 16) / esize;
+                const int64_t nn =
+                    (SEL == kSelGateUp ? t0 * kNTile : n0) + wn * WNO + (seg * 16) / esize;
                 const u32x4 v = *(const u32x4 *)(ebuf + seg_off(r, seg));
-                if (row < m && nn < n)
-                    *(u32x4 *)((uint8_t *)out + (row * ldo + nn) * esize) = v;
+                if (row < m && nn < (SEL == kSelGateUp ? sel.inter : n)) {
+                    const int64_t orow = SEL == kSelScatter ? sel.map[row] : row;
+                    *(u32x4 *)((uint8_t *)out + (orow * ldo + nn) * esize) = v;
+                }
             }
             asm volatile("" ::: "memory");
         }
@@ -1269,7 +1413,7 @@ void launch_skinny(const void *act, const float *a_scale, const uint8_t *w_packe
     gemm_skinny_kernel<WF, MT, NT, WAVES, D, FUSED, AV, AB, KF><<<grid, 64 * WAVES, dyn_lds,
                                                             stream>>>(
         act, a_scale, w_packed, grp_scale, ch_scale, (int)m, n, k, out, out_dtype, ws_q, ws_s,
-        (int64_t)device_cu_count());
+        (int64_t)device_cu_count(), SelArgs{});
 }
 
 // Output columns [n_off, n_off + n_sub) of an [m, ldo] product: the weight
@@ -1293,7 +1437,8 @@ void launch_tiled_cols(const int8_t *a_q, const float *a_scale, const uint8_t *w
                                                           64 * WAVES_M * WAVES_N, 0, stream>>>(
         a_q, a_scale, w_packed + t_off * wtile,
         grp_scale ? grp_scale + t_off * ptile : grp_scale, ch_scale + n_off, m, n_sub, k,
-        (uint8_t *)out + n_off * esize, ldo, out_dtype, kslice, (int64_t)device_cu_count());
+        (uint8_t *)out + n_off * esize, ldo, out_dtype, kslice, (int64_t)device_cu_count(),
+        SelArgs{});
 }
 
 // ------------------------------------------------------------- split K --

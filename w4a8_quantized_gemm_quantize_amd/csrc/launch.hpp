@@ -12,6 +12,9 @@ int device_cu_count();
 
 hipError_t launch_quantize_act(const uint16_t *x, int64_t rows, int64_t cols, int32_t block,
                                int8_t *q, float *scales, hipStream_t stream);
+// Per-row form with act_scale_pair_rcp (device_common.hpp), cols % 8 == 0.
+hipError_t launch_quantize_rows(const uint16_t *x, int64_t rows, int64_t cols, int8_t *q,
+                                float *scales, hipStream_t stream);
 hipError_t launch_dequantize_act(const int8_t *q, const float *scales, int64_t rows,
                                  int64_t cols, int32_t block, void *out, bool bf16,
                                  hipStream_t stream);
@@ -84,5 +87,37 @@ hipError_t launch_dequant_add_requant(const int8_t *q_in, const float *s_in, con
 // int8 matrix-core reference loop (measurement aid).
 hipError_t launch_mfma_probe(int64_t workgroups, int32_t iters, int32_t *sink, uint64_t *clocks,
                              hipStream_t stream);
+
+// Routing (route.hip), arguments as moe_route in w4a8.h.
+hipError_t launch_route(const void *logits, bool bf16, int64_t ld, const float *bias,
+                        int64_t tokens, int32_t experts, int32_t top_k, bool sigmoid,
+                        int32_t groups, int32_t topk_groups, int32_t group_top, bool renorm,
+                        float scale, int32_t *ids, float *weights, hipStream_t stream);
+
+// Rows sorted by the group they choose, in tiles of bm rows (plan.hip): order
+// [rows] the row of each sorted position, src (may be null) order / top_k,
+// tiles [plan_slots] x 4 int32 {group, first sorted row, rows, 0}.
+constexpr int kPlanMaxGroups = 4096;
+int64_t plan_slots(int64_t rows, int64_t groups, int bm);
+hipError_t launch_plan(const int32_t *ids, int64_t rows, int32_t groups, bool none_last,
+                       int32_t top_k, int bm, int32_t *order, int32_t *src, int32_t *tiles,
+                       hipStream_t stream);
+
+// Experts' products (experts.hip), arguments as w4a8_moe_ffn in w4a8.h.
+size_t moe_workspace_bytes(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden,
+                           int64_t inter, int out_dtype);
+hipError_t launch_moe_ffn(const uint16_t *x, const int32_t *ids, const float *weights,
+                          const uint8_t *w13, const uint8_t *g13, const float *c13,
+                          const uint8_t *w2, const uint8_t *g2, const float *c2, int64_t tokens,
+                          int32_t experts, int32_t top_k, int64_t hidden, int64_t inter,
+                          void *out, int out_dtype, void *workspace, hipStream_t stream);
+
+// Low-rank adapters (lora.hip), arguments as w4a8_lora_add in w4a8.h.
+size_t lora_workspace_bytes(int64_t tokens, int64_t adapters, int64_t rank, int64_t k);
+hipError_t launch_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, const uint16_t *b,
+                           const int32_t *ids, const float *scale, int64_t tokens,
+                           int32_t adapters, int32_t rank, int64_t k, int64_t n, const void *y,
+                           int64_t ldy, void *out, int64_t ldo, bool bf16, void *workspace,
+                           hipStream_t stream);
 
 }  // namespace w4a8

@@ -1,0 +1,412 @@
+// lora.hip -- low-rank adapters of many requests beside a shared projection
+// (w4a8_lora_add in w4a8.h): out[t] = y[t] + scale[l] B[l] (A[l] x[t]), l = ids[t].
+//
+// Two launches.  Both walk row tiles, up to BM rows that share an adapter, so an
+// adapter's A and B are read once per tile however the requests are mixed:
+//   shrink  v = A x over one of `slices` parts of K: the four wavefronts split
+//           the part, each holding the tile's whole v in accumulators, and add up
+//           in LDS; the part's v goes to the workspace in binary32.
+//   expand  sums the parts (in order), folds the adapter's scale in, and
+//           multiplies by B on the matrix cores with y added in the epilogue.
+// v stays binary32 throughout: the matrix cores take bf16, so expand splits it
+// into bf16 terms (v = hi + lo, error 2^-16, for bf16 outputs; three terms, exact
+// to 2^-24, for binary32 outputs) and multiplies each by the same B operand.
+//
+// v_mfma_f32_16x16x32_bf16: lane (r = l % 16, q = l / 16) supplies row r of the
+// first operand and column r of the second, both at k = 8 q .. 8 q + 7 (16
+// bytes), and receives elements (4 q + i, r) of the result.  A rows, x rows
+// and B rows are contiguous along that k, so every operand is one 16-byte load
+// straight from memory.
+//
+// Row tiles come from the plan (plan.hip; rows without an adapter are a group of
+// their own, copied from y), or, for up to 64 rows, from one ballot: row t
+// leads the tile of the 16 rows of its adapter that start with it.
+#include "device_common.hpp"
+#include "launch.hpp"
+
+namespace w4a8 {
+namespace {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+struct LoraArgs {
+    const uint16_t *x, *a, *b;
+    const int32_t *ids;
+    const float *scale;
+    const void *y;
+    void *out;
+    float *part;              // [slices][slots][BM][RP]
+    const int4 *tiles;        // plan form only
+    const int32_t *order;
+    int64_t ldx, ldy, ldo, k, n;
+    int tokens, adapters, rank, slots, slices, kslice;
+};
+
+constexpr int kLoraWaves = 4;
+
+// The rows of tile `slot`: their indices into `rows` (LDS, padded with the last
+// one), their count and adapter (>= adapters: none).  False: no rows.
+template <int BM, bool PLAN>
+__device__ __forceinline__ bool tile_rows(const LoraArgs &p, int slot, int *rows, int &count,
+                                          int &adapter) {
+    const int tid = threadIdx.x;
+    if constexpr (PLAN) {
+        const int4 t = p.tiles[slot];
+        count = t.z;
+        adapter = t.x;
+        if (count == 0) return false;
+        if (tid < BM) rows[tid] = p.order[t.y + (tid < count ? tid : count - 1)];
+    } else {
+        static_assert(BM == 16, "one ballot");
+        const int lane = tid & 63;
+        const int id = lane < p.tokens ? p.ids[lane] : -2;
+        const int norm = lane < p.tokens ? (id >= 0 && id < p.adapters ? id : p.adapters) : -1;
+        adapter = __builtin_amdgcn_readlane(norm, slot);
+        const uint64_t same = __ballot(norm == adapter);
+        const int before = __popcll(same & ((1ull << slot) - 1));
+        if (before & 15) return false;                  // in an earlier row's tile
+        const int after = __popcll(same) - before;
+        count = after < 16 ? after : 16;
+        if (tid < 64) {
+            const int rank = __popcll(same & ((1ull << lane) - 1)) - before;
+            if (norm == adapter && rank >= 0 && rank < 16) {
+                rows[rank] = lane;
+                if (rank == count - 1)
+                    for (int i = count; i < BM; ++i) rows[i] = lane;
+            }
+        }
+    }
+    __syncthreads();
+    return true;
+}
+
+// ----------------------------------------------------------------- shrink --
+template <int RT, int MT, bool PLAN>
+__global__ __launch_bounds__(64 * kLoraWaves) void lora_shrink_kernel(LoraArgs p) {
+    constexpr int BM = 16 * MT, RP = 16 * RT;
+    constexpr int U = RT + MT <= 2 ? 8 : RT + MT <= 5 ? 4 : RT + MT <= 8 ? 3 : 2;
+    __shared__ int rows[BM];
+    __shared__ f32x4 red[kLoraWaves][RT][64];
+    int count, adapter;
+    if (!tile_rows<BM, PLAN>(p, blockIdx.x, rows, count, adapter)) return;
+    if (adapter >= p.adapters) return;
+    const int tid = threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const int r = lane & 15, q = lane >> 4;
+
+    const uint16_t *arow[RT], *xrow[MT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        const int ar = 16 * i + r < p.rank ? 16 * i + r : p.rank - 1;   // past rank: not used
+        arow[i] = p.a + ((int64_t)adapter * p.rank + ar) * p.k + 8 * q;
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) xrow[i] = p.x + (int64_t)rows[16 * i + r] * p.ldx + 8 * q;
+
+    f32x4 acc[RT][MT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    // this wavefront's part of the slice, in steps of 32
+    const int64_t s0 = (int64_t)blockIdx.y * p.kslice;
+    const int64_t s1 = s0 + p.kslice < p.k ? s0 + p.kslice : p.k;
+    const int wpart = p.kslice / kLoraWaves;                   // a multiple of 32
+    const int64_t k0 = s0 + (int64_t)wave * wpart;
+    const int64_t kend = k0 + wpart < s1 ? k0 + wpart : s1;
+    int64_t kk = k0;
+    for (; kk + 32 * U <= kend; kk += 32 * U) {
+        u32x4 av[U][RT], xv[U][MT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int i = 0; i < RT; ++i) av[u][i] = *(const u32x4 *)(arow[i] + kk + 32 * u);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) xv[u][i] = *(const u32x4 *)(xrow[i] + kk + 32 * u);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int j = 0; j < MT; ++j)
+                    acc[i][j] = mfma_bf16(av[u][i], xv[u][j], acc[i][j]);
+    }
+    for (; kk < kend; kk += 32) {
+        const bool in = kk + 8 * q < kend;                     // k % 8 == 0: whole vectors
+        const int64_t at = in ? kk : kk - 8 * q;               // a valid place; zeroed below
+        u32x4 av[RT], xv[MT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            av[i] = *(const u32x4 *)(arow[i] + at);
+            av[i] = in ? av[i] : u32x4{0u, 0u, 0u, 0u};
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            xv[i] = *(const u32x4 *)(xrow[i] + at);
+            xv[i] = in ? xv[i] : u32x4{0u, 0u, 0u, 0u};
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int j = 0; j < MT; ++j) acc[i][j] = mfma_bf16(av[i], xv[j], acc[i][j]);
+    }
+
+    // the four wavefronts' sums, in order; lane (t = r, q) holds ranks 16 i + 4 q ..
+    float *part = p.part + ((int64_t)blockIdx.y * p.slots + blockIdx.x) * (BM * RP);
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+        if (j > 0) __syncthreads();
+#pragma unroll
+        for (int i = 0; i < RT; ++i) red[wave][i][lane] = acc[i][j];
+        __syncthreads();
+        for (int i = wave; i < RT; i += kLoraWaves) {
+            f32x4 v = red[0][i][lane];
+#pragma unroll
+            for (int w = 1; w < kLoraWaves; ++w) {
+                const f32x4 o = red[w][i][lane];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = v[e] + o[e];
+            }
+            *(f32x4 *)(part + (16 * j + r) * RP + 16 * i + 4 * q) = v;
+        }
+    }
+}
+
+// ----------------------------------------------------------------- expand --
+// Workgroup: one row tile x 256 columns, 64 per wavefront.  The four 16-row
+// operand tiles of a wavefront take the B rows in the order that gives lane
+// (t, q) the 16 consecutive columns 16 q .. 16 q + 15 of row t: y and out move in
+// 16-byte pieces of whole cache lines.
+constexpr int kExpandN = 64 * kLoraWaves;
+
+template <int RT, int MT, bool PLAN, bool BF16>
+__global__ __launch_bounds__(64 * kLoraWaves) void lora_expand_kernel(LoraArgs p) {
+    constexpr int BM = 16 * MT, RP = 16 * RT;
+    constexpr int RK = (RT + 1) / 2;               // steps of 32 along the rank
+    constexpr int TERMS = BF16 ? 2 : 3;
+    constexpr int VS = 32 * RK + 8;                // LDS row stride (bf16)
+    constexpr int YV = BF16 ? 2 : 4;               // 16-byte pieces of 16 columns
+    constexpr int PER = BF16 ? 8 : 4;              // columns of a piece
+    __shared__ int rows[BM];
+    __shared__ __attribute__((aligned(16))) uint16_t vs[TERMS][BM][VS];
+    int count, adapter;
+    if (!tile_rows<BM, PLAN>(p, blockIdx.x, rows, count, adapter)) return;
+    const bool none = adapter >= p.adapters;
+    if (none && p.y == p.out) return;              // nothing to add or move
+    const int tid = threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const int r = lane & 15, q = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.y * kExpandN + wave * 64;
+    const int64_t col = n0 + 16 * q;               // this lane's first column
+    const int esize = BF16 ? 2 : 4;
+
+    // y of this lane's rows and columns, in flight while v is put together
+    u32x4 yv[MT][YV];
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+        const int64_t base = (int64_t)rows[16 * j + r] * p.ldy;
+#pragma unroll
+        for (int c = 0; c < YV; ++c) {
+            const bool in = 16 * j + r < count && col + c * PER < p.n;
+            yv[j][c] = in ? *(const u32x4 *)((const uint8_t *)p.y + (base + col + c * PER) * esize)
+                          : u32x4{0u, 0u, 0u, 0u};
+        }
+    }
+    u32x4 bv[RK][4];
+    if (!none) {
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            const int64_t row = n0 + (r >> 2) * 16 + f * 4 + (r & 3);
+            const uint16_t *brow =
+                p.b + ((int64_t)adapter * p.n + (row < p.n ? row : p.n - 1)) * p.rank;
+#pragma unroll
+            for (int s = 0; s < RK; ++s) {
+                const int kk = 32 * s + 8 * q;
+                const bool in = kk < p.rank;       // rank % 8 == 0: whole vectors
+                bv[s][f] = *(const u32x4 *)(brow + (in ? kk : 0));
+                bv[s][f] = in ? bv[s][f] : u32x4{0u, 0u, 0u, 0u};
+            }
+        }
+        // v = scale * sum of the parts, in bf16 terms; zero past the rank
+        const float sc = p.scale ? p.scale[adapter] : 1.0f;
+        const int64_t stride = (int64_t)p.slots * (BM * RP);
+        const float *part = p.part + (int64_t)blockIdx.x * (BM * RP);
+        constexpr int VEC = 32 * RK / 4;           // 4-rank pieces of a row
+        for (int i = tid; i < BM * VEC; i += 64 * kLoraWaves) {
+            const int t = i / VEC, c4 = (i - t * VEC) * 4;
+            f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (t < count && c4 < p.rank) {
+                const float *src = part + t * RP + c4;
+                for (int s = 0; s < p.slices; ++s) {
+                    const f32x4 o = *(const f32x4 *)(src + s * stride);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = v[e] + o[e];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = v[e] * sc;
+#pragma unroll
+            for (int m = 0; m < TERMS; ++m) {
+                const u32x2 h = {bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+                *(u32x2 *)&vs[m][t][c4] = h;
+                v[0] = v[0] - __uint_as_float(h.x << 16);
+                v[1] = v[1] - __uint_as_float(h.x & 0xffff0000u);
+                v[2] = v[2] - __uint_as_float(h.y << 16);
+                v[3] = v[3] - __uint_as_float(h.y & 0xffff0000u);
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+        if (16 * j >= count) break;
+        f32x4 acc[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) acc[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (!none) {
+            // smallest terms first
+#pragma unroll
+            for (int m = TERMS - 1; m >= 0; --m)
+#pragma unroll
+                for (int s = 0; s < RK; ++s) {
+                    const u32x4 vt = *(const u32x4 *)&vs[m][16 * j + r][32 * s + 8 * q];
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) acc[f] = mfma_bf16(bv[s][f], vt, acc[f]);
+                }
+        }
+        if (16 * j + r >= count) continue;
+        uint8_t *dst = (uint8_t *)p.out + ((int64_t)rows[16 * j + r] * p.ldo + col) * esize;
+#pragma unroll
+        for (int c = 0; c < YV; ++c) {
+            if (col + c * PER >= p.n) break;
+            u32x4 o = yv[j][c];
+            if (!none) {
+                if constexpr (BF16) {
+                    float f[8];
+                    bf16x8_to_f32(o, f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] = f[e] + acc[2 * c + (e >> 2)][e & 3];
+                    o = u32x4{bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]),
+                              bf16x2_rne(f[4], f[5]), bf16x2_rne(f[6], f[7])};
+                } else {
+                    f32x4 f = __builtin_bit_cast(f32x4, o);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[e] = f[e] + acc[c][e];
+                    o = __builtin_bit_cast(u32x4, f);
+                }
+            }
+            *(u32x4 *)(dst + c * 16) = o;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- launches --
+constexpr int64_t kBallotRows = 64;
+
+struct LoraSpace {
+    bool plan;
+    int bm, rp, slices, kslice;
+    int64_t slots;
+    size_t order, tiles, part, end;
+};
+
+LoraSpace lora_space(int64_t tokens, int64_t adapters, int64_t rank, int64_t k) {
+    LoraSpace s;
+    s.plan = tokens > kBallotRows;
+    s.bm = s.plan ? 64 : 16;
+    s.rp = rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128;
+    s.slots = s.plan ? plan_slots(tokens, adapters + 1, s.bm) : tokens;
+    // about 768 workgroups, each wavefront at least 128 of K
+    int64_t want = 768 / s.slots;
+    const int64_t most = (k + 511) / 512;
+    if (want > most) want = most;
+    if (want > 16) want = 16;
+    if (want < 1) want = 1;
+    const int64_t unit = 32 * kLoraWaves;
+    s.kslice = (int)(((k + want - 1) / want + unit - 1) / unit * unit);
+    s.slices = (int)((k + s.kslice - 1) / s.kslice);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    s.order = take(s.plan ? (size_t)tokens * 4 : 0);
+    s.tiles = take(s.plan ? (size_t)s.slots * 16 : 0);
+    s.part = take((size_t)s.slices * s.slots * s.bm * s.rp * 4);
+    s.end = at;
+    return s;
+}
+
+template <int RT, int MT, bool PLAN>
+void launch_lora_rank(const LoraArgs &p, bool bf16, hipStream_t stream) {
+    const dim3 block(64 * kLoraWaves);
+    lora_shrink_kernel<RT, MT, PLAN>
+        <<<dim3((unsigned)p.slots, (unsigned)p.slices), block, 0, stream>>>(p);
+    const dim3 grid((unsigned)p.slots, (unsigned)((p.n + kExpandN - 1) / kExpandN));
+    if (bf16) lora_expand_kernel<RT, MT, PLAN, true><<<grid, block, 0, stream>>>(p);
+    else lora_expand_kernel<RT, MT, PLAN, false><<<grid, block, 0, stream>>>(p);
+}
+
+template <int MT, bool PLAN>
+void launch_lora_rows(const LoraArgs &p, int rp, bool bf16, hipStream_t stream) {
+    if (rp == 16) launch_lora_rank<1, MT, PLAN>(p, bf16, stream);
+    else if (rp == 32) launch_lora_rank<2, MT, PLAN>(p, bf16, stream);
+    else if (rp == 64) launch_lora_rank<4, MT, PLAN>(p, bf16, stream);
+    else launch_lora_rank<8, MT, PLAN>(p, bf16, stream);
+}
+
+}  // namespace
+
+size_t lora_workspace_bytes(int64_t tokens, int64_t adapters, int64_t rank, int64_t k) {
+    return lora_space(tokens, adapters, rank, k).end;
+}
+
+hipError_t launch_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, const uint16_t *b,
+                           const int32_t *ids, const float *scale, int64_t tokens,
+                           int32_t adapters, int32_t rank, int64_t k, int64_t n, const void *y,
+                           int64_t ldy, void *out, int64_t ldo, bool bf16, void *workspace,
+                           hipStream_t stream) {
+    const LoraSpace s = lora_space(tokens, adapters, rank, k);
+    uint8_t *ws = (uint8_t *)workspace;
+    if (s.plan) {
+        const hipError_t err =
+            launch_plan(ids, tokens, adapters + 1, true, 1, s.bm, (int32_t *)(ws + s.order),
+                        nullptr, (int32_t *)(ws + s.tiles), stream);
+        if (err != hipSuccess) return err;
+    }
+    LoraArgs p;
+    p.x = x;
+    p.a = a;
+    p.b = b;
+    p.ids = ids;
+    p.scale = scale;
+    p.y = y;
+    p.out = out;
+    p.part = (float *)(ws + s.part);
+    p.tiles = (const int4 *)(ws + s.tiles);
+    p.order = (const int32_t *)(ws + s.order);
+    p.ldx = ldx;
+    p.ldy = ldy;
+    p.ldo = ldo;
+    p.k = k;
+    p.n = n;
+    p.tokens = (int)tokens;
+    p.adapters = adapters;
+    p.rank = rank;
+    p.slots = (int)s.slots;
+    p.slices = s.slices;
+    p.kslice = s.kslice;
+    if (s.plan) launch_lora_rows<4, true>(p, s.rp, bf16, stream);
+    else launch_lora_rows<1, false>(p, s.rp, bf16, stream);
+    return hipGetLastError();
+}
+
+}  // namespace w4a8

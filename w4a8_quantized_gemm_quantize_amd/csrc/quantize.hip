@@ -82,12 +82,20 @@ __global__ __launch_bounds__(256) void quant_pow2_kernel(const u32x4 *__restrict
     }
 }
 
+// RCP: the row quantization of the routed experts' products (launch_quantize_rows):
+// scale and inverse from products with rounded reciprocals.
+template <bool RCP>
+__device__ __forceinline__ void scale_pair(float amax, float &s, float &inv) {
+    if constexpr (RCP) act_scale_pair_rcp(amax, s, inv);
+    else act_scale_pair(amax, s, inv);
+}
+
 // Blocks of up to 64 * V vectors (8 elements each), one wavefront per block and
 // four per workgroup: each lane holds V vectors, all requested before any is
 // used (indices past the block are clamped to its last vector and ignored), so
 // a lane has V loads in flight; the block maximum is a wavefront reduction with
 // no barrier.  Per-token rows up to 8192 elements take this path.
-template <int V>
+template <int V, bool RCP = false>
 __global__ __launch_bounds__(256) void quant_row_wave_kernel(const u32x4 *__restrict__ x,
                                                              int64_t nblocks, int block_vecs,
                                                              u32x2 *__restrict__ q,
@@ -112,7 +120,7 @@ __global__ __launch_bounds__(256) void quant_row_wave_kernel(const u32x4 *__rest
         // amax >= 0 and never NaN, so its bits order like unsigned integers
         amax = __uint_as_float(wave_max_u32(__float_as_uint(amax)));
         float s, inv;
-        act_scale_pair(amax, s, inv);
+        scale_pair<RCP>(amax, s, inv);
         u32x2 *qb = q + b * block_vecs;
 #pragma unroll
         for (int u = 0; u < V; ++u) {
@@ -131,7 +139,7 @@ __global__ __launch_bounds__(256) void quant_row_wave_kernel(const u32x4 *__rest
 // 256 * MAXV vectors stay in registers between the two phases, all requested
 // before any is used (clamped indices, as above); a longer block is read a
 // second time (from cache) for phase 2.
-template <int MAXV>
+template <int MAXV, bool RCP = false>
 __global__ __launch_bounds__(256) void quant_wide_kernel(const u32x4 *__restrict__ x,
                                                          int64_t nblocks, int64_t block_vecs,
                                                          u32x2 *__restrict__ q,
@@ -164,7 +172,7 @@ __global__ __launch_bounds__(256) void quant_wide_kernel(const u32x4 *__restrict
         amax = __builtin_fmaxf(__builtin_fmaxf(red[0], red[1]), __builtin_fmaxf(red[2], red[3]));
         __syncthreads();
         float s, inv;
-        act_scale_pair(amax, s, inv);
+        scale_pair<RCP>(amax, s, inv);
 #pragma unroll
         for (int u = 0; u < MAXV; ++u) {
             const int64_t idx = tid + (int64_t)u * 256;
@@ -190,7 +198,7 @@ __global__ __launch_bounds__(256) void quant_wide_kernel(const u32x4 *__restrict
 // per row and takes 3.2 us here; 2048 x 28672: 31.2 -> 29.7 us; 4096 x 16384:
 // 40.6 -> 34.9 us.  The block maximum is a wavefront reduction, then one over
 // the 16 wavefronts in LDS.
-template <int MAXV>
+template <int MAXV, bool RCP = false>
 __global__ __launch_bounds__(1024) void quant_wide1k_kernel(const u32x4 *__restrict__ x,
                                                             int64_t nblocks, int64_t block_vecs,
                                                             u32x2 *__restrict__ q,
@@ -221,7 +229,7 @@ __global__ __launch_bounds__(1024) void quant_wide1k_kernel(const u32x4 *__restr
         for (int i = 1; i < 16; ++i) m = max(m, red[i]);
         __syncthreads();
         float s, inv;
-        act_scale_pair(__uint_as_float(m), s, inv);
+        scale_pair<RCP>(__uint_as_float(m), s, inv);
 #pragma unroll
         for (int u = 0; u < MAXV; ++u) {
             const int64_t idx = tid + (int64_t)u * 1024;
@@ -321,6 +329,36 @@ hipError_t launch_quantize_act(const uint16_t *x, int64_t rows, int64_t cols, in
                                                                 scales);
             }
         }
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_quantize_rows(const uint16_t *x, int64_t rows, int64_t cols, int8_t *q,
+                                float *scales, hipStream_t stream) {
+    const u32x4 *xv = (const u32x4 *)x;
+    u32x2 *qv = (u32x2 *)q;
+    const int64_t vecs = cols / 8;
+    if (rows == 0 || vecs == 0) return hipSuccess;
+    if (vecs <= 64 * 16) {
+        const int64_t wg = (rows + 3) / 4;
+        const int grid = (int)(wg < 65536 ? wg : 65536);
+        const int bv = (int)vecs;
+        if (vecs <= 64)
+            quant_row_wave_kernel<1, true><<<grid, 256, 0, stream>>>(xv, rows, bv, qv, scales);
+        else if (vecs <= 128)
+            quant_row_wave_kernel<2, true><<<grid, 256, 0, stream>>>(xv, rows, bv, qv, scales);
+        else if (vecs <= 256)
+            quant_row_wave_kernel<4, true><<<grid, 256, 0, stream>>>(xv, rows, bv, qv, scales);
+        else if (vecs <= 512)
+            quant_row_wave_kernel<8, true><<<grid, 256, 0, stream>>>(xv, rows, bv, qv, scales);
+        else
+            quant_row_wave_kernel<16, true><<<grid, 256, 0, stream>>>(xv, rows, bv, qv, scales);
+    } else {
+        const int grid = (int)(rows < 65536 ? rows : 65536);
+        if (vecs <= 1024 * 4)
+            quant_wide1k_kernel<4, true><<<grid, 1024, 0, stream>>>(xv, rows, vecs, qv, scales);
+        else
+            quant_wide_kernel<16, true><<<grid, 256, 0, stream>>>(xv, rows, vecs, qv, scales);
     }
     return hipGetLastError();
 }
