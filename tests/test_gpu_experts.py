@@ -136,6 +136,12 @@ CASES = [
     (8, 64, 8, 512, 128),
     (40, 6, 3, 320, 448),
     (33, 200, 2, 128, 320),
+    (1, 9, 3, 1088, 192),           # few rows: taken one by one
+    (2, 64, 8, 320, 4160),
+    (3, 128, 20, 128, 2112),
+    (30, 8, 1, 512, 2112),          # fused down product, then with codes from memory
+    (60, 8, 2, 4160, 1088),
+    (20, 10, 2, 192, 8256),
     (150, 4, 2, 448, 256),          # about 64 rows an expert
     (301, 7, 4, 256, 320),          # 128-row tiles
     (700, 2, 2, 320, 192),          # 256-row tiles

@@ -99,12 +99,11 @@ def test_moe_refusals(lib, kw, want):
 
 def test_moe_workspace(lib):
     need = lib.w4a8_moe_ffn_workspace_bytes(4, 8, 2, 256, 128, BF16)
-    # x codes, h, its codes and the products of every slot
-    assert need >= 4 * 256 + 8 * 128 * 3 + 8 * 256 * 2
+    assert need >= 8 * 128 * 2                         # h of every slot
     assert moe(lib, ws_bytes=need - 1) == SHAPE
     assert lib.w4a8_moe_ffn_workspace_bytes(0, 8, 2, 256, 128, BF16) == 0
     assert lib.w4a8_moe_ffn_workspace_bytes(4, 8, 2, 250, 128, BF16) == 0
-    assert (lib.w4a8_moe_ffn_workspace_bytes(4, 8, 2, 256, 128, F32) > need)
+    assert lib.w4a8_moe_ffn_workspace_bytes(4, 8, 2, 256, 128, F32) >= need
 
 
 def lora(lib, **kw):

@@ -17,10 +17,10 @@ namespace {
 // out[t][c] = sum over the token's slots j, in order, of weights[t][j] *
 // y[t top_k + j][c], in binary32; slots without an expert were never written and
 // are skipped.  A stream over y: 8 columns a thread, four slots' loads in
-// flight.  y has the output's type: for bf16 outputs each product is rounded to
-// bf16 once before the sum (halving the largest intermediate; two roundings of
-// 2^-8 instead of one).
-template <bool BF16>
+// flight.  YBF16: y was rounded to bf16 on its way here (bf16 outputs of large
+// batches, where y is the largest intermediate: two roundings of 2^-8 instead of
+// one, for half of its traffic).
+template <bool YBF16, bool BF16>
 __global__ __launch_bounds__(256) void combine_kernel(const void *__restrict__ y,
                                                       const int32_t *__restrict__ ids,
                                                       const float *__restrict__ weights,
@@ -46,8 +46,8 @@ __global__ __launch_bounds__(256) void combine_kernel(const void *__restrict__ y
             const int id = ids[j];
             ok[jj] = j0 + jj < top_k && id >= 0 && id < experts;
             w[jj] = weights[j];
-            const u32x4 *p = (const u32x4 *)y + (row0 + j) * (BF16 ? vecs : 2 * vecs);
-            if constexpr (BF16) {
+            const u32x4 *p = (const u32x4 *)y + (row0 + j) * (YBF16 ? vecs : 2 * vecs);
+            if constexpr (YBF16) {
                 a[jj] = p[v];
             } else {
                 a[jj] = p[2 * v];
@@ -57,7 +57,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const void *__restrict__ y
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
             float f[8];
-            if constexpr (BF16) {
+            if constexpr (YBF16) {
                 bf16x8_to_f32(a[jj], f);
             } else {
                 const f32x4 lo = __builtin_bit_cast(f32x4, a[jj]);
@@ -84,7 +84,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const void *__restrict__ y
 
 // --------------------------------------------------------------- products --
 struct Product {
-    const int8_t *a_q;
+    const void *a_q;
     const float *a_s;
     const uint8_t *w, *grp;
     const float *ch;
@@ -100,41 +100,245 @@ void launch_sel_tiled(const Product &p, hipStream_t stream) {
     const int64_t grid = (int64_t)p.sel.slots * ((p.n + BN - 1) / BN);
     gemm_tiled_kernel<kW4Sym, BM, BN, WM, WN, 0, SEL>
         <<<dim3((unsigned)grid, 1), 64 * WM * WN, 0, stream>>>(
-            p.a_q, p.a_s, p.w, p.grp, p.ch, 0, p.n, p.k, p.out, p.ldo, p.out_dtype, p.k,
+            (const int8_t *)p.a_q, p.a_s, p.w, p.grp, p.ch, 0, p.n, p.k, p.out, p.ldo, p.out_dtype, p.k,
             (int64_t)device_cu_count(), p.sel);
 }
 
+// Few rows an expert: two 16-channel tiles per workgroup of four wavefronts that
+// split K, load batches of two chunks.  Measured on one box (16 tokens of 4 over
+// 32 experts of 4096 x 2048; gate-up, down): 8 wavefronts with 4 chunks 57.7, 55.0
+// us (registers leave one workgroup per CU); 8 with 2 41.2, 24.4; 4 with 2 35.5,
+// 18.8; 2 with 2 36.8, 19.5; one tile per workgroup for the down product 21.2 at
+// best.
+template <int SEL, bool FUSED, int AV>
+void launch_sel_skinny(const Product &p, int bm, hipStream_t stream) {
+    constexpr int NT = 2, WAVES = 4, D = 2;
+    const unsigned rows = SEL == kSelDirect ? (unsigned)p.rows : (unsigned)p.sel.slots;
+    const dim3 grid((unsigned)((p.n / kNTile + NT - 1) / NT), rows);
+    const size_t lds = FUSED ? (size_t)bm * (p.k + 16) : 0;
+    gemm_skinny_kernel<kW4Sym, 1, NT, WAVES, D, FUSED, AV, 0, false, SEL>
+        <<<grid, 64 * WAVES, lds, stream>>>(p.a_q, p.a_s, p.w, p.grp, p.ch, 0, p.n, p.k, p.out,
+                                            p.out_dtype, nullptr, nullptr,
+                                            (int64_t)device_cu_count(), p.sel);
+}
+
+// FUSED: the row vectors a lane holds, for rows of up to kFusedRowMax.
+constexpr int64_t kFusedRowMax = 8192;
 template <int SEL>
-void launch_sel_skinny(const Product &p, hipStream_t stream) {
-    constexpr int NT = SEL == kSelGateUp ? 2 : 1;
-    const dim3 grid((unsigned)(p.n / (kNTile * NT)), (unsigned)p.sel.slots);
-    gemm_skinny_kernel<kW4Sym, 1, NT, 8, 4, false, 1, 0, false, SEL>
-        <<<grid, 512, 0, stream>>>(p.a_q, p.a_s, p.w, p.grp, p.ch, 0, p.n, p.k, p.out,
-                                   p.out_dtype, nullptr, nullptr, (int64_t)device_cu_count(),
-                                   p.sel);
+void launch_sel_fused(const Product &p, int bm, hipStream_t stream) {
+    if (p.k <= 1024) launch_sel_skinny<SEL, true, 2>(p, bm, stream);
+    else if (p.k <= 2048) launch_sel_skinny<SEL, true, 4>(p, bm, stream);
+    else if (p.k <= 4096) launch_sel_skinny<SEL, true, 8>(p, bm, stream);
+    else launch_sel_skinny<SEL, true, 16>(p, bm, stream);
+}
+
+// ----------------------------------------------------- down, token by token --
+// The down product and the weighted sum of a token in one workgroup, 16 output
+// columns each (kSelDirect batches: too few rows for two tokens to share an
+// expert's weights often).  A wavefront takes one slot, or one of `parts` parts
+// of K of a slot: it reads the slot's row of h (from L2) for the maximum, puts the
+// codes of its part into LDS of its own, and multiplies; all 16 rows of its MFMA
+// are that one row.  The exact int32 sums of a slot's parts meet in LDS; then 16
+// threads add the slots up in order.  y is never rounded.
+//   Bound by latency: ids, then weights and h side by side, then the sum.  What
+// the sum needs is read before it (read after, 8 slots of dependent loads cost
+// 3 us), and the codes pass through LDS, which keeps the multiplying loop
+// short (rounding at the operand gave 20 KB of straight code: 9.8 us).
+constexpr int kTokenWaves = 8;
+constexpr int kTokenKMax = 16384;        // LDS: at most 8 parts of K, 128 KB
+
+__global__ __launch_bounds__(64 * kTokenWaves) void token_down_kernel(
+    const uint16_t *__restrict__ h, const int32_t *__restrict__ ids,
+    const float *__restrict__ weights, const uint8_t *__restrict__ w,
+    const uint8_t *__restrict__ grp, const float *__restrict__ ch, int top_k, int experts,
+    int64_t n, int k, int parts, int part_bytes, void *__restrict__ out, int bf16) {
+    constexpr int D = 2;
+    extern __shared__ __attribute__((aligned(16))) uint8_t code_lds[];   // [waves][part_bytes]
+    __shared__ int red[32][16];
+    __shared__ float sc[32][16];         // channel scales, row scale and weight of a slot
+    __shared__ float sa[32], sw[32];
+    const int tid = threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const int c = lane & 15, kq = lane >> 4;
+    const int64_t t = blockIdx.y;
+    const int64_t tile = blockIdx.x;
+    ids += t * top_k;
+    weights += t * top_k;
+    (&red[0][0])[tid] = 0;
+    (&sc[0][0])[tid] = 0.0f;
+    if (tid < 32) sa[tid] = sw[tid] = 0.0f;      // unused slots add nothing
+    __syncthreads();
+
+    const int nfull = k >> 7, G = k >> 6, vecs = k >> 3;
+    const bool has_half = (k & 64) != 0;
+    const int part = wave % parts;
+    const int per = (nfull + parts - 1) / parts;
+    const int j0 = part * per < nfull ? part * per : nfull;
+    const int j1 = j0 + per < nfull ? j0 + per : nfull;
+    const bool half_here = has_half && part == parts - 1;
+    // this part's vectors of the row (the last part's with the trailing half chunk)
+    const int v0 = j0 * 16, v1 = half_here ? vecs : j1 * 16;
+    uint8_t *codes = code_lds + wave * part_bytes;
+    const WParamSel psel = wparam_selectors<kW4Sym>(c);
+    for (int slot = wave / parts; slot < top_k; slot += kTokenWaves / parts) {
+        const int e = ids[slot];
+        if (e < 0 || e >= experts) continue;
+        const int64_t wrow = (int64_t)e * n + tile * kNTile;
+        const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(w + wrow * k / 2, (uint32_t)(8 * k));
+        const __amdgpu_buffer_rsrc_t rp = buffer_rsrc(grp + wrow * G, (uint32_t)(16 * G));
+        const __amdgpu_buffer_rsrc_t rh =
+            buffer_rsrc(h + (t * top_k + slot) * (int64_t)k, (uint32_t)(2 * k));
+        struct Batch {
+            u32x4 w[D];
+            uint32_t p[D][2];
+        };
+        // chunks past the part are clamped to a valid one and not used
+        auto load = [&](Batch &b, int jb) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                const int j = jb + d < j1 ? jb + d : nfull - 1;
+                b.w[d] = buffer_load16_nt(rw, lane * 16, j * kChunkBytes);
+                b.p[d][0] = buffer_load4(rp, c & ~3, 2 * j * kNTile);
+                b.p[d][1] = buffer_load4(rp, c & ~3, (2 * j + 1) * kNTile);
+            }
+        };
+        u32x4 v[4];
+        auto load_row = [&](int i0) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + u * 64 + lane;
+                v[u] = buffer_load16(rh, (i < vecs ? i : vecs - 1) * 16, 0);
+            }
+        };
+        // the first vectors of h ahead of the weights: loads complete in order
+        load_row(0);
+        Batch b0, b1;
+        load(b0, j0);
+        load(b1, j0 + D);
+        __builtin_amdgcn_sched_barrier(0);
+        float chv = 0.0f, wv = 0.0f;
+        if (part == 0) {
+            chv = ch[wrow + c];
+            wv = weights[slot];
+        }
+        float amax = 0.0f;
+#pragma unroll 1
+        for (int i0 = 0; i0 < vecs; i0 += 256) {
+            if (i0) load_row(i0);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float f[8];
+                bf16x8_to_f32(v[u], f);
+                amax = __builtin_fmaxf(amax, absmax_f32x8(f));
+            }
+        }
+        amax = __uint_as_float(wave_max_u32(__float_as_uint(amax)));
+        float s, inv;
+        act_scale_pair_rcp(amax, s, inv);
+#pragma unroll 1
+        for (int i = v0 + lane; i < v1; i += 64) {
+            float f[8];
+            bf16x8_to_f32(buffer_load16(rh, i * 16, 0), f);
+            *(u32x2 *)(codes + (i - v0) * 8) = codes8(f, inv);
+        }
+        // written and read by this wavefront alone: its LDS operations are in order
+        __builtin_amdgcn_wave_barrier();
+        asm volatile("" ::: "memory");
+        v4i acc = {0, 0, 0, 0};
+        auto compute = [&](const Batch &b, int jb) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                if (jb + d >= j1) break;
+#pragma unroll
+                for (int st = 0; st < 2; ++st) {
+                    uint32_t mul, add;
+                    wparam_consts<kW4Sym>(b.p[d][st], psel, mul, add);
+                    const WRec<kW4Sym> rec = {b.w[d]};
+                    const v4i a =
+                        *(const v4i *)(codes + (jb + d - j0) * 128 + st * 64 + kq * 16);
+                    acc = mfma16x16x64(wrec_operand_ma<kW4Sym>(rec, st, mul, add), a, acc);
+                }
+            }
+        };
+#pragma unroll 1
+        for (int jb = j0; jb < j1; jb += 2 * D) {
+            compute(b0, jb);
+            load(b0, jb + 2 * D);
+            compute(b1, jb + D);
+            load(b1, jb + 3 * D);
+        }
+        if (half_here) {
+            // trailing 64-wide chunk: 8-byte records, one K step
+            const u32x2 r = *(const u32x2 *)(w + wrow * k / 2 + (int64_t)nfull * kChunkBytes +
+                                             lane * 8);
+            uint32_t mul, add;
+            wparam_consts<kW4Sym>(buffer_load4(rp, c & ~3, 2 * nfull * kNTile), psel, mul, add);
+            const v4i a = *(const v4i *)(codes + (nfull - j0) * 128 + kq * 16);
+            acc = mfma16x16x64(unpack_step(r.x, r.y, mul, add), a, acc);
+        }
+        if (c == 0)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) atomicAdd(&red[slot][4 * kq + i], acc[i]);
+        if (part == 0 && lane < 16) {
+            sc[slot][lane] = chv;
+            if (lane == 0) {
+                sa[slot] = s;
+                sw[slot] = wv;
+            }
+        }
+    }
+    __syncthreads();
+    if (tid < 16) {
+        const int64_t col = tile * kNTile + tid;
+        float sum = 0.0f;
+        for (int slot = 0; slot < top_k; ++slot) {
+            const float y = (float)red[slot][tid] * sa[slot] * sc[slot][tid];
+            sum = sum + sw[slot] * y;
+        }
+        if (bf16) ((uint16_t *)out)[t * n + col] = (uint16_t)bf16x2_rne(sum, sum);
+        else ((float *)out)[t * n + col] = sum;
+    }
 }
 
 template <int SEL>
 void launch_sel(const Product &p, int bm, hipStream_t stream) {
-    // the skinny kernel needs one whole 128-wide chunk of K
-    if (bm == 16 && p.k >= kChunkK) launch_sel_skinny<SEL>(p, stream);
-    else if (bm <= 64) launch_sel_tiled<64, 256, 1, 8, SEL>(p, stream);
+    if (bm <= 64) launch_sel_tiled<64, 256, 1, 8, SEL>(p, stream);
     else if (bm == 128) launch_sel_tiled<128, 256, 1, 8, SEL>(p, stream);
     else launch_sel_tiled<256, 256, 4, 4, SEL>(p, stream);
 }
 
-// Row block of the products for `rows` rows over `experts` experts.
+// Row block of the products for `rows` rows over `experts` experts, by the rows
+// an expert has on average.
 int row_block(int64_t rows, int64_t experts) {
     const int64_t met = rows < experts ? rows : experts;
     const int64_t avg = rows / met;
-    return avg <= 16 ? 16 : avg <= 64 ? 64 : avg <= 512 ? 128 : 256;
+    return avg <= 4 ? 8 : avg <= 16 ? 16 : avg <= 64 ? 64 : avg <= 512 ? 128 : 256;
+}
+
+// Whether a batch is taken row by row (kSelDirect, two launches) rather than
+// sorted (four): where the weights that two tokens then read separately cost
+// less than two launches and their gaps, about 10 us.
+bool direct_pays(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inter) {
+    if (tokens * top_k > 64 || hidden > kFusedRowMax || hidden < kChunkK || inter < kChunkK ||
+        inter > kTokenKMax)
+        return false;
+    double miss = 1.0;          // an expert that no token chose, choices even
+    const double hit = top_k < experts ? (double)top_k / experts : 1.0;
+    for (int64_t t = 0; t < tokens; ++t) miss *= 1.0 - hit;
+    const double again = (double)(tokens * top_k) - experts * (1.0 - miss);
+    return again * 1.55 * hidden * inter < 50e6;       // bytes of an expert's weights
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
+enum MoeForm { kMoeDirect, kMoeFew, kMoeTiled };
+
 struct MoeSpace {
     size_t xq, xs, order, src, tiles, h, hq, hs, y, end;
+    MoeForm form;
     int bm;
+    int y_dtype;              // 0 binary32, 1 bf16
+    bool fused_down;          // kMoeFew: the down product takes its rows' codes itself
     int64_t slots;
 };
 
@@ -143,22 +347,29 @@ MoeSpace moe_space(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidde
     const size_t t = (size_t)tokens, r = (size_t)(tokens * top_k);
     MoeSpace s;
     s.bm = row_block((int64_t)r, experts);
+    // the skinny kernel needs one whole 128-wide chunk of K
+    s.form = direct_pays(tokens, experts, top_k, hidden, inter)    ? kMoeDirect
+             : s.bm <= 16 && hidden >= kChunkK && inter >= kChunkK ? kMoeFew
+                                                                   : kMoeTiled;
+    s.fused_down = s.form == kMoeFew && inter <= kFusedRowMax && s.bm * (inter + 16) <= 34 * 1024;
     s.slots = plan_slots((int64_t)r, experts, s.bm);
+    s.y_dtype = s.form == kMoeTiled ? out_dtype : 0;
     size_t at = 0;
-    auto take = [&](size_t bytes) {
+    auto take = [&](bool used, size_t bytes) {
         const size_t here = at;
-        at += up256(bytes);
+        at += used ? up256(bytes) : 0;
         return here;
     };
-    s.xq = take(t * hidden);
-    s.xs = take(t * 4);
-    s.order = take(r * 4);
-    s.src = take(r * 4);
-    s.tiles = take((size_t)s.slots * 16);
-    s.h = take(r * inter * 2);
-    s.hq = take(r * inter);
-    s.hs = take(r * 4);
-    s.y = take(r * hidden * (out_dtype == 1 ? 2 : 4));
+    const bool sorted = s.form != kMoeDirect;
+    s.xq = take(sorted, t * hidden);
+    s.xs = take(sorted, t * 4);
+    s.order = take(sorted, r * 4);
+    s.src = take(sorted, r * 4);
+    s.tiles = take(sorted, (size_t)s.slots * 16);
+    s.h = take(true, r * inter * 2);
+    s.hq = take(sorted && !s.fused_down, r * inter);
+    s.hs = take(sorted && !s.fused_down, r * 4);
+    s.y = take(sorted, r * hidden * (s.y_dtype == 1 ? 2 : 4));
     s.end = at;
     return s;
 }
@@ -179,15 +390,8 @@ hipError_t launch_moe_ffn(const uint16_t *x, const int32_t *ids, const float *we
     uint8_t *ws = (uint8_t *)workspace;
     const int64_t rows = tokens * top_k;
     int32_t *order = (int32_t *)(ws + s.order), *src = (int32_t *)(ws + s.src);
-    const int4 *tiles = (const int4 *)(ws + s.tiles);
-    hipError_t err = launch_plan(ids, rows, experts, false, top_k, s.bm, order, src,
-                                 (int32_t *)(ws + s.tiles), stream);
-    if (err != hipSuccess) return err;
-    err = launch_quantize_rows(x, tokens, hidden, (int8_t *)(ws + s.xq), (float *)(ws + s.xs),
-                               stream);
-    if (err != hipSuccess) return err;
     Product p{};
-    p.a_q = (const int8_t *)(ws + s.xq);
+    p.a_q = ws + s.xq;
     p.a_s = (const float *)(ws + s.xs);
     p.w = w13;
     p.grp = g13;
@@ -198,13 +402,36 @@ hipError_t launch_moe_ffn(const uint16_t *x, const int32_t *ids, const float *we
     p.out = ws + s.h;
     p.ldo = inter;
     p.out_dtype = 1;
-    p.sel = SelArgs{tiles, src, (uint32_t)(tokens * hidden), (int32_t)s.slots, inter};
-    launch_sel<kSelGateUp>(p, s.bm, stream);
-    err = launch_quantize_rows((const uint16_t *)(ws + s.h), rows, inter, (int8_t *)(ws + s.hq),
-                               (float *)(ws + s.hs), stream);
+    if (s.form == kMoeDirect) {
+        p.a_q = x;
+        p.sel = SelArgs{nullptr, ids, 0u, top_k, experts, inter};
+        launch_sel_fused<kSelDirect>(p, 1, stream);
+        int parts = 1;                    // wavefronts of a slot, a power of two
+        while (parts * 2 * top_k <= kTokenWaves) parts *= 2;
+        const int part_bytes =
+            (int)(((inter / 128 + parts - 1) / parts) * 128 + 64);   // and a half chunk
+        token_down_kernel<<<dim3((unsigned)(hidden / kNTile), (unsigned)tokens),
+                            64 * kTokenWaves, (size_t)(kTokenWaves * part_bytes), stream>>>(
+            (const uint16_t *)(ws + s.h), ids, weights, w2, g2, c2, top_k, experts, hidden,
+            (int)inter, parts, part_bytes, out, out_dtype == 1);
+        return hipGetLastError();
+    }
+    hipError_t err = launch_plan_quantize(ids, rows, experts, top_k, s.bm, order, src,
+                                          (int32_t *)(ws + s.tiles), x, tokens, hidden,
+                                          (int8_t *)(ws + s.xq), (float *)(ws + s.xs), stream);
     if (err != hipSuccess) return err;
-    p.a_q = (const int8_t *)(ws + s.hq);
-    p.a_s = (const float *)(ws + s.hs);
+    p.sel = SelArgs{(const int4 *)(ws + s.tiles), src, (uint32_t)(tokens * hidden),
+                    (int32_t)s.slots, experts, inter};
+    if (s.form == kMoeFew) launch_sel_skinny<kSelGateUp, false, 1>(p, s.bm, stream);
+    else launch_sel<kSelGateUp>(p, s.bm, stream);
+    p.a_q = ws + s.h;
+    if (!s.fused_down) {
+        err = launch_quantize_rows((const uint16_t *)(ws + s.h), rows, inter,
+                                   (int8_t *)(ws + s.hq), (float *)(ws + s.hs), stream);
+        if (err != hipSuccess) return err;
+        p.a_q = ws + s.hq;
+        p.a_s = (const float *)(ws + s.hs);
+    }
     p.w = w2;
     p.grp = g2;
     p.ch = c2;
@@ -212,18 +439,18 @@ hipError_t launch_moe_ffn(const uint16_t *x, const int32_t *ids, const float *we
     p.k = inter;
     p.out = ws + s.y;
     p.ldo = hidden;
-    p.out_dtype = out_dtype;
-    p.sel = SelArgs{tiles, order, 0u, (int32_t)s.slots, 0};
-    launch_sel<kSelScatter>(p, s.bm, stream);
+    p.out_dtype = s.y_dtype;
+    p.sel.map = order;
+    if (s.fused_down) launch_sel_fused<kSelScatter>(p, s.bm, stream);
+    else if (s.form == kMoeFew) launch_sel_skinny<kSelScatter, false, 1>(p, s.bm, stream);
+    else launch_sel<kSelScatter>(p, s.bm, stream);
     const int64_t gy = tokens < 32768 ? tokens : 32768;
     const dim3 grid((unsigned)((hidden / 8 + 255) / 256), (unsigned)gy,
                     (unsigned)((tokens + gy - 1) / gy));
-    if (out_dtype == 1)
-        combine_kernel<true><<<grid, 256, 0, stream>>>(ws + s.y, ids, weights, tokens, experts,
-                                                       top_k, hidden, out);
-    else
-        combine_kernel<false><<<grid, 256, 0, stream>>>(ws + s.y, ids, weights, tokens, experts,
-                                                        top_k, hidden, out);
+    const auto combine = s.y_dtype == 1     ? combine_kernel<true, true>
+                         : out_dtype == 1 ? combine_kernel<false, true>
+                                          : combine_kernel<false, false>;
+    combine<<<grid, 256, 0, stream>>>(ws + s.y, ids, weights, tokens, experts, top_k, hidden, out);
     return hipGetLastError();
 }
 

@@ -140,12 +140,18 @@ __device__ __forceinline__ u32x4 buffer_load16_nt(__amdgpu_buffer_rsrc_t r, int 
 //               bf16(silu(gate) * up) to sorted row i of [rows, inter].
 //   kSelScatter the rows of A are the sorted rows; sorted row i is stored to
 //               row dst[i].
-enum Sel : int { kSelNone = 0, kSelGateUp = 1, kSelScatter = 2 };
+//   kSelDirect  kSelGateUp without a table, for batches so small that sorting
+//               them would take longer than it saves: tile y is the one row y,
+//               of expert map[y] and token y / slots.
+// FUSED with SEL: A is bf16 and each workgroup takes the codes of its tile's rows
+// into LDS, a wavefront per row (act_scale_pair_rcp).
+enum Sel : int { kSelNone = 0, kSelGateUp = 1, kSelScatter = 2, kSelDirect = 3 };
 struct SelArgs {
     const int4 *tiles;       // [slots] {expert, first sorted row, rows, 0}
-    const int32_t *map;      // src (kSelGateUp) or dst (kSelScatter) of a sorted row
+    const int32_t *map;      // src (kSelGateUp) or dst (kSelScatter) of a sorted row, or the ids
     uint32_t a_bytes;        // bytes of A (kSelGateUp: gathered through 32-bit offsets)
-    int32_t slots;
+    int32_t slots;           // entries of the table; kSelDirect: rows of a token
+    int32_t experts;         // kSelDirect: ids outside [0, experts) are unused
     int64_t inter;
 };
 
@@ -224,27 +230,40 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_skinny_kernel(
     constexpr int ROWS = MT * 16;
     extern __shared__ __attribute__((aligned(16))) uint8_t act_lds[];  // FUSED: [m][k + 16]
     static_assert(AB == 0 || !FUSED, "per-block scales only in the non-fused form");
-    static_assert(SEL == kSelNone || (!FUSED && AB == 0), "rows that choose weights");
-    static_assert(SEL != kSelGateUp || NT == 2, "a gate tile and its up tile");
-    int first_row = 0;                       // the tile's first sorted row
-    if constexpr (SEL != kSelNone) {
-        const int4 tile = sel.tiles[blockIdx.y];
-        if (tile.z == 0) return;
-        first_row = tile.y;
-        m = tile.z;
-        w_packed += (int64_t)tile.x * (n * k / 2);
-        grp_scale += (int64_t)tile.x * (n * (k / kGroup)) * (WF == kW4Lqq ? 2 : 1);
-        ch_scale += (int64_t)tile.x * n;
-        sel.map += first_row;
-        if constexpr (SEL == kSelScatter) {
-            act = (const int8_t *)act + (int64_t)first_row * k;
-            a_scale += first_row;
-        }
-    }
     __shared__ int red[AB ? 1 : NT][16][AB ? 1 : ROWS + 4];
     __shared__ float redf[AB ? WAVES : 1][AB ? NT : 1][16][AB ? ROWS + 1 : 1];
     __shared__ float sa_lds[ROWS];
     __shared__ unsigned amax_lds[ROWS];
+    static_assert(SEL == kSelNone || AB == 0, "rows that choose weights");
+    constexpr bool kGateUp = SEL == kSelGateUp || SEL == kSelDirect;
+    static_assert(!kGateUp || NT == 2, "a gate tile and its up tile");
+    static_assert(SEL != kSelDirect || FUSED, "the row itself");
+    static_assert(SEL != kSelGateUp || !FUSED, "gathered rows come as codes");
+    int first_row = 0;                       // the tile's first sorted row
+    if constexpr (SEL != kSelNone) {
+        int expert;
+        if constexpr (SEL == kSelDirect) {
+            expert = sel.map[blockIdx.y];
+            if (expert < 0 || expert >= sel.experts) return;
+            first_row = blockIdx.y;
+            m = 1;
+            act = (const uint16_t *)act + (int64_t)(first_row / sel.slots) * k;
+        } else {
+            const int4 tile = sel.tiles[blockIdx.y];
+            if (tile.z == 0) return;
+            expert = tile.x;
+            first_row = tile.y;
+            m = tile.z;
+            sel.map += first_row;
+            if constexpr (SEL == kSelScatter) {
+                act = (const int8_t *)act + (int64_t)first_row * k * (FUSED ? 2 : 1);
+                a_scale += first_row;
+            }
+        }
+        w_packed += (int64_t)expert * (n * k / 2);
+        grp_scale += (int64_t)expert * (n * (k / kGroup)) * (WF == kW4Lqq ? 2 : 1);
+        ch_scale += (int64_t)expert * n;
+    }
 
     const int tid = threadIdx.x;
     // readfirstlane: the compiler then knows the wavefront index, and so each
@@ -252,9 +271,9 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_skinny_kernel(
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int c = lane & 15, kq = lane >> 4;
     const int64_t ntiles = n / kNTile;
-    const int64_t t0 = (int64_t)blockIdx.x * (SEL == kSelGateUp ? 1 : NT);
+    const int64_t t0 = (int64_t)blockIdx.x * (kGateUp ? 1 : NT);
     // tiles from one of this workgroup's to the next
-    const int tstep = SEL == kSelGateUp ? (int)(sel.inter / kNTile) : 1;
+    const int tstep = kGateUp ? (int)(sel.inter / kNTile) : 1;
     // k <= K_MAX: the K-derived counts fit 32 bits (shorter scalar code ahead
     // of the first loads: 150 -> 123 instructions before the decode kernel's
     // last prologue request, decode 6.52 -> 6.46 us, 4 x 4096 x 4096 5.67 ->
@@ -295,8 +314,8 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_skinny_kernel(
     constexpr int kPSize = WF == kW4Lqq ? 2 : 1;                 // bytes per group parameter
     const int wtile = kWTileMul * (int)k;
     const int ptile = kNTile * (int)G * kPSize;
-    const int tiles_here = (int)(SEL == kSelGateUp ? tstep + 1
-                                                   : ntiles - t0 < NT ? ntiles - t0 : NT);
+    const int tiles_here =
+        (int)(kGateUp ? tstep + 1 : ntiles - t0 < NT ? ntiles - t0 : NT);
     const int wstep = tstep * wtile, pstep = tstep * ptile;
     const __amdgpu_buffer_rsrc_t rw =
         buffer_rsrc(w_packed + t0 * (int64_t)wtile, (uint32_t)tiles_here * wtile);
@@ -365,6 +384,47 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_skinny_kernel(
     if constexpr (!FUSED) {
         load_batch(cur, j0);
         lds_barrier();  // red cleared
+    } else if constexpr (SEL != kSelNone) {
+        // A wavefront per row, its AV vectors per lane requested ahead of the
+        // first weight batch: the maximum is a wavefront reduction, so one
+        // barrier after the codes is all.  Vectors past the row are clamped to
+        // its last one, which changes no maximum, and not stored.
+        const int vpr = k32 >> 3;
+        u32x4 av[AV];
+        auto load_row = [&](int row) {
+#pragma unroll
+            for (int u = 0; u < AV; ++u) {
+                const int v = lane + u * 64;
+                av[u] = buffer_load16(ra, (row * vpr + (v < vpr ? v : vpr - 1)) * 16, 0);
+            }
+        };
+        if (wave < m) load_row(wave);
+        __builtin_amdgcn_sched_barrier(0);
+        load_batch(cur, j0);
+        for (int row = wave; row < m; row += WAVES) {
+            if (row != wave) load_row(row);
+            float amax = 0.0f;
+#pragma unroll
+            for (int u = 0; u < AV; ++u) {
+                float f[8];
+                bf16x8_to_f32(av[u], f);
+                amax = __builtin_fmaxf(amax, absmax_f32x8(f));
+            }
+            amax = __uint_as_float(wave_max_u32(__float_as_uint(amax)));
+            float s, inv;
+            act_scale_pair_rcp(amax, s, inv);
+            if (lane == 0) sa_lds[row] = s;
+#pragma unroll
+            for (int u = 0; u < AV; ++u) {
+                const int v = lane + u * 64;
+                if (v < vpr) {
+                    float f[8];
+                    bf16x8_to_f32(av[u], f);
+                    *(u32x2 *)(act_lds + row * lds_stride + v * 8) = codes8(f, inv);
+                }
+            }
+        }
+        lds_barrier();  // red cleared, codes written
     } else {
         // Per-row absmax -> scale, then the row's codes into LDS.  Threads are
         // split into m groups of tpr (a power of two) threads per row.  All
@@ -654,11 +714,11 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_skinny_kernel(
 #pragma unroll
             for (int i = 0; i < 4; ++i) atomicAdd(&red[nt][4 * kq + i][mt * 16 + c], acc[nt][mt][i]);
     __syncthreads();
-    if constexpr (SEL == kSelGateUp) {
+    if constexpr (kGateUp) {
         for (int idx = tid; idx < m * 4; idx += THREADS) {
             const int row = idx >> 2, quad = idx & 3;
             const int64_t nn = t0 * kNTile + 4 * quad;
-            const float sa = a_scale[sel.map[row]];
+            const float sa = FUSED ? sa_lds[row] : a_scale[sel.map[row]];
             const f32x4 sg = *(const f32x4 *)(ch_scale + nn);
             const f32x4 su = *(const f32x4 *)(ch_scale + sel.inter + nn);
             float y[4];

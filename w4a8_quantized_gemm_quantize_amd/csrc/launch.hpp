@@ -103,6 +103,13 @@ hipError_t launch_plan(const int32_t *ids, int64_t rows, int32_t groups, bool no
                        int32_t top_k, int bm, int32_t *order, int32_t *src, int32_t *tiles,
                        hipStream_t stream);
 
+// The plan (ids outside the groups take no part) and the per-row codes and scales of
+// x [xrows, cols] (launch_quantize_rows) in one launch.
+hipError_t launch_plan_quantize(const int32_t *ids, int64_t rows, int32_t groups, int32_t top_k,
+                                int bm, int32_t *order, int32_t *src, int32_t *tiles,
+                                const uint16_t *x, int64_t xrows, int64_t cols, int8_t *q,
+                                float *scales, hipStream_t stream);
+
 // Experts' products (experts.hip), arguments as w4a8_moe_ffn in w4a8.h.
 size_t moe_workspace_bytes(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden,
                            int64_t inter, int out_dtype);

@@ -1,5 +1,6 @@
 // plan.hip -- sorting rows by the weights they choose and cutting each group
 // into row tiles: the table that the products of experts.hip and lora.hip walk.
+// The experts' layer quantizes its rows in the same launch.
 #include "device_common.hpp"
 #include "launch.hpp"
 
@@ -19,39 +20,63 @@ namespace {
 // host has without the ids.
 //   none_last: ids outside [0, groups - 1) make up group groups - 1; else ids
 // outside [0, groups) take no part.
+//   Bound by the latency of the id loads: each wavefront requests kIdBatch of
+// its 64-id chunks together (one at a time, 16384 rows took 16.8 us).
 constexpr int kPlanThreads = 1024;
+constexpr int kIdBatch = 8;
+
+struct PlanArgs {
+    const int32_t *ids;
+    int32_t *order, *src;
+    int4 *tiles;
+    int rows, groups, none_last, top_k, bm, slots;
+};
 
 __device__ __forceinline__ int plan_group(int id, int groups, int none_last) {
     if (none_last) return id >= 0 && id < groups - 1 ? id : groups - 1;
     return id < groups ? id : -1;
 }
 
-__global__ __launch_bounds__(kPlanThreads) void plan_kernel(
-    const int32_t *__restrict__ ids, int rows, int groups, int none_last, int top_k, int bm,
-    int slots, int32_t *__restrict__ order, int32_t *__restrict__ src, int4 *__restrict__ tiles) {
+__device__ __forceinline__ void plan_block(const PlanArgs &p, int g) {
     __shared__ uint32_t seen[kPlanMaxGroups / 32];
     __shared__ int lt_of[kPlanThreads / 64], eq_of[kPlanThreads / 64];
-    const int g = blockIdx.x;
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int waves = blockDim.x >> 6;
-    const int words = (groups + 31) >> 5;
-    for (int w = tid; w < words; w += blockDim.x) seen[w] = 0u;
-    __syncthreads();
+    const int words = (p.groups + 31) >> 5;
     // a contiguous run of whole 64-row chunks per wavefront
-    const int chunks = (rows + 63) >> 6;
+    const int chunks = (p.rows + 63) >> 6;
     const int per = (chunks + waves - 1) / waves;
     const int c0 = wave * per, c1 = c0 + per < chunks ? c0 + per : chunks;
+    int id[kIdBatch];
+    auto load = [&](int c) {
+#pragma unroll
+        for (int u = 0; u < kIdBatch; ++u) {
+            const int i = (c + u) * 64 + lane;
+            id[u] = c + u < c1 && i < p.rows ? p.ids[i] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kIdBatch; ++u) {
+            const int i = (c + u) * 64 + lane;
+            id[u] = c + u < c1 && i < p.rows ? plan_group(id[u], p.groups, p.none_last) : -1;
+        }
+    };
+    load(c0);
+    for (int w = tid; w < words; w += blockDim.x) seen[w] = 0u;
+    __syncthreads();
     int lt = 0, eq = 0;
-    for (int c = c0; c < c1; ++c) {
-        const int i = c * 64 + lane;
-        const int id = i < rows ? plan_group(ids[i], groups, none_last) : -1;
-        const bool low = id >= 0 && id < g;
-        lt += __popcll(__ballot(low));
-        eq += __popcll(__ballot(id == g));
-        if (low) {
-            const uint32_t bit = 1u << (id & 31);
-            if (!(((volatile uint32_t *)seen)[id >> 5] & bit)) atomicOr(&seen[id >> 5], bit);
+    for (int c = c0; c < c1; c += kIdBatch) {
+        if (c > c0) load(c);
+#pragma unroll
+        for (int u = 0; u < kIdBatch; ++u) {
+            const bool low = id[u] >= 0 && id[u] < g;
+            lt += __popcll(__ballot(low));
+            eq += __popcll(__ballot(id[u] == g));
+            if (low) {
+                const uint32_t bit = 1u << (id[u] & 31);
+                if (!(((volatile uint32_t *)seen)[id[u] >> 5] & bit))
+                    atomicOr(&seen[id[u] >> 5], bit);
+            }
         }
     }
     if (lane == 0) {
@@ -66,31 +91,105 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(
         mine += eq_of[w];
     }
     for (int w = 0; w < words; ++w) active += __popc(seen[w]);
-    const int slot0 = before / bm + active;
-    if (g == groups) {
-        for (int s = slot0 + tid; s < slots; s += blockDim.x) tiles[s] = int4{0, 0, 0, 0};
+    const int slot0 = before / p.bm + active;
+    if (g == p.groups) {
+        for (int s = slot0 + tid; s < p.slots; s += blockDim.x) p.tiles[s] = int4{0, 0, 0, 0};
         return;
     }
     if (mine == 0) return;
-    const int slot1 = (before + mine) / bm + active + 1;
+    const int slot1 = (before + mine) / p.bm + active + 1;
     for (int s = tid; s < slot1 - slot0; s += blockDim.x) {
-        const int left = mine - s * bm;
-        tiles[slot0 + s] = left > 0 ? int4{g, before + s * bm, left < bm ? left : bm, 0}
-                                    : int4{0, 0, 0, 0};
+        const int left = mine - s * p.bm;
+        p.tiles[slot0 + s] = left > 0 ? int4{g, before + s * p.bm, left < p.bm ? left : p.bm, 0}
+                                      : int4{0, 0, 0, 0};
     }
     int at = before + base;
-    for (int c = c0; c < c1; ++c) {
-        const int i = c * 64 + lane;
-        const bool is = i < rows && plan_group(ids[i], groups, none_last) == g;
-        const uint64_t m = __ballot(is);
-        if (is) {
-            const int p = at + __popcll(m & ((1ull << lane) - 1));
-            order[p] = i;
-            if (src) src[p] = i / top_k;
+    for (int c = c0; c < c1; c += kIdBatch) {
+        // one batch holds a short run whole: its ids are still in registers
+        if (c1 - c0 > kIdBatch) load(c);
+#pragma unroll
+        for (int u = 0; u < kIdBatch; ++u) {
+            const bool is = id[u] == g;
+            const uint64_t m = __ballot(is);
+            if (is) {
+                const int i = (c + u) * 64 + lane;
+                const int q = at + __popcll(m & ((1ull << lane) - 1));
+                p.order[q] = i;
+                if (p.src) p.src[q] = i / p.top_k;
+            }
+            at += __popcll(m);
         }
-        at += __popcll(m);
     }
 }
+
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs p) {
+    plan_block(p, blockIdx.x);
+}
+
+// The plan in workgroups 0 .. groups, then the rows' codes and scales
+// (act_scale_pair_rcp), a wavefront per row: neither depends on the other, and
+// side by side they cost one launch and the longer of the two.  V vectors (8 elements) per lane stay in registers;
+// longer rows are read a second time.
+template <int V>
+__global__ __launch_bounds__(kPlanThreads) void plan_quantize_kernel(
+    PlanArgs p, const u32x4 *__restrict__ x, int64_t xrows, int vecs, u32x2 *__restrict__ q,
+    float *__restrict__ scales) {
+    if ((int)blockIdx.x <= p.groups) {
+        plan_block(p, blockIdx.x);
+        return;
+    }
+    const int64_t b = blockIdx.x - p.groups - 1;
+    const int64_t row = b * (blockDim.x >> 6) + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    if (row >= xrows) return;
+    const u32x4 *xr = x + row * vecs;
+    u32x4 v[V];
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        const int i = lane + u * 64;
+        v[u] = xr[i < vecs ? i : vecs - 1];
+    }
+    float amax = 0.0f;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        float f[8];
+        bf16x8_to_f32(v[u], f);
+        amax = __builtin_fmaxf(amax, absmax_f32x8(f));        // clamped repeats change nothing
+    }
+    for (int i = lane + V * 64; i < vecs; i += 64) {
+        float f[8];
+        bf16x8_to_f32(xr[i], f);
+        amax = __builtin_fmaxf(amax, absmax_f32x8(f));
+    }
+    amax = __uint_as_float(wave_max_u32(__float_as_uint(amax)));
+    float s, inv;
+    act_scale_pair_rcp(amax, s, inv);
+    u32x2 *qr = q + row * vecs;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        const int i = lane + u * 64;
+        if (i < vecs) {
+            float f[8];
+            bf16x8_to_f32(v[u], f);
+            qr[i] = codes8(f, inv);
+        }
+    }
+    for (int i = lane + V * 64; i < vecs; i += 64) {
+        float f[8];
+        bf16x8_to_f32(xr[i], f);
+        qr[i] = codes8(f, inv);
+    }
+    if (lane == 0) scales[row] = s;
+}
+
+PlanArgs plan_args(const int32_t *ids, int64_t rows, int32_t groups, bool none_last,
+                   int32_t top_k, int bm, int32_t *order, int32_t *src, int32_t *tiles) {
+    return PlanArgs{ids, order, src, (int4 *)tiles, (int)rows, groups, none_last, top_k, bm,
+                    (int)plan_slots(rows, groups, bm)};
+}
+
+// 16 wavefronts once each has a few chunks to read
+int plan_threads(int64_t rows) { return rows >= 4096 ? kPlanThreads : 256; }
 
 }  // namespace
 
@@ -101,11 +200,28 @@ int64_t plan_slots(int64_t rows, int64_t groups, int bm) {
 hipError_t launch_plan(const int32_t *ids, int64_t rows, int32_t groups, bool none_last,
                        int32_t top_k, int bm, int32_t *order, int32_t *src, int32_t *tiles,
                        hipStream_t stream) {
-    // 16 wavefronts once each has a few chunks to read
-    const int threads = rows >= 4096 ? kPlanThreads : 256;
-    plan_kernel<<<groups + 1, threads, 0, stream>>>(ids, (int)rows, groups, none_last, top_k, bm,
-                                                    (int)plan_slots(rows, groups, bm), order, src,
-                                                    (int4 *)tiles);
+    plan_kernel<<<groups + 1, plan_threads(rows), 0, stream>>>(
+        plan_args(ids, rows, groups, none_last, top_k, bm, order, src, tiles));
+    return hipGetLastError();
+}
+
+hipError_t launch_plan_quantize(const int32_t *ids, int64_t rows, int32_t groups, int32_t top_k,
+                                int bm, int32_t *order, int32_t *src, int32_t *tiles,
+                                const uint16_t *x, int64_t xrows, int64_t cols, int8_t *q,
+                                float *scales, hipStream_t stream) {
+    const PlanArgs p = plan_args(ids, rows, groups, false, top_k, bm, order, src, tiles);
+    const int threads = plan_threads(rows);
+    const int64_t per = threads / 64;
+    const unsigned grid = (unsigned)(groups + 1 + (xrows + per - 1) / per);
+    const u32x4 *xv = (const u32x4 *)x;
+    u32x2 *qv = (u32x2 *)q;
+    const int vecs = (int)(cols / 8);
+    if (vecs <= 64 * 4)
+        plan_quantize_kernel<4><<<grid, threads, 0, stream>>>(p, xv, xrows, vecs, qv, scales);
+    else if (vecs <= 64 * 8)
+        plan_quantize_kernel<8><<<grid, threads, 0, stream>>>(p, xv, xrows, vecs, qv, scales);
+    else
+        plan_quantize_kernel<16><<<grid, threads, 0, stream>>>(p, xv, xrows, vecs, qv, scales);
     return hipGetLastError();
 }
 
