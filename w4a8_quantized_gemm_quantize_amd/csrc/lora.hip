@@ -1,16 +1,16 @@
 // lora.hip -- low-rank adapters of many requests beside a shared projection
 // (w4a8_lora_add in w4a8.h): out[t] = y[t] + scale[l] B[l] (A[l] x[t]), l = ids[t].
 //
-// Two launches.  Both walk row tiles, up to BM rows that share an adapter, so an
-// adapter's A and B are read once per tile however the requests are mixed:
+// Both products walk row tiles, up to BM rows that share an adapter, so an adapter's
+// A and B are read once per tile however the requests are mixed:
 //   shrink  v = A x over one of `slices` parts of K: the four wavefronts split
 //           the part, each holding the tile's whole v in accumulators, and add up
 //           in LDS; the part's v goes to the workspace in binary32.
 //   expand  sums the parts (in order), folds the adapter's scale in, and
 //           multiplies by B on the matrix cores with y added in the epilogue.
-// v stays binary32 throughout: the matrix cores take bf16, so expand splits it
-// into bf16 terms (v = hi + lo, error 2^-16, for bf16 outputs; three terms, exact
-// to 2^-24, for binary32 outputs) and multiplies each by the same B operand.
+// v stays binary32 throughout: the matrix cores take bf16, so it is split into
+// bf16 terms (v = hi + lo, error 2^-16, for bf16 outputs; three terms, exact to
+// 2^-24, for binary32 outputs), each multiplied by the same B operand.
 //
 // v_mfma_f32_16x16x32_bf16: lane (r = l % 16, q = l / 16) supplies row r of the
 // first operand and column r of the second, both at k = 8 q .. 8 q + 7 (16
@@ -18,9 +18,13 @@
 // and B rows are contiguous along that k, so every operand is one 16-byte load
 // straight from memory.
 //
-// Row tiles come from the plan (plan.hip; rows without an adapter are a group of
-// their own, copied from y), or, for up to 64 rows, from one ballot: row t
-// leads the tile of the 16 rows of its adapter that start with it.
+// Row tiles: for up to 64 rows from one ballot (row t leads the tile of the 16 rows
+// of its adapter that start with it) and expand sums the parts itself; for more,
+// 64-row tiles from the plan (plan.hip; rows without an adapter are a group of
+// their own, copied from y), and a pass between the two sums the parts and splits
+// them once (every 256 columns of expand read the parts again before: 2.4 times
+// the traffic of y itself at 2047 x 28672 x 8192, rank 32).
+//   Both are bound by HBM (x once, y once in and out, A and B).
 #include "device_common.hpp"
 #include "launch.hpp"
 
@@ -41,6 +45,7 @@ struct LoraArgs {
     const void *y;
     void *out;
     float *part;              // [slices][slots][BM][RP]
+    uint16_t *terms;          // plan form: v in bf16 terms [slots][TERMS][BM][32 RK]
     const int4 *tiles;        // plan form only
     const int32_t *order;
     int64_t ldx, ldy, ldo, k, n;
@@ -89,7 +94,8 @@ __device__ __forceinline__ bool tile_rows(const LoraArgs &p, int slot, int *rows
 template <int RT, int MT, bool PLAN>
 __global__ __launch_bounds__(64 * kLoraWaves) void lora_shrink_kernel(LoraArgs p) {
     constexpr int BM = 16 * MT, RP = 16 * RT;
-    constexpr int U = RT + MT <= 2 ? 8 : RT + MT <= 5 ? 4 : RT + MT <= 8 ? 3 : 2;
+    // steps of 32 along K per load batch; two batches are in flight
+    constexpr int U = RT + MT <= 3 ? 4 : RT + MT <= 6 ? 2 : 1;
     __shared__ int rows[BM];
     __shared__ f32x4 red[kLoraWaves][RT][64];
     int count, adapter;
@@ -120,23 +126,45 @@ __global__ __launch_bounds__(64 * kLoraWaves) void lora_shrink_kernel(LoraArgs p
     const int wpart = p.kslice / kLoraWaves;                   // a multiple of 32
     const int64_t k0 = s0 + (int64_t)wave * wpart;
     const int64_t kend = k0 + wpart < s1 ? k0 + wpart : s1;
-    int64_t kk = k0;
-    for (; kk + 32 * U <= kend; kk += 32 * U) {
-        u32x4 av[U][RT], xv[U][MT];
+    struct Batch {
+        u32x4 a[U][RT], x[U][MT];
+    };
+    auto load = [&](Batch &t, int64_t at) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
 #pragma unroll
-            for (int i = 0; i < RT; ++i) av[u][i] = *(const u32x4 *)(arow[i] + kk + 32 * u);
+            for (int i = 0; i < RT; ++i) t.a[u][i] = *(const u32x4 *)(arow[i] + at + 32 * u);
 #pragma unroll
-            for (int i = 0; i < MT; ++i) xv[u][i] = *(const u32x4 *)(xrow[i] + kk + 32 * u);
+            for (int i = 0; i < MT; ++i) t.x[u][i] = *(const u32x4 *)(xrow[i] + at + 32 * u);
         }
+    };
+    auto multiply = [&](const Batch &t) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < RT; ++i)
 #pragma unroll
-                for (int j = 0; j < MT; ++j)
-                    acc[i][j] = mfma_bf16(av[u][i], xv[u][j], acc[i][j]);
+                for (int j = 0; j < MT; ++j) acc[i][j] = mfma_bf16(t.a[u][i], t.x[u][j], acc[i][j]);
+    };
+    int64_t kk = k0;
+    if (kk + 32 * U <= kend) {
+        // two register sets in turn: one is requested before the other is used
+        Batch b0, b1;
+        load(b0, kk);
+        while (true) {
+            const bool more1 = kk + 64 * U <= kend;
+            if (more1) load(b1, kk + 32 * U);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(b0);
+            kk += 32 * U;
+            if (!more1) break;
+            const bool more0 = kk + 64 * U <= kend;
+            if (more0) load(b0, kk + 32 * U);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(b1);
+            kk += 32 * U;
+            if (!more0) break;
+        }
     }
     for (; kk < kend; kk += 32) {
         const bool in = kk + 8 * q < kend;                     // k % 8 == 0: whole vectors
@@ -179,11 +207,64 @@ __global__ __launch_bounds__(64 * kLoraWaves) void lora_shrink_kernel(LoraArgs p
     }
 }
 
+// ------------------------------------------------------------------ terms --
+// Four ranks of scale * (sum of the parts, in order) as TERMS bf16 terms.
+template <int TERMS>
+__device__ __forceinline__ void split_terms(f32x4 v, float sc, u32x2 (&t)[TERMS]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = v[e] * sc;
+#pragma unroll
+    for (int m = 0; m < TERMS; ++m) {
+        t[m] = u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+        v[0] = v[0] - __uint_as_float(t[m].x << 16);
+        v[1] = v[1] - __uint_as_float(t[m].x & 0xffff0000u);
+        v[2] = v[2] - __uint_as_float(t[m].y << 16);
+        v[3] = v[3] - __uint_as_float(t[m].y & 0xffff0000u);
+    }
+}
+
+// Eight parts' loads in flight at a time.
+__device__ __forceinline__ f32x4 sum_parts(const float *src, int slices, int64_t stride) {
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s0 = 0; s0 < slices; s0 += 8) {
+        f32x4 o[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            o[s] = *(const f32x4 *)(src + (s0 + s < slices ? s0 + s : slices - 1) * stride);
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = s0 + s < slices ? v[e] + o[s][e] : v[e];
+    }
+    return v;
+}
+
+template <int RT, bool BF16>
+__global__ __launch_bounds__(256) void lora_terms_kernel(LoraArgs p) {
+    constexpr int BM = 64, RP = 16 * RT, RK = (RT + 1) / 2, TERMS = BF16 ? 2 : 3;
+    constexpr int VEC = 8 * RK;                    // 4-rank pieces of a row
+    const int4 tile = p.tiles[blockIdx.x];
+    if (tile.z == 0 || tile.x >= p.adapters) return;
+    const float sc = p.scale ? p.scale[tile.x] : 1.0f;
+    const int64_t stride = (int64_t)p.slots * (BM * RP);
+    const int i = blockIdx.y * 256 + threadIdx.x;
+    const int t = i / VEC, c4 = (i - t * VEC) * 4;
+    if (t >= tile.z) return;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (c4 < p.rank)
+        v = sum_parts(p.part + (int64_t)blockIdx.x * (BM * RP) + t * RP + c4, p.slices, stride);
+    u32x2 w[TERMS];
+    split_terms<TERMS>(v, sc, w);
+#pragma unroll
+    for (int m = 0; m < TERMS; ++m)
+        *(u32x2 *)(p.terms + (((int64_t)blockIdx.x * TERMS + m) * BM + t) * (32 * RK) + c4) = w[m];
+}
+
 // ----------------------------------------------------------------- expand --
-// Workgroup: one row tile x 256 columns, 64 per wavefront.  The four 16-row
-// operand tiles of a wavefront take the B rows in the order that gives lane
-// (t, q) the 16 consecutive columns 16 q .. 16 q + 15 of row t: y and out move in
-// 16-byte pieces of whole cache lines.
+// Workgroup: 16 MT rows of a row tile (part blockIdx.z of the plan's) x 256
+// columns, 64 per wavefront.  The four 16-row operand tiles of a wavefront take
+// the B rows in the order that gives lane (t, q) the 16 consecutive columns 16 q
+// .. 16 q + 15 of row t: y and out move in 16-byte pieces of whole cache lines.
 constexpr int kExpandN = 64 * kLoraWaves;
 
 template <int RT, int MT, bool PLAN, bool BF16>
@@ -194,38 +275,40 @@ __global__ __launch_bounds__(64 * kLoraWaves) void lora_expand_kernel(LoraArgs p
     constexpr int VS = 32 * RK + 8;                // LDS row stride (bf16)
     constexpr int YV = BF16 ? 2 : 4;               // 16-byte pieces of 16 columns
     constexpr int PER = BF16 ? 8 : 4;              // columns of a piece
-    __shared__ int rows[BM];
-    __shared__ __attribute__((aligned(16))) uint16_t vs[TERMS][BM][VS];
-    int count, adapter;
-    if (!tile_rows<BM, PLAN>(p, blockIdx.x, rows, count, adapter)) return;
-    const bool none = adapter >= p.adapters;
-    if (none && p.y == p.out) return;              // nothing to add or move
+    __shared__ int rows[PLAN ? 1 : BM];
+    __shared__ __attribute__((aligned(16))) uint16_t vs[PLAN ? 1 : TERMS][PLAN ? 1 : BM][VS];
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int r = lane & 15, q = lane >> 4;
+    int count, adapter;
+    int row[MT];
+    if constexpr (PLAN) {
+        const int4 tile = p.tiles[blockIdx.x];
+        const int first = blockIdx.z * BM;
+        adapter = tile.x;
+        count = tile.z - first;
+        if (count <= 0) return;
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+            row[j] = p.order[tile.y + first + (16 * j + r < count ? 16 * j + r : count - 1)];
+    } else {
+        if (!tile_rows<BM, false>(p, blockIdx.x, rows, count, adapter)) return;
+#pragma unroll
+        for (int j = 0; j < MT; ++j) row[j] = rows[16 * j + r];
+    }
+    const bool none = adapter >= p.adapters;
+    if (none && p.y == p.out) return;              // nothing to add or move
     const int64_t n0 = (int64_t)blockIdx.y * kExpandN + wave * 64;
     const int64_t col = n0 + 16 * q;               // this lane's first column
     const int esize = BF16 ? 2 : 4;
 
-    // y of this lane's rows and columns, in flight while v is put together
-    u32x4 yv[MT][YV];
-#pragma unroll
-    for (int j = 0; j < MT; ++j) {
-        const int64_t base = (int64_t)rows[16 * j + r] * p.ldy;
-#pragma unroll
-        for (int c = 0; c < YV; ++c) {
-            const bool in = 16 * j + r < count && col + c * PER < p.n;
-            yv[j][c] = in ? *(const u32x4 *)((const uint8_t *)p.y + (base + col + c * PER) * esize)
-                          : u32x4{0u, 0u, 0u, 0u};
-        }
-    }
     u32x4 bv[RK][4];
     if (!none) {
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
-            const int64_t row = n0 + (r >> 2) * 16 + f * 4 + (r & 3);
+            const int64_t br = n0 + (r >> 2) * 16 + f * 4 + (r & 3);
             const uint16_t *brow =
-                p.b + ((int64_t)adapter * p.n + (row < p.n ? row : p.n - 1)) * p.rank;
+                p.b + ((int64_t)adapter * p.n + (br < p.n ? br : p.n - 1)) * p.rank;
 #pragma unroll
             for (int s = 0; s < RK; ++s) {
                 const int kk = 32 * s + 8 * q;
@@ -234,36 +317,38 @@ __global__ __launch_bounds__(64 * kLoraWaves) void lora_expand_kernel(LoraArgs p
                 bv[s][f] = in ? bv[s][f] : u32x4{0u, 0u, 0u, 0u};
             }
         }
-        // v = scale * sum of the parts, in bf16 terms; zero past the rank
-        const float sc = p.scale ? p.scale[adapter] : 1.0f;
-        const int64_t stride = (int64_t)p.slots * (BM * RP);
-        const float *part = p.part + (int64_t)blockIdx.x * (BM * RP);
-        constexpr int VEC = 32 * RK / 4;           // 4-rank pieces of a row
-        for (int i = tid; i < BM * VEC; i += 64 * kLoraWaves) {
-            const int t = i / VEC, c4 = (i - t * VEC) * 4;
-            f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (t < count && c4 < p.rank) {
-                const float *src = part + t * RP + c4;
-                for (int s = 0; s < p.slices; ++s) {
-                    const f32x4 o = *(const f32x4 *)(src + s * stride);
+    }
+    // y of this lane's rows and columns, in flight with B (and while v is put
+    // together); past the columns: the row's last piece, not stored
+    u32x4 yv[MT][YV];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = v[e] + o[e];
-                }
-            }
+    for (int j = 0; j < MT; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = v[e] * sc;
+        for (int c = 0; c < YV; ++c) {
+            const int64_t cc = col + c * PER < p.n ? col + c * PER : p.n - PER;
+            yv[j][c] = *(const u32x4 *)((const uint8_t *)p.y + ((int64_t)row[j] * p.ldy + cc) * esize);
+        }
+    if constexpr (!PLAN) {
+        if (!none) {
+            // v in bf16 terms; zero past the rank
+            const float sc = p.scale ? p.scale[adapter] : 1.0f;
+            const float *part = p.part + (int64_t)blockIdx.x * (BM * RP);
+            constexpr int VEC = 8 * RK;            // 4-rank pieces of a row
+            for (int i = tid; i < count * VEC; i += 64 * kLoraWaves) {
+                const int t = i / VEC, c4 = (i - t * VEC) * 4;
+                f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (c4 < p.rank)
+                    v = sum_parts(part + t * RP + c4, p.slices, (int64_t)p.slots * (BM * RP));
+                u32x2 w[TERMS];
+                split_terms<TERMS>(v, sc, w);
 #pragma unroll
-            for (int m = 0; m < TERMS; ++m) {
-                const u32x2 h = {bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
-                *(u32x2 *)&vs[m][t][c4] = h;
-                v[0] = v[0] - __uint_as_float(h.x << 16);
-                v[1] = v[1] - __uint_as_float(h.x & 0xffff0000u);
-                v[2] = v[2] - __uint_as_float(h.y << 16);
-                v[3] = v[3] - __uint_as_float(h.y & 0xffff0000u);
+                for (int m = 0; m < TERMS; ++m) *(u32x2 *)&vs[m][t][c4] = w[m];
             }
         }
         __syncthreads();
     }
+    const uint16_t *terms =
+        p.terms + (int64_t)blockIdx.x * (TERMS * 64 * 32 * RK) + blockIdx.z * (BM * 32 * RK);
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
         if (16 * j >= count) break;
@@ -271,18 +356,24 @@ __global__ __launch_bounds__(64 * kLoraWaves) void lora_expand_kernel(LoraArgs p
 #pragma unroll
         for (int f = 0; f < 4; ++f) acc[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if (!none) {
-            // smallest terms first
+            // smallest terms first; rows past the count are never stored, and a
+            // row of v reaches no other row of the result
+            const int t = 16 * j + r < count ? 16 * j + r : count - 1;
 #pragma unroll
             for (int m = TERMS - 1; m >= 0; --m)
 #pragma unroll
                 for (int s = 0; s < RK; ++s) {
-                    const u32x4 vt = *(const u32x4 *)&vs[m][16 * j + r][32 * s + 8 * q];
+                    u32x4 vt;
+                    if constexpr (PLAN)
+                        vt = *(const u32x4 *)(terms + (m * 64 + t) * (32 * RK) + 32 * s + 8 * q);
+                    else
+                        vt = *(const u32x4 *)&vs[m][t][32 * s + 8 * q];
 #pragma unroll
                     for (int f = 0; f < 4; ++f) acc[f] = mfma_bf16(bv[s][f], vt, acc[f]);
                 }
         }
         if (16 * j + r >= count) continue;
-        uint8_t *dst = (uint8_t *)p.out + ((int64_t)rows[16 * j + r] * p.ldo + col) * esize;
+        uint8_t *dst = (uint8_t *)p.out + ((int64_t)row[j] * p.ldo + col) * esize;
 #pragma unroll
         for (int c = 0; c < YV; ++c) {
             if (col + c * PER >= p.n) break;
@@ -314,7 +405,7 @@ struct LoraSpace {
     bool plan;
     int bm, rp, slices, kslice;
     int64_t slots;
-    size_t order, tiles, part, end;
+    size_t order, tiles, part, terms, end;
 };
 
 LoraSpace lora_space(int64_t tokens, int64_t adapters, int64_t rank, int64_t k) {
@@ -341,26 +432,37 @@ LoraSpace lora_space(int64_t tokens, int64_t adapters, int64_t rank, int64_t k) 
     s.order = take(s.plan ? (size_t)tokens * 4 : 0);
     s.tiles = take(s.plan ? (size_t)s.slots * 16 : 0);
     s.part = take((size_t)s.slices * s.slots * s.bm * s.rp * 4);
+    // up to three terms, whole steps of 32 ranks
+    s.terms = take(s.plan ? (size_t)s.slots * 3 * s.bm * (s.rp < 32 ? 32 : s.rp) * 2 : 0);
     s.end = at;
     return s;
 }
 
-template <int RT, int MT, bool PLAN>
-void launch_lora_rank(const LoraArgs &p, bool bf16, hipStream_t stream) {
+template <int RT, bool PLAN, bool BF16>
+void launch_lora_form(const LoraArgs &p, hipStream_t stream) {
     const dim3 block(64 * kLoraWaves);
-    lora_shrink_kernel<RT, MT, PLAN>
-        <<<dim3((unsigned)p.slots, (unsigned)p.slices), block, 0, stream>>>(p);
-    const dim3 grid((unsigned)p.slots, (unsigned)((p.n + kExpandN - 1) / kExpandN));
-    if (bf16) lora_expand_kernel<RT, MT, PLAN, true><<<grid, block, 0, stream>>>(p);
-    else lora_expand_kernel<RT, MT, PLAN, false><<<grid, block, 0, stream>>>(p);
+    const dim3 shrink((unsigned)p.slots, (unsigned)p.slices);
+    const unsigned cols = (unsigned)((p.n + kExpandN - 1) / kExpandN);
+    if constexpr (PLAN) {
+        lora_shrink_kernel<RT, 4, true><<<shrink, block, 0, stream>>>(p);
+        constexpr int RK = (RT + 1) / 2;
+        lora_terms_kernel<RT, BF16>
+            <<<dim3((unsigned)p.slots, 64 * 8 * RK / 256), 256, 0, stream>>>(p);
+        lora_expand_kernel<RT, 2, true, BF16>
+            <<<dim3((unsigned)p.slots, cols, 2), block, 0, stream>>>(p);
+    } else {
+        lora_shrink_kernel<RT, 1, false><<<shrink, block, 0, stream>>>(p);
+        lora_expand_kernel<RT, 1, false, BF16>
+            <<<dim3((unsigned)p.slots, cols), block, 0, stream>>>(p);
+    }
 }
 
-template <int MT, bool PLAN>
-void launch_lora_rows(const LoraArgs &p, int rp, bool bf16, hipStream_t stream) {
-    if (rp == 16) launch_lora_rank<1, MT, PLAN>(p, bf16, stream);
-    else if (rp == 32) launch_lora_rank<2, MT, PLAN>(p, bf16, stream);
-    else if (rp == 64) launch_lora_rank<4, MT, PLAN>(p, bf16, stream);
-    else launch_lora_rank<8, MT, PLAN>(p, bf16, stream);
+template <bool PLAN, bool BF16>
+void launch_lora_rank(const LoraArgs &p, int rp, hipStream_t stream) {
+    if (rp == 16) launch_lora_form<1, PLAN, BF16>(p, stream);
+    else if (rp == 32) launch_lora_form<2, PLAN, BF16>(p, stream);
+    else if (rp == 64) launch_lora_form<4, PLAN, BF16>(p, stream);
+    else launch_lora_form<8, PLAN, BF16>(p, stream);
 }
 
 }  // namespace
@@ -391,6 +493,7 @@ hipError_t launch_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, co
     p.y = y;
     p.out = out;
     p.part = (float *)(ws + s.part);
+    p.terms = (uint16_t *)(ws + s.terms);
     p.tiles = (const int4 *)(ws + s.tiles);
     p.order = (const int32_t *)(ws + s.order);
     p.ldx = ldx;
@@ -404,8 +507,10 @@ hipError_t launch_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, co
     p.slots = (int)s.slots;
     p.slices = s.slices;
     p.kslice = s.kslice;
-    if (s.plan) launch_lora_rows<4, true>(p, s.rp, bf16, stream);
-    else launch_lora_rows<1, false>(p, s.rp, bf16, stream);
+    if (s.plan && bf16) launch_lora_rank<true, true>(p, s.rp, stream);
+    else if (s.plan) launch_lora_rank<true, false>(p, s.rp, stream);
+    else if (bf16) launch_lora_rank<false, true>(p, s.rp, stream);
+    else launch_lora_rank<false, false>(p, s.rp, stream);
     return hipGetLastError();
 }
 
