@@ -491,6 +491,7 @@ w4a8_status w4a8_moe_ffn(const uint16_t *x, const int32_t *ids, const float *wei
 
 #define W4A8_LORA_RANK_MAX 128
 #define W4A8_LORA_ADAPTERS_MAX 4095
+#define W4A8_LORA_TOKENS_MAX (1 << 21)
 
 /* Bytes of workspace w4a8_lora_add needs (0 for sizes it refuses). */
 size_t w4a8_lora_workspace_bytes(int64_t tokens, int32_t adapters, int32_t rank, int64_t k);
@@ -511,8 +512,8 @@ size_t w4a8_lora_workspace_bytes(int64_t tokens, int32_t adapters, int32_t rank,
  * Requires rank, k, n > 0, rank, k, n, ldx multiples of 8, ldy and ldo multiples
  * of 8 (bf16) or 4 (binary32), ldx >= k, ldy, ldo >= n, adapters >= 1
  * (W4A8_ERR_SHAPE); rank <= W4A8_LORA_RANK_MAX, adapters <=
- * W4A8_LORA_ADAPTERS_MAX, k <= 2^30, tokens below 2^31, n below 2^24
- * (W4A8_ERR_UNSUPPORTED).  Workspace rules as for w4a8_moe_ffn.
+ * W4A8_LORA_ADAPTERS_MAX, tokens <= W4A8_LORA_TOKENS_MAX, k <= 2^30, n below 2^24
+ * and n * rank below 2^30 (W4A8_ERR_UNSUPPORTED).  Workspace rules as for w4a8_moe_ffn.
  */
 w4a8_status w4a8_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, const uint16_t *b,
                           const float *scale, const int32_t *ids, int64_t tokens,

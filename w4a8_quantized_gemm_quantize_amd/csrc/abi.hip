@@ -154,7 +154,8 @@ w4a8_status check_lora_shape(int64_t tokens, int32_t adapters, int32_t rank, int
         n % 8 != 0)
         return W4A8_ERR_SHAPE;
     if (rank > W4A8_LORA_RANK_MAX || adapters > W4A8_LORA_ADAPTERS_MAX ||
-        k > ((int64_t)1 << 30) || n >= ((int64_t)1 << 24) || tokens > INT32_MAX)
+        k > ((int64_t)1 << 30) || n >= ((int64_t)1 << 24) || n * rank >= ((int64_t)1 << 30) ||
+        tokens > W4A8_LORA_TOKENS_MAX)
         return W4A8_ERR_UNSUPPORTED;
     return W4A8_OK;
 }

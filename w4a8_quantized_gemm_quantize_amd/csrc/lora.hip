@@ -50,9 +50,19 @@ struct LoraArgs {
     const int32_t *order;
     int64_t ldx, ldy, ldo, k, n;
     int tokens, adapters, rank, slots, slices, kslice;
+    int steps;                // 256-column steps of an expand workgroup
 };
 
 constexpr int kLoraWaves = 4;
+
+// Workgroup barrier that waits for this wavefront's LDS operations only: global
+// loads stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_s_waitcnt(0xc07f);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
 
 // The rows of tile `slot`: their indices into `rows` (LDS, padded with the last
 // one), their count and adapter (>= adapters: none).  False: no rows.
@@ -223,7 +233,7 @@ __device__ __forceinline__ void split_terms(f32x4 v, float sc, u32x2 (&t)[TERMS]
     }
 }
 
-// Eight parts' loads in flight at a time.
+// Four ranks of the parts, added in order; eight parts' loads in flight at a time.
 __device__ __forceinline__ f32x4 sum_parts(const float *src, int slices, int64_t stride) {
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int s0 = 0; s0 < slices; s0 += 8) {
@@ -261,10 +271,14 @@ __global__ __launch_bounds__(256) void lora_terms_kernel(LoraArgs p) {
 }
 
 // ----------------------------------------------------------------- expand --
-// Workgroup: 16 MT rows of a row tile (part blockIdx.z of the plan's) x 256
-// columns, 64 per wavefront.  The four 16-row operand tiles of a wavefront take
-// the B rows in the order that gives lane (t, q) the 16 consecutive columns 16 q
-// .. 16 q + 15 of row t: y and out move in 16-byte pieces of whole cache lines.
+// Workgroup: 16 MT rows of a row tile (part blockIdx.z of the plan's) x `steps`
+// times 256 columns, 64 per wavefront.  The four 16-row operand tiles of a
+// wavefront take the B rows in the order that gives lane (t, q) the 16 consecutive
+// columns 16 q .. 16 q + 15 of row t: y and out move in 16-byte pieces of whole
+// cache lines.  For decode batches the time is instructions and latencies as
+// much as bytes (2.4 ns a dependent instruction), so B comes through buffer
+// loads whose bounds replace the tests of rank and columns, and addresses only
+// advance.
 constexpr int kExpandN = 64 * kLoraWaves;
 
 template <int RT, int MT, bool PLAN, bool BF16>
@@ -275,6 +289,7 @@ __global__ __launch_bounds__(64 * kLoraWaves) void lora_expand_kernel(LoraArgs p
     constexpr int VS = 32 * RK + 8;                // LDS row stride (bf16)
     constexpr int YV = BF16 ? 2 : 4;               // 16-byte pieces of 16 columns
     constexpr int PER = BF16 ? 8 : 4;              // columns of a piece
+    constexpr int ES = BF16 ? 2 : 4;
     __shared__ int rows[PLAN ? 1 : BM];
     __shared__ __attribute__((aligned(16))) uint16_t vs[PLAN ? 1 : TERMS][PLAN ? 1 : BM][VS];
     const int tid = threadIdx.x;
@@ -298,69 +313,115 @@ __global__ __launch_bounds__(64 * kLoraWaves) void lora_expand_kernel(LoraArgs p
     }
     const bool none = adapter >= p.adapters;
     if (none && p.y == p.out) return;              // nothing to add or move
-    const int64_t n0 = (int64_t)blockIdx.y * kExpandN + wave * 64;
-    const int64_t col = n0 + 16 * q;               // this lane's first column
-    const int esize = BF16 ? 2 : 4;
+    int n0 = (int)blockIdx.y * p.steps * kExpandN + wave * 64;
+    const int n = (int)p.n;
+    const int nend = n0 + p.steps * kExpandN < n ? n0 + p.steps * kExpandN : n;
+    const uint8_t *yp[MT];
+    uint8_t *op[MT];
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+        yp[j] = (const uint8_t *)p.y + ((int64_t)row[j] * p.ldy + n0 + 16 * q) * ES;
+        op[j] = (uint8_t *)p.out + ((int64_t)row[j] * p.ldo + n0 + 16 * q) * ES;
+    }
+    // y of the step's columns; in the row's last, partial step only what is there
+    u32x4 yv[MT][YV];
+    auto load_y = [&]() {
+        if (n0 + 64 <= n) {
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+#pragma unroll
+                for (int c = 0; c < YV; ++c) yv[j][c] = *(const u32x4 *)(yp[j] + c * 16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+#pragma unroll
+                for (int c = 0; c < YV; ++c)
+                    if (n0 + 16 * q + c * PER < n) yv[j][c] = *(const u32x4 *)(yp[j] + c * 16);
+        }
+    };
+    auto store = [&](int j, int c, u32x4 v) {
+        if (n0 + 64 <= n || n0 + 16 * q + c * PER < n) *(u32x4 *)(op[j] + c * 16) = v;
+    };
+    auto advance = [&]() {
+        n0 += kExpandN;
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            yp[j] += kExpandN * ES;
+            op[j] += kExpandN * ES;
+        }
+    };
+    if (none) {                                    // copied
+#pragma unroll 1
+        while (n0 < nend) {
+            load_y();
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+#pragma unroll
+                for (int c = 0; c < YV; ++c)
+                    if (16 * j + r < count) store(j, c, yv[j][c]);
+            advance();
+        }
+        return;
+    }
 
-    u32x4 bv[RK][4];
-    if (!none) {
+    // B of the adapter: rows past n and ranks past the rank read zero
+    const __amdgpu_buffer_rsrc_t rb =
+        buffer_rsrc(p.b + (int64_t)adapter * n * p.rank, (uint32_t)(n * p.rank * 2));
+    uint32_t boff[RK][4];
+#pragma unroll
+    for (int s = 0; s < RK; ++s)
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
-            const int64_t br = n0 + (r >> 2) * 16 + f * 4 + (r & 3);
-            const uint16_t *brow =
-                p.b + ((int64_t)adapter * p.n + (br < p.n ? br : p.n - 1)) * p.rank;
+            const int kk = 32 * s + 8 * q;         // rank % 8 == 0: whole vectors
+            const uint32_t o =
+                (uint32_t)((n0 + (r >> 2) * 16 + f * 4 + (r & 3)) * p.rank + kk) * 2;
+            boff[s][f] = kk < p.rank ? o : 0x80000000u;
+        }
+    const uint32_t bstep = (uint32_t)(kExpandN * p.rank * 2);
+    u32x4 bv[RK][4];
+    auto load_b = [&]() {
 #pragma unroll
-            for (int s = 0; s < RK; ++s) {
-                const int kk = 32 * s + 8 * q;
-                const bool in = kk < p.rank;       // rank % 8 == 0: whole vectors
-                bv[s][f] = *(const u32x4 *)(brow + (in ? kk : 0));
-                bv[s][f] = in ? bv[s][f] : u32x4{0u, 0u, 0u, 0u};
+        for (int s = 0; s < RK; ++s)
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                bv[s][f] = buffer_load16(rb, (int)boff[s][f], 0);
+                boff[s][f] += bstep;
             }
-        }
-    }
-    // y of this lane's rows and columns, in flight with B (and while v is put
-    // together); past the columns: the row's last piece, not stored
-    u32x4 yv[MT][YV];
-#pragma unroll
-    for (int j = 0; j < MT; ++j)
-#pragma unroll
-        for (int c = 0; c < YV; ++c) {
-            const int64_t cc = col + c * PER < p.n ? col + c * PER : p.n - PER;
-            yv[j][c] = *(const u32x4 *)((const uint8_t *)p.y + ((int64_t)row[j] * p.ldy + cc) * esize);
-        }
+    };
+    load_b();
+    load_y();
     if constexpr (!PLAN) {
-        if (!none) {
-            // v in bf16 terms; zero past the rank
-            const float sc = p.scale ? p.scale[adapter] : 1.0f;
-            const float *part = p.part + (int64_t)blockIdx.x * (BM * RP);
-            constexpr int VEC = 8 * RK;            // 4-rank pieces of a row
-            for (int i = tid; i < count * VEC; i += 64 * kLoraWaves) {
-                const int t = i / VEC, c4 = (i - t * VEC) * 4;
-                f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (c4 < p.rank)
-                    v = sum_parts(part + t * RP + c4, p.slices, (int64_t)p.slots * (BM * RP));
-                u32x2 w[TERMS];
-                split_terms<TERMS>(v, sc, w);
+        // v in bf16 terms; zero past the rank
+        const float sc = p.scale ? p.scale[adapter] : 1.0f;
+        const float *part = p.part + (int64_t)blockIdx.x * (BM * RP);
+        constexpr int VEC = 8 * RK;                // 4-rank pieces of a row
+        for (int i = tid; i < count * VEC; i += 64 * kLoraWaves) {
+            const int t = i / VEC, c4 = (i - t * VEC) * 4;
+            f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (c4 < p.rank)
+                v = sum_parts(part + t * RP + c4, p.slices, (int64_t)p.slots * (BM * RP));
+            u32x2 w[TERMS];
+            split_terms<TERMS>(v, sc, w);
 #pragma unroll
-                for (int m = 0; m < TERMS; ++m) *(u32x2 *)&vs[m][t][c4] = w[m];
-            }
+            for (int m = 0; m < TERMS; ++m) *(u32x2 *)&vs[m][t][c4] = w[m];
         }
-        __syncthreads();
+        lds_barrier();                             // B and y stay in flight
     }
     const uint16_t *terms =
         p.terms + (int64_t)blockIdx.x * (TERMS * 64 * 32 * RK) + blockIdx.z * (BM * 32 * RK);
+#pragma unroll 1
+    while (true) {
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-        if (16 * j >= count) break;
-        f32x4 acc[4];
+        for (int j = 0; j < MT; ++j) {
+            if (16 * j >= count) break;
+            f32x4 acc[4];
 #pragma unroll
-        for (int f = 0; f < 4; ++f) acc[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (!none) {
-            // smallest terms first; rows past the count are never stored, and a
-            // row of v reaches no other row of the result
+            for (int f = 0; f < 4; ++f) acc[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            // rows past the count are never stored, and a row of v reaches no
+            // other row of the result
             const int t = 16 * j + r < count ? 16 * j + r : count - 1;
 #pragma unroll
-            for (int m = TERMS - 1; m >= 0; --m)
+            for (int m = TERMS - 1; m >= 0; --m)   // smallest terms first
 #pragma unroll
                 for (int s = 0; s < RK; ++s) {
                     u32x4 vt;
@@ -371,14 +432,10 @@ __global__ __launch_bounds__(64 * kLoraWaves) void lora_expand_kernel(LoraArgs p
 #pragma unroll
                     for (int f = 0; f < 4; ++f) acc[f] = mfma_bf16(bv[s][f], vt, acc[f]);
                 }
-        }
-        if (16 * j + r >= count) continue;
-        uint8_t *dst = (uint8_t *)p.out + ((int64_t)row[j] * p.ldo + col) * esize;
+            if (16 * j + r >= count) continue;
 #pragma unroll
-        for (int c = 0; c < YV; ++c) {
-            if (col + c * PER >= p.n) break;
-            u32x4 o = yv[j][c];
-            if (!none) {
+            for (int c = 0; c < YV; ++c) {
+                u32x4 o = yv[j][c];
                 if constexpr (BF16) {
                     float f[8];
                     bf16x8_to_f32(o, f);
@@ -392,9 +449,14 @@ __global__ __launch_bounds__(64 * kLoraWaves) void lora_expand_kernel(LoraArgs p
                     for (int e = 0; e < 4; ++e) f[e] = f[e] + acc[c][e];
                     o = __builtin_bit_cast(u32x4, f);
                 }
+                store(j, c, o);
             }
-            *(u32x4 *)(dst + c * 16) = o;
         }
+        // out may be y: no two steps share a column
+        advance();
+        if (n0 >= nend) break;
+        load_b();
+        load_y();
     }
 }
 
@@ -442,7 +504,8 @@ template <int RT, bool PLAN, bool BF16>
 void launch_lora_form(const LoraArgs &p, hipStream_t stream) {
     const dim3 block(64 * kLoraWaves);
     const dim3 shrink((unsigned)p.slots, (unsigned)p.slices);
-    const unsigned cols = (unsigned)((p.n + kExpandN - 1) / kExpandN);
+    const unsigned step_cols = (unsigned)(p.steps * kExpandN);
+    const unsigned cols = (unsigned)((p.n + step_cols - 1) / step_cols);
     if constexpr (PLAN) {
         lora_shrink_kernel<RT, 4, true><<<shrink, block, 0, stream>>>(p);
         constexpr int RK = (RT + 1) / 2;
@@ -507,6 +570,10 @@ hipError_t launch_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, co
     p.slots = (int)s.slots;
     p.slices = s.slices;
     p.kslice = s.kslice;
+    // column steps of an expand workgroup: about 1024 workgroups
+    const int64_t tiles = s.plan ? 2 * s.slots : s.slots;
+    const int64_t steps = s.plan ? 1 : tiles * ((n + kExpandN - 1) / kExpandN) / 1024;
+    p.steps = (int)(steps < 1 ? 1 : steps > 8 ? 8 : steps);
     if (s.plan && bf16) launch_lora_rank<true, true>(p, s.rp, stream);
     else if (s.plan) launch_lora_rank<true, false>(p, s.rp, stream);
     else if (bf16) launch_lora_rank<false, true>(p, s.rp, stream);
