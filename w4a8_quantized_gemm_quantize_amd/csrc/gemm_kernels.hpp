@@ -147,7 +147,7 @@ __device__ __forceinline__ u32x4 buffer_load16_nt(__amdgpu_buffer_rsrc_t r, int 
 // into LDS, a wavefront per row (act_scale_pair_rcp).
 enum Sel : int { kSelNone = 0, kSelGateUp = 1, kSelScatter = 2, kSelDirect = 3 };
 struct SelArgs {
-    const int4 *tiles;       // [slots] {expert, first sorted row, rows, 0}
+    const int4 *tiles;       // [slots + 1] {expert, first sorted row, rows, 0}, last: {in use, ..}
     const int32_t *map;      // src (kSelGateUp) or dst (kSelScatter) of a sorted row, or the ids
     uint32_t a_bytes;        // bytes of A (kSelGateUp: gathered through 32-bit offsets)
     int32_t slots;           // entries of the table; kSelDirect: rows of a token
@@ -843,11 +843,21 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, AB == 64 || AB == 128 ? 2 :
     // each XCD gets a contiguous slice of a grouped traversal (4 row tiles per
     // group) and the workgroups sharing an L2 share activation rows and weights.
     static_assert(SEL == kSelNone || AB == 0, "rows that choose weights: per-token scales");
-    const int64_t mtiles = SEL != kSelNone ? sel.slots : (m + BM - 1) / BM;
+    const int64_t mtiles =
+        SEL != kSelNone ? sel.tiles[sel.slots].x : (m + BM - 1) / BM;
     const int64_t ntb = (n + BN - 1) / BN;
     const int64_t nwg = mtiles * ntb;
     int64_t id = blockIdx.x;
-    if ((nwg & 7) == 0) id = (id & 7) * (nwg >> 3) + (id >> 3);
+    if constexpr (SEL != kSelNone) {
+        // The grid covers the most tiles there can be; the slices are of those in
+        // use, or the last XCD would get the unused ones.
+        const int64_t per = (nwg + 7) >> 3;
+        if ((id >> 3) >= per) return;
+        id = (id & 7) * per + (id >> 3);
+        if (id >= nwg) return;
+    } else if ((nwg & 7) == 0) {
+        id = (id & 7) * (nwg >> 3) + (id >> 3);
+    }
     constexpr int64_t GM = 4;
     const int64_t group = id / (GM * ntb);
     const int64_t first_m = group * GM;
@@ -861,7 +871,6 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, AB == 64 || AB == 128 ? 2 :
     const int64_t ntiles = n / kNTile;
     if constexpr (SEL != kSelNone) {
         const int4 tile = sel.tiles[first_m + within % gsize];
-        if (tile.z == 0) return;
         m0 = tile.y;
         m = m0 + tile.z;
         w_packed += (int64_t)tile.x * (n * k / 2);
@@ -921,13 +930,14 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, AB == 64 || AB == 128 ? 2 :
         if constexpr (SEL == kSelGateUp) {
             // row scales gathered, four bytes a lane; channel scales: the gate's
             // BN / 2, then the up projection's (past the end: zero, not stored)
-            static_assert(BM % 64 == 0 && BM / 64 < WAVES && BN <= 256, "scale blocks");
-            if (wave < BM / 64) {
+            constexpr int kRowBlocks = (BM + 63) / 64;
+            static_assert(kRowBlocks < WAVES && BN <= 256, "scale blocks");
+            if (wave < kRowBlocks) {
                 const int r = wave * 64 + lane;
                 const int64_t row = m0 + (r < rows_here ? r : rows_here - 1);
                 const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(a_scale, 0xffffffffu);
                 buffer_to_lds4(rs, scl_a + wave * 256, sel.map[row] * 4, 0);
-            } else if (wave == BM / 64) {
+            } else if (wave == kRowBlocks) {
                 const int64_t h0 = t0 * kNTile;
                 const __amdgpu_buffer_rsrc_t rs =
                     buffer_rsrc(ch_scale + h0, (uint32_t)(2 * sel.inter - h0) * 4);
@@ -1110,7 +1120,11 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, AB == 64 || AB == 128 ? 2 :
     // fragment: lane (c, kq) reads row c of the row tile at 16-byte column
     // 4 h + kq; weight fragments are stored in operand order.
     const int kq = lane >> 4;
+    // SEL: tiles are often not full (an expert's last rows): a wavefront whose rows
+    // are all past the tile's has nothing to multiply
+    const bool any_row = SEL == kSelNone || WAVES_M == 1 || wm * WM < rows_here;
     auto mma_step = [&](auto buf_tag, int h) {
+        if (SEL != kSelNone && WAVES_M > 1 && !any_row) return;
         const uint8_t *abase = act_of(buf_tag);
         const uint8_t *wbase = decltype(buf_tag)::value ? wl1 : wl0;
         v4i av[TM], wv[TN];
@@ -1248,10 +1262,20 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, AB == 64 || AB == 128 ? 2 :
     }
     auto iteration = [&](int j, auto cur, auto nxt) {
         __builtin_amdgcn_s_setprio(2);
+        // SEL: the experts' weights and rows do not stay in the caches between
+        // layers, and the activation loads have longer to wait for; they go out
+        // first (down product of 8192 rows of 14336: 527 -> 514 us)
+        if constexpr (SEL != kSelNone) {
+            if (j + 1 < nfull) issue_act(j + 1, nxt, full_chunk);
+            else if (j + 1 < nchunks) issue_act(j + 1, nxt, half_chunk);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         mma_step(cur, 0);
         __builtin_amdgcn_sched_barrier(0);
-        if (j + 1 < nfull) issue_act(j + 1, nxt, full_chunk);
-        else if (j + 1 < nchunks) issue_act(j + 1, nxt, half_chunk);
+        if constexpr (SEL == kSelNone) {
+            if (j + 1 < nfull) issue_act(j + 1, nxt, full_chunk);
+            else if (j + 1 < nchunks) issue_act(j + 1, nxt, half_chunk);
+        }
         fetch_w(j + 2, cur, general);
         if constexpr (AB > 0)
             if (j + 1 < nchunks) fetch_s(j + 1, snxt);

@@ -96,7 +96,8 @@ hipError_t launch_route(const void *logits, bool bf16, int64_t ld, const float *
 
 // Rows sorted by the group they choose, in tiles of bm rows (plan.hip): order
 // [rows] the row of each sorted position, src (may be null) order / top_k,
-// tiles [plan_slots] x 4 int32 {group, first sorted row, rows, 0}.
+// tiles [plan_slots + 1] x 4 int32 {group, first sorted row, rows, 0}; the last
+// entry holds {entries in use, rows in use, 0, 0}.
 constexpr int kPlanMaxGroups = 4096;
 int64_t plan_slots(int64_t rows, int64_t groups, int bm);
 hipError_t launch_plan(const int32_t *ids, int64_t rows, int32_t groups, bool none_last,
@@ -104,10 +105,11 @@ hipError_t launch_plan(const int32_t *ids, int64_t rows, int32_t groups, bool no
                        hipStream_t stream);
 
 // The plan (ids outside the groups take no part) and the per-row codes and scales of
-// x [xrows, cols] (launch_quantize_rows) in one launch.
+// x [xrows, cols] (launch_quantize_rows) in one launch; bm2 > 0: also a table of
+// tiles of bm2 rows, in tiles2.
 hipError_t launch_plan_quantize(const int32_t *ids, int64_t rows, int32_t groups, int32_t top_k,
-                                int bm, int32_t *order, int32_t *src, int32_t *tiles,
-                                const uint16_t *x, int64_t xrows, int64_t cols, int8_t *q,
+                                int bm, int bm2, int32_t *order, int32_t *src, int32_t *tiles,
+                                int32_t *tiles2, const uint16_t *x, int64_t xrows, int64_t cols, int8_t *q,
                                 float *scales, hipStream_t stream);
 
 // Experts' products (experts.hip), arguments as w4a8_moe_ffn in w4a8.h.

@@ -492,7 +492,7 @@ LoraSpace lora_space(int64_t tokens, int64_t adapters, int64_t rank, int64_t k) 
         return here;
     };
     s.order = take(s.plan ? (size_t)tokens * 4 : 0);
-    s.tiles = take(s.plan ? (size_t)s.slots * 16 : 0);
+    s.tiles = take(s.plan ? (size_t)(s.slots + 1) * 16 : 0);
     s.part = take((size_t)s.slices * s.slots * s.bm * s.rp * 4);
     // up to three terms, whole steps of 32 ranks
     s.terms = take(s.plan ? (size_t)s.slots * 3 * s.bm * (s.rp < 32 ? 32 : s.rp) * 2 : 0);

@@ -8,16 +8,14 @@ namespace w4a8 {
 namespace {
 
 // Workgroup g (0 .. groups) finds on its own what group g needs: how many rows
-// go to lower groups (its first sorted row), which lower groups have any (its
-// first tile) and its own rows in order (a stable sort: the result does not
-// depend on timing).  Two passes over the ids from L2 with ballots and
-// popcounts; no atomics on global memory and no second launch.
-//   Tiles: group g starts at entry rows_before / bm + groups_with_rows_before.
-// Since floor(a + b) >= floor(a) + ceil(b) - 1, the next group with rows starts
-// at or after the end of g's ceil(rows / bm) tiles, and at most one entry
-// between them stays unused (0 rows).  Workgroup `groups` clears the rest of
-// the table.  So rows / bm + min(groups, rows) entries are enough, a count the
-// host has without the ids.
+// each lower group has, so its first sorted row and its first tile, and its own
+// rows in order (a stable sort: the result does not depend on timing).  Two passes
+// over the ids from L2, counts of the lower groups in LDS, its own by ballots;
+// no atomics on global memory and no second launch.  Workgroup `groups` clears the
+// rest of the table and writes the entries and rows in use past its end.  rows /
+// bm + min(groups, rows) entries are always enough, a count the host has without
+// the ids.
+//   A second table with tiles of another size may be written along.
 //   none_last: ids outside [0, groups - 1) make up group groups - 1; else ids
 // outside [0, groups) take no part.
 //   Bound by the latency of the id loads: each wavefront requests kIdBatch of
@@ -28,8 +26,9 @@ constexpr int kIdBatch = 8;
 struct PlanArgs {
     const int32_t *ids;
     int32_t *order, *src;
-    int4 *tiles;
-    int rows, groups, none_last, top_k, bm, slots;
+    int4 *tiles[2];
+    int bm[2], slots[2];      // bm[1] == 0: one table
+    int rows, groups, none_last, top_k;
 };
 
 __device__ __forceinline__ int plan_group(int id, int groups, int none_last) {
@@ -38,12 +37,12 @@ __device__ __forceinline__ int plan_group(int id, int groups, int none_last) {
 }
 
 __device__ __forceinline__ void plan_block(const PlanArgs &p, int g) {
-    __shared__ uint32_t seen[kPlanMaxGroups / 32];
-    __shared__ int lt_of[kPlanThreads / 64], eq_of[kPlanThreads / 64];
+    __shared__ int count[kPlanMaxGroups];
+    __shared__ int eq_of[kPlanThreads / 64];
+    __shared__ int sums[kPlanThreads / 64][3];
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int waves = blockDim.x >> 6;
-    const int words = (p.groups + 31) >> 5;
     // a contiguous run of whole 64-row chunks per wavefront
     const int chunks = (p.rows + 63) >> 6;
     const int per = (chunks + waves - 1) / waves;
@@ -62,47 +61,58 @@ __device__ __forceinline__ void plan_block(const PlanArgs &p, int g) {
         }
     };
     load(c0);
-    for (int w = tid; w < words; w += blockDim.x) seen[w] = 0u;
+    for (int w = tid; w < g; w += blockDim.x) count[w] = 0;
     __syncthreads();
-    int lt = 0, eq = 0;
+    int eq = 0;
     for (int c = c0; c < c1; c += kIdBatch) {
         if (c > c0) load(c);
 #pragma unroll
         for (int u = 0; u < kIdBatch; ++u) {
-            const bool low = id[u] >= 0 && id[u] < g;
-            lt += __popcll(__ballot(low));
+            if (id[u] >= 0 && id[u] < g) atomicAdd(&count[id[u]], 1);
             eq += __popcll(__ballot(id[u] == g));
-            if (low) {
-                const uint32_t bit = 1u << (id[u] & 31);
-                if (!(((volatile uint32_t *)seen)[id[u] >> 5] & bit))
-                    atomicOr(&seen[id[u] >> 5], bit);
+        }
+    }
+    if (lane == 0) eq_of[wave] = eq;
+    __syncthreads();
+    // rows and tiles of the lower groups
+    int part[3] = {0, 0, 0};
+    for (int w = tid; w < g; w += blockDim.x) {
+        const int c = count[w];
+        part[0] += c;
+        part[1] += (c + p.bm[0] - 1) / p.bm[0];
+        if (p.bm[1]) part[2] += (c + p.bm[1] - 1) / p.bm[1];
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        for (int off = 1; off < 64; off <<= 1) part[i] += __shfl_xor(part[i], off);
+        if (lane == 0) sums[wave][i] = part[i];
+    }
+    __syncthreads();
+    int before = 0, mine = 0, base = 0;
+    int first[2] = {0, 0};
+    for (int w = 0; w < waves; ++w) {
+        if (w == wave) base = mine;
+        mine += eq_of[w];
+        before += sums[w][0];
+        first[0] += sums[w][1];
+        first[1] += sums[w][2];
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int bm = p.bm[t];
+        if (bm == 0) continue;
+        if (g == p.groups) {
+            for (int s = first[t] + tid; s < p.slots[t]; s += blockDim.x)
+                p.tiles[t][s] = int4{0, 0, 0, 0};
+            if (tid == 0) p.tiles[t][p.slots[t]] = int4{first[t], before, 0, 0};
+        } else {
+            for (int s = tid; s * bm < mine; s += blockDim.x) {
+                const int left = mine - s * bm;
+                p.tiles[t][first[t] + s] = int4{g, before + s * bm, left < bm ? left : bm, 0};
             }
         }
     }
-    if (lane == 0) {
-        lt_of[wave] = lt;
-        eq_of[wave] = eq;
-    }
-    __syncthreads();
-    int before = 0, mine = 0, base = 0, active = 0;
-    for (int w = 0; w < waves; ++w) {
-        if (w == wave) base = mine;
-        before += lt_of[w];
-        mine += eq_of[w];
-    }
-    for (int w = 0; w < words; ++w) active += __popc(seen[w]);
-    const int slot0 = before / p.bm + active;
-    if (g == p.groups) {
-        for (int s = slot0 + tid; s < p.slots; s += blockDim.x) p.tiles[s] = int4{0, 0, 0, 0};
-        return;
-    }
-    if (mine == 0) return;
-    const int slot1 = (before + mine) / p.bm + active + 1;
-    for (int s = tid; s < slot1 - slot0; s += blockDim.x) {
-        const int left = mine - s * p.bm;
-        p.tiles[slot0 + s] = left > 0 ? int4{g, before + s * p.bm, left < p.bm ? left : p.bm, 0}
-                                      : int4{0, 0, 0, 0};
-    }
+    if (g == p.groups || mine == 0) return;
     int at = before + base;
     for (int c = c0; c < c1; c += kIdBatch) {
         // one batch holds a short run whole: its ids are still in registers
@@ -184,8 +194,18 @@ __global__ __launch_bounds__(kPlanThreads) void plan_quantize_kernel(
 
 PlanArgs plan_args(const int32_t *ids, int64_t rows, int32_t groups, bool none_last,
                    int32_t top_k, int bm, int32_t *order, int32_t *src, int32_t *tiles) {
-    return PlanArgs{ids, order, src, (int4 *)tiles, (int)rows, groups, none_last, top_k, bm,
-                    (int)plan_slots(rows, groups, bm)};
+    PlanArgs p{};
+    p.ids = ids;
+    p.order = order;
+    p.src = src;
+    p.tiles[0] = (int4 *)tiles;
+    p.bm[0] = bm;
+    p.slots[0] = (int)plan_slots(rows, groups, bm);
+    p.rows = (int)rows;
+    p.groups = groups;
+    p.none_last = none_last;
+    p.top_k = top_k;
+    return p;
 }
 
 // 16 wavefronts once each has a few chunks to read
@@ -206,10 +226,15 @@ hipError_t launch_plan(const int32_t *ids, int64_t rows, int32_t groups, bool no
 }
 
 hipError_t launch_plan_quantize(const int32_t *ids, int64_t rows, int32_t groups, int32_t top_k,
-                                int bm, int32_t *order, int32_t *src, int32_t *tiles,
-                                const uint16_t *x, int64_t xrows, int64_t cols, int8_t *q,
+                                int bm, int bm2, int32_t *order, int32_t *src, int32_t *tiles,
+                                int32_t *tiles2, const uint16_t *x, int64_t xrows, int64_t cols, int8_t *q,
                                 float *scales, hipStream_t stream) {
-    const PlanArgs p = plan_args(ids, rows, groups, false, top_k, bm, order, src, tiles);
+    PlanArgs p = plan_args(ids, rows, groups, false, top_k, bm, order, src, tiles);
+    if (bm2) {
+        p.tiles[1] = (int4 *)tiles2;
+        p.bm[1] = bm2;
+        p.slots[1] = (int)plan_slots(rows, groups, bm2);
+    }
     const int threads = plan_threads(rows);
     const int64_t per = threads / 64;
     const unsigned grid = (unsigned)(groups + 1 + (xrows + per - 1) / per);
