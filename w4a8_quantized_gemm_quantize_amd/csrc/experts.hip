@@ -301,42 +301,24 @@ __global__ __launch_bounds__(64 * kTokenWaves) void token_down_kernel(
     }
 }
 
-// The tiled products.  Up to 64 rows an expert: 64 x 128 tiles of four wavefronts
-// (64 x 256 of eight: 43.4, 27.7 us where these take 42.8, 26.4).  More: 256 x 256
-// or 128 x 256 tiles (tables for both), whichever takes less by rounds of the CUs,
-// with the expected tiles: rows / block and half a tile of each expert.  A round
-// of 256-row tiles costs 1.75 of the others in the gate-up product, 1.625 in the
-// down product.  Measured (gate-up, down; 256 | 128): 8192 rows of 4096 x 14336
-// over 8 experts 1080, 530 | 1195, 535 us (16, 3 | 30, 5 rounds); 16384 rows of 4096 x
-// 1408 over 32 experts 280, 152 | 250, 165 us (4, 5 | 7, 9 rounds).
+// The tiled products: 64 x 128 tiles of four wavefronts or 256 x 256 tiles.
 template <int SEL>
-void launch_sel(const Product &p, int bm, const int4 *tiles2, int64_t slots2, hipStream_t stream) {
-    if (bm <= 64) {
-        launch_sel_tiled<64, 128, 1, 4, SEL>(p, stream);
-        return;
-    }
-    const int64_t ncu = device_cu_count();
-    const int64_t nb = (p.n + 255) / 256;
-    const int64_t some = (p.sel.experts + 1) / 2;
-    auto rounds = [&](int64_t tiles) { return (tiles * nb + ncu - 1) / ncu; };
-    const int64_t large = rounds(p.rows / 256 + some) * (SEL == kSelGateUp ? 14 : 13);
-    const int64_t small = rounds(p.rows / 128 + some) * 8;
-    if (large < small) {
-        launch_sel_tiled<256, 256, 4, 4, SEL>(p, stream);
-    } else {
-        Product q = p;
-        q.sel.tiles = tiles2;
-        q.sel.slots = (int32_t)slots2;
-        launch_sel_tiled<128, 256, 1, 8, SEL>(q, stream);
-    }
+void launch_sel(const Product &p, int bm, hipStream_t stream) {
+    if (bm <= 64) launch_sel_tiled<64, 128, 1, 4, SEL>(p, stream);
+    else launch_sel_tiled<256, 256, 4, 4, SEL>(p, stream);
 }
 
 // Row block of the products for `rows` rows over `experts` experts, by the rows
-// an expert has on average.
+// an expert has on average.  Measured on one box, gate-up + down, us, for blocks of
+// 64 | 128 (128 x 256 tiles) | 256:
+//   4096 x 1408, 32 experts: 65 rows an expert 107 | 121 | 151, 160 rows 179 | 186 |
+//   189, 256 rows 252 | 256 | 246, 375 rows 362 | 305 | 290, 512 rows 482 | 425 | 375;
+//   2048 x 1024, 64 experts: 131 rows 124 | 147 | 164, 253 rows 202 | 194 | 179;
+//   4096 x 14336, 8 experts: 1024 rows 2124 | 1683 | 1524.
 int row_block(int64_t rows, int64_t experts) {
     const int64_t met = rows < experts ? rows : experts;
     const int64_t avg = rows / met;
-    return avg <= 4 ? 8 : avg <= 16 ? 16 : avg <= 64 ? 64 : 256;
+    return avg <= 4 ? 8 : avg <= 16 ? 16 : avg <= 200 ? 64 : 256;
 }
 
 // Whether a batch is taken row by row (kSelDirect, two launches) rather than
@@ -358,12 +340,12 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 enum MoeForm { kMoeDirect, kMoeFew, kMoeTiled };
 
 struct MoeSpace {
-    size_t xq, xs, order, src, tiles, tiles2, h, hq, hs, y, end;
+    size_t xq, xs, order, src, tiles, h, hq, hs, y, end;
     MoeForm form;
     int bm;
     int y_dtype;              // 0 binary32, 1 bf16
     bool fused_down;          // kMoeFew: the down product takes its rows' codes itself
-    int64_t slots, slots2;    // entries of the tables; the second of 128-row tiles with bm 256
+    int64_t slots;
 };
 
 MoeSpace moe_space(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inter,
@@ -377,7 +359,6 @@ MoeSpace moe_space(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidde
                                                                    : kMoeTiled;
     s.fused_down = s.form == kMoeFew && inter <= kFusedRowMax && s.bm * (inter + 16) <= 34 * 1024;
     s.slots = plan_slots((int64_t)r, experts, s.bm);
-    s.slots2 = s.bm == 256 ? plan_slots((int64_t)r, experts, 128) : 0;
     s.y_dtype = s.form == kMoeTiled ? out_dtype : 0;
     size_t at = 0;
     auto take = [&](bool used, size_t bytes) {
@@ -391,7 +372,6 @@ MoeSpace moe_space(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidde
     s.order = take(sorted, r * 4);
     s.src = take(sorted, r * 4);
     s.tiles = take(sorted, (size_t)(s.slots + 1) * 16);
-    s.tiles2 = take(s.slots2 > 0, (size_t)(s.slots2 + 1) * 16);
     s.h = take(true, r * inter * 2);
     s.hq = take(sorted && !s.fused_down, r * inter);
     s.hs = take(sorted && !s.fused_down, r * 4);
@@ -442,15 +422,14 @@ hipError_t launch_moe_ffn(const uint16_t *x, const int32_t *ids, const float *we
             (int)inter, parts, part_bytes, out, out_dtype == 1);
         return hipGetLastError();
     }
-    hipError_t err = launch_plan_quantize(ids, rows, experts, top_k, s.bm, s.slots2 ? 128 : 0,
-                                          order, src, (int32_t *)(ws + s.tiles),
-                                          (int32_t *)(ws + s.tiles2), x, tokens, hidden,
+    hipError_t err = launch_plan_quantize(ids, rows, experts, top_k, s.bm, order, src,
+                                          (int32_t *)(ws + s.tiles), x, tokens, hidden,
                                           (int8_t *)(ws + s.xq), (float *)(ws + s.xs), stream);
     if (err != hipSuccess) return err;
     p.sel = SelArgs{(const int4 *)(ws + s.tiles), src, (uint32_t)(tokens * hidden),
                     (int32_t)s.slots, experts, inter};
     if (s.form == kMoeFew) launch_sel_skinny<kSelGateUp, false, 1>(p, s.bm, stream);
-    else launch_sel<kSelGateUp>(p, s.bm, (const int4 *)(ws + s.tiles2), s.slots2, stream);
+    else launch_sel<kSelGateUp>(p, s.bm, stream);
     p.a_q = ws + s.h;
     if (!s.fused_down) {
         err = launch_quantize_rows((const uint16_t *)(ws + s.h), rows, inter,
@@ -470,7 +449,7 @@ hipError_t launch_moe_ffn(const uint16_t *x, const int32_t *ids, const float *we
     p.sel.map = order;
     if (s.fused_down) launch_sel_fused<kSelScatter>(p, s.bm, stream);
     else if (s.form == kMoeFew) launch_sel_skinny<kSelScatter, false, 1>(p, s.bm, stream);
-    else launch_sel<kSelScatter>(p, s.bm, (const int4 *)(ws + s.tiles2), s.slots2, stream);
+    else launch_sel<kSelScatter>(p, s.bm, stream);
     const int64_t gy = tokens < 32768 ? tokens : 32768;
     const dim3 grid((unsigned)((hidden / 8 + 255) / 256), (unsigned)gy,
                     (unsigned)((tokens + gy - 1) / gy));

@@ -105,11 +105,10 @@ hipError_t launch_plan(const int32_t *ids, int64_t rows, int32_t groups, bool no
                        hipStream_t stream);
 
 // The plan (ids outside the groups take no part) and the per-row codes and scales of
-// x [xrows, cols] (launch_quantize_rows) in one launch; bm2 > 0: also a table of
-// tiles of bm2 rows, in tiles2.
+// x [xrows, cols] (launch_quantize_rows) in one launch.
 hipError_t launch_plan_quantize(const int32_t *ids, int64_t rows, int32_t groups, int32_t top_k,
-                                int bm, int bm2, int32_t *order, int32_t *src, int32_t *tiles,
-                                int32_t *tiles2, const uint16_t *x, int64_t xrows, int64_t cols, int8_t *q,
+                                int bm, int32_t *order, int32_t *src, int32_t *tiles,
+                                const uint16_t *x, int64_t xrows, int64_t cols, int8_t *q,
                                 float *scales, hipStream_t stream);
 
 // Experts' products (experts.hip), arguments as w4a8_moe_ffn in w4a8.h.

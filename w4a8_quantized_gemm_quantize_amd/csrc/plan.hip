@@ -15,7 +15,6 @@ namespace {
 // rest of the table and writes the entries and rows in use past its end.  rows /
 // bm + min(groups, rows) entries are always enough, a count the host has without
 // the ids.
-//   A second table with tiles of another size may be written along.
 //   none_last: ids outside [0, groups - 1) make up group groups - 1; else ids
 // outside [0, groups) take no part.
 //   Bound by the latency of the id loads: each wavefront requests kIdBatch of
@@ -26,9 +25,8 @@ constexpr int kIdBatch = 8;
 struct PlanArgs {
     const int32_t *ids;
     int32_t *order, *src;
-    int4 *tiles[2];
-    int bm[2], slots[2];      // bm[1] == 0: one table
-    int rows, groups, none_last, top_k;
+    int4 *tiles;
+    int rows, groups, none_last, top_k, bm, slots;
 };
 
 __device__ __forceinline__ int plan_group(int id, int groups, int none_last) {
@@ -39,7 +37,7 @@ __device__ __forceinline__ int plan_group(int id, int groups, int none_last) {
 __device__ __forceinline__ void plan_block(const PlanArgs &p, int g) {
     __shared__ int count[kPlanMaxGroups];
     __shared__ int eq_of[kPlanThreads / 64];
-    __shared__ int sums[kPlanThreads / 64][3];
+    __shared__ int sums[kPlanThreads / 64][2];
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int waves = blockDim.x >> 6;
@@ -75,44 +73,34 @@ __device__ __forceinline__ void plan_block(const PlanArgs &p, int g) {
     if (lane == 0) eq_of[wave] = eq;
     __syncthreads();
     // rows and tiles of the lower groups
-    int part[3] = {0, 0, 0};
+    int part[2] = {0, 0};
     for (int w = tid; w < g; w += blockDim.x) {
-        const int c = count[w];
-        part[0] += c;
-        part[1] += (c + p.bm[0] - 1) / p.bm[0];
-        if (p.bm[1]) part[2] += (c + p.bm[1] - 1) / p.bm[1];
+        part[0] += count[w];
+        part[1] += (count[w] + p.bm - 1) / p.bm;
     }
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 2; ++i) {
         for (int off = 1; off < 64; off <<= 1) part[i] += __shfl_xor(part[i], off);
         if (lane == 0) sums[wave][i] = part[i];
     }
     __syncthreads();
-    int before = 0, mine = 0, base = 0;
-    int first[2] = {0, 0};
+    int before = 0, mine = 0, base = 0, first = 0;
     for (int w = 0; w < waves; ++w) {
         if (w == wave) base = mine;
         mine += eq_of[w];
         before += sums[w][0];
-        first[0] += sums[w][1];
-        first[1] += sums[w][2];
+        first += sums[w][1];
     }
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int bm = p.bm[t];
-        if (bm == 0) continue;
-        if (g == p.groups) {
-            for (int s = first[t] + tid; s < p.slots[t]; s += blockDim.x)
-                p.tiles[t][s] = int4{0, 0, 0, 0};
-            if (tid == 0) p.tiles[t][p.slots[t]] = int4{first[t], before, 0, 0};
-        } else {
-            for (int s = tid; s * bm < mine; s += blockDim.x) {
-                const int left = mine - s * bm;
-                p.tiles[t][first[t] + s] = int4{g, before + s * bm, left < bm ? left : bm, 0};
-            }
-        }
+    if (g == p.groups) {
+        for (int s = first + tid; s < p.slots; s += blockDim.x) p.tiles[s] = int4{0, 0, 0, 0};
+        if (tid == 0) p.tiles[p.slots] = int4{first, before, 0, 0};
+        return;
     }
-    if (g == p.groups || mine == 0) return;
+    if (mine == 0) return;
+    for (int s = tid; s * p.bm < mine; s += blockDim.x) {
+        const int left = mine - s * p.bm;
+        p.tiles[first + s] = int4{g, before + s * p.bm, left < p.bm ? left : p.bm, 0};
+    }
     int at = before + base;
     for (int c = c0; c < c1; c += kIdBatch) {
         // one batch holds a short run whole: its ids are still in registers
@@ -194,18 +182,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_quantize_kernel(
 
 PlanArgs plan_args(const int32_t *ids, int64_t rows, int32_t groups, bool none_last,
                    int32_t top_k, int bm, int32_t *order, int32_t *src, int32_t *tiles) {
-    PlanArgs p{};
-    p.ids = ids;
-    p.order = order;
-    p.src = src;
-    p.tiles[0] = (int4 *)tiles;
-    p.bm[0] = bm;
-    p.slots[0] = (int)plan_slots(rows, groups, bm);
-    p.rows = (int)rows;
-    p.groups = groups;
-    p.none_last = none_last;
-    p.top_k = top_k;
-    return p;
+    return PlanArgs{ids,    order,     src,   (int4 *)tiles, (int)rows,
+                    groups, none_last, top_k, bm,            (int)plan_slots(rows, groups, bm)};
 }
 
 // 16 wavefronts once each has a few chunks to read
@@ -226,15 +204,10 @@ hipError_t launch_plan(const int32_t *ids, int64_t rows, int32_t groups, bool no
 }
 
 hipError_t launch_plan_quantize(const int32_t *ids, int64_t rows, int32_t groups, int32_t top_k,
-                                int bm, int bm2, int32_t *order, int32_t *src, int32_t *tiles,
-                                int32_t *tiles2, const uint16_t *x, int64_t xrows, int64_t cols, int8_t *q,
+                                int bm, int32_t *order, int32_t *src, int32_t *tiles,
+                                const uint16_t *x, int64_t xrows, int64_t cols, int8_t *q,
                                 float *scales, hipStream_t stream) {
-    PlanArgs p = plan_args(ids, rows, groups, false, top_k, bm, order, src, tiles);
-    if (bm2) {
-        p.tiles[1] = (int4 *)tiles2;
-        p.bm[1] = bm2;
-        p.slots[1] = (int)plan_slots(rows, groups, bm2);
-    }
+    const PlanArgs p = plan_args(ids, rows, groups, false, top_k, bm, order, src, tiles);
     const int threads = plan_threads(rows);
     const int64_t per = threads / 64;
     const unsigned grid = (unsigned)(groups + 1 + (xrows + per - 1) / per);
