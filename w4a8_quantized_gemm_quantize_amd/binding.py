@@ -542,18 +542,25 @@ _FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
 def _rows(fn, t, dtypes, cols, name):
     """A 2-D CUDA tensor of one of `dtypes` and `cols` columns whose rows are
     contiguous; returns the elements from one row to the next."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{fn}: {name} must be a 2-D CUDA tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{fn}: {name} must be of dtype {' or '.join(map(str, dtypes))}, "
                          f"not {t.dtype}")
-    rows, have = t.shape
-    if have != cols:
-        raise W4A8SizeError(fn, f"a row of {name}", have, cols)
-    step, inner = t.stride()
-    if inner != 1 and cols > 1:
+    if t.size(1) != cols:
+        raise W4A8SizeError(fn, f"a row of {name}", t.size(1), cols)
+    if t.is_contiguous():
+        return cols
+    if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{fn}: rows of {name} must be contiguous")
-    return step if rows > 1 else cols
+    return t.stride(0) if t.size(0) > 1 else cols
+
+
+def _workspace(stream, need, device):
+    """A call's workspace, as _empty; at least 16 bytes."""
+    if stream is None:
+        return torch.empty(need or 16, dtype=torch.uint8, device=device)
+    return _empty(stream, (need or 16,), torch.uint8, device)
 
 
 def moe_route(logits, top_k: int, bias=None, score: str = "softmax", groups: int = 1,
@@ -637,7 +644,7 @@ def w4a8_moe_ffn(x, ids, weights, w13, w2, inter: int, out_dtype=torch.bfloat16,
     _sized(fn, c2, _F32, n2, "w2 ch_scale")
     if workspace is None:
         need = _moe_bytes(tokens, experts, top_k, hidden, inter, code)
-        workspace = _empty(stream, (need or 16,), torch.uint8, x.device)
+        workspace = _workspace(stream, need, x.device)
     else:
         _sized(fn, workspace, _U8, 0, "workspace")
     status = _lib.w4a8_moe_ffn(
@@ -663,17 +670,22 @@ def lora_add(x, a, b, ids, y, scale=None, out=None, workspace=None, stream=None)
     fn = "lora_add"
     _dev(a, torch.bfloat16, "a")
     _dev(b, torch.bfloat16, "b")
-    if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+    if a.dim() != 3 or b.dim() != 3:
         raise ValueError(f"{fn}: a must be [adapters, rank, k] and b [adapters, n, rank]")
     adapters, rank, k = a.shape
-    n = b.shape[1]
+    of_b, n, rank_b = b.shape
+    if of_b != adapters or rank_b != rank:
+        raise ValueError(f"{fn}: a must be [adapters, rank, k] and b [adapters, n, rank]")
     ldx = _rows(fn, x, (torch.bfloat16,), k, "x")
     ldy = _rows(fn, y, _FLOATS, n, "y")
-    tokens = x.shape[0]
-    if y.shape[0] != tokens:
-        raise W4A8SizeError(fn, "y (rows)", y.shape[0], tokens)
+    tokens = x.size(0)
+    if y.size(0) != tokens:
+        raise W4A8SizeError(fn, "y (rows)", y.size(0), tokens)
     if out is None:
-        out = _empty(stream, (tokens, n), y.dtype, y.device)
+        if stream is None and ldy == n:
+            out = torch.empty_like(y)
+        else:
+            out = _empty(stream, (tokens, n), y.dtype, y.device)
         ldo = n
     else:
         ldo = _rows(fn, out, (y.dtype,), n, "out")
@@ -683,7 +695,7 @@ def lora_add(x, a, b, ids, y, scale=None, out=None, workspace=None, stream=None)
     _sized(fn, scale, _F32, adapters, "scale")
     if workspace is None:
         need = lora_workspace_bytes(tokens, adapters, rank, k)
-        workspace = _empty(stream, (need or 16,), torch.uint8, x.device)
+        workspace = _workspace(stream, need, x.device)
     else:
         _sized(fn, workspace, _U8, 0, "workspace")
     status = _lib.w4a8_lora_add(

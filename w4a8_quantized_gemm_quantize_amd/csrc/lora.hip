@@ -101,20 +101,13 @@ __device__ __forceinline__ bool tile_rows(const LoraArgs &p, int slot, int *rows
 }
 
 // ----------------------------------------------------------------- shrink --
-template <int RT, int MT, bool PLAN>
-__global__ __launch_bounds__(64 * kLoraWaves) void lora_shrink_kernel(LoraArgs p) {
-    constexpr int BM = 16 * MT, RP = 16 * RT;
-    // steps of 32 along K per load batch; two batches are in flight
-    constexpr int U = RT + MT <= 3 ? 4 : RT + MT <= 6 ? 2 : 1;
-    __shared__ int rows[BM];
-    __shared__ f32x4 red[kLoraWaves][RT][64];
-    int count, adapter;
-    if (!tile_rows<BM, PLAN>(p, blockIdx.x, rows, count, adapter)) return;
-    if (adapter >= p.adapters) return;
-    const int tid = threadIdx.x;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+// acc += A x over k in [k0, kend) for the tile's rows (LDS) by one wavefront: lane
+// (r, q) ends with ranks 16 i + 4 q .. of row 16 j + r.
+template <int RT, int MT, int U>
+__device__ __forceinline__ void shrink_part(const LoraArgs &p, const int *rows, int adapter,
+                                            int64_t k0, int64_t kend, f32x4 (&acc)[RT][MT]) {
+    const int lane = threadIdx.x & 63;
     const int r = lane & 15, q = lane >> 4;
-
     const uint16_t *arow[RT], *xrow[MT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
@@ -123,19 +116,11 @@ __global__ __launch_bounds__(64 * kLoraWaves) void lora_shrink_kernel(LoraArgs p
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i) xrow[i] = p.x + (int64_t)rows[16 * i + r] * p.ldx + 8 * q;
-
-    f32x4 acc[RT][MT];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    // this wavefront's part of the slice, in steps of 32
-    const int64_t s0 = (int64_t)blockIdx.y * p.kslice;
-    const int64_t s1 = s0 + p.kslice < p.k ? s0 + p.kslice : p.k;
-    const int wpart = p.kslice / kLoraWaves;                   // a multiple of 32
-    const int64_t k0 = s0 + (int64_t)wave * wpart;
-    const int64_t kend = k0 + wpart < s1 ? k0 + wpart : s1;
     struct Batch {
         u32x4 a[U][RT], x[U][MT];
     };
@@ -195,6 +180,29 @@ __global__ __launch_bounds__(64 * kLoraWaves) void lora_shrink_kernel(LoraArgs p
 #pragma unroll
             for (int j = 0; j < MT; ++j) acc[i][j] = mfma_bf16(av[i], xv[j], acc[i][j]);
     }
+
+}
+
+template <int RT, int MT, bool PLAN>
+__global__ __launch_bounds__(64 * kLoraWaves) void lora_shrink_kernel(LoraArgs p) {
+    constexpr int BM = 16 * MT, RP = 16 * RT;
+    // steps of 32 along K per load batch; two batches are in flight
+    constexpr int U = RT + MT <= 3 ? 4 : RT + MT <= 6 ? 2 : 1;
+    __shared__ int rows[BM];
+    __shared__ f32x4 red[kLoraWaves][RT][64];
+    int count, adapter;
+    if (!tile_rows<BM, PLAN>(p, blockIdx.x, rows, count, adapter)) return;
+    if (adapter >= p.adapters) return;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int r = lane & 15, q = lane >> 4;
+
+    // this wavefront's part of the slice
+    const int64_t s0 = (int64_t)blockIdx.y * p.kslice;
+    const int64_t s1 = s0 + p.kslice < p.k ? s0 + p.kslice : p.k;
+    const int wpart = p.kslice / kLoraWaves;                   // a multiple of 32
+    const int64_t k0 = s0 + (int64_t)wave * wpart;
+    f32x4 acc[RT][MT];
+    shrink_part<RT, MT, U>(p, rows, adapter, k0, k0 + wpart < s1 ? k0 + wpart : s1, acc);
 
     // the four wavefronts' sums, in order; lane (t = r, q) holds ranks 16 i + 4 q ..
     float *part = p.part + ((int64_t)blockIdx.y * p.slots + blockIdx.x) * (BM * RP);
@@ -460,11 +468,130 @@ __global__ __launch_bounds__(64 * kLoraWaves) void lora_expand_kernel(LoraArgs p
     }
 }
 
+// ------------------------------------------------------------------ small --
+// Both products of a decode batch in one launch, where A of an adapter is small
+// enough to be read by every workgroup of its rows (from L2): a row tile x 512
+// columns, eight wavefronts that split K and then the columns.  B and y are on their
+// way while v is formed; v never leaves the workgroup.  Latency is all there is: ids,
+// then A, x, B and y side by side, then the result.
+constexpr int kSmallWaves = 8;
+constexpr int kSmallN = 64 * kSmallWaves;
+
+template <int RT, bool BF16>
+__global__ __launch_bounds__(64 * kSmallWaves) void lora_small_kernel(LoraArgs p) {
+    constexpr int BM = 16, RK = (RT + 1) / 2, TERMS = BF16 ? 2 : 3;
+    constexpr int VS = 32 * RK + 8;                // LDS row stride (bf16)
+    constexpr int YV = BF16 ? 2 : 4;               // 16-byte pieces of 16 columns
+    constexpr int PER = BF16 ? 8 : 4;              // columns of a piece
+    constexpr int ES = BF16 ? 2 : 4;
+    __shared__ int rows[BM];
+    __shared__ f32x4 red[kSmallWaves][RT][64];
+    __shared__ __attribute__((aligned(16))) uint16_t vs[TERMS][BM][VS];
+    int count, adapter;
+    if (!tile_rows<BM, false>(p, blockIdx.x, rows, count, adapter)) return;
+    const bool none = adapter >= p.adapters;
+    if (none && p.y == p.out) return;              // nothing to add or move
+    const int tid = threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const int r = lane & 15, q = lane >> 4;
+    const int n = (int)p.n;
+    const int n0 = (int)blockIdx.y * kSmallN + wave * 64;
+    const int col = n0 + 16 * q;
+    const int64_t row = rows[r];
+
+    // B: rows past n and ranks past the rank read zero
+    u32x4 bv[RK][4];
+    if (!none) {
+        const __amdgpu_buffer_rsrc_t rb =
+            buffer_rsrc(p.b + (int64_t)adapter * n * p.rank, (uint32_t)(n * p.rank * 2));
+#pragma unroll
+        for (int s = 0; s < RK; ++s)
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                const int kk = 32 * s + 8 * q;     // rank % 8 == 0: whole vectors
+                const uint32_t o =
+                    (uint32_t)((n0 + (r >> 2) * 16 + f * 4 + (r & 3)) * p.rank + kk) * 2;
+                bv[s][f] = buffer_load16(rb, kk < p.rank ? (int)o : (int)0x80000000u, 0);
+            }
+    }
+    u32x4 yv[YV];
+#pragma unroll
+    for (int c = 0; c < YV; ++c)
+        if (col + c * PER < n)
+            yv[c] = *(const u32x4 *)((const uint8_t *)p.y + (row * p.ldy + col + c * PER) * ES);
+    f32x4 sum[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) sum[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (!none) {
+        const int64_t part = ((p.k + 32 * kSmallWaves - 1) / (32 * kSmallWaves)) * 32;
+        const int64_t k0 = wave * part;
+        f32x4 acc[RT][1];
+        shrink_part<RT, 1, RT == 1 ? 8 : RT == 2 ? 4 : 2>(
+            p, rows, adapter, k0, k0 + part < p.k ? k0 + part : p.k, acc);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) red[wave][i][lane] = acc[i][0];
+        lds_barrier();
+        // the wavefronts' sums, in order, as bf16 terms; an odd last step of 16
+        // ranks is filled with zeros
+        const float sc = p.scale ? p.scale[adapter] : 1.0f;
+        for (int i = tid; i < 2 * RK * 64; i += 64 * kSmallWaves) {
+            f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+            const int it = i >> 6;
+            if (it < RT) {
+#pragma unroll
+                for (int w = 0; w < kSmallWaves; ++w) {
+                    const f32x4 o = red[w][it][i & 63];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = v[e] + o[e];
+                }
+            }
+            u32x2 t[TERMS];
+            split_terms<TERMS>(v, sc, t);
+#pragma unroll
+            for (int m = 0; m < TERMS; ++m)
+                *(u32x2 *)&vs[m][i & 15][16 * it + 4 * ((i & 63) >> 4)] = t[m];
+        }
+        lds_barrier();
+#pragma unroll
+        for (int m = TERMS - 1; m >= 0; --m)       // smallest terms first
+#pragma unroll
+            for (int s = 0; s < RK; ++s) {
+                const u32x4 vt = *(const u32x4 *)&vs[m][r][32 * s + 8 * q];
+#pragma unroll
+                for (int f = 0; f < 4; ++f) sum[f] = mfma_bf16(bv[s][f], vt, sum[f]);
+            }
+    }
+    if (r >= count) return;
+    uint8_t *dst = (uint8_t *)p.out + (row * p.ldo + col) * ES;
+#pragma unroll
+    for (int c = 0; c < YV; ++c) {
+        if (col + c * PER >= n) break;
+        u32x4 o = yv[c];
+        if (!none) {
+            if constexpr (BF16) {
+                float f[8];
+                bf16x8_to_f32(o, f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = f[e] + sum[2 * c + (e >> 2)][e & 3];
+                o = u32x4{bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]),
+                          bf16x2_rne(f[4], f[5]), bf16x2_rne(f[6], f[7])};
+            } else {
+                f32x4 f = __builtin_bit_cast(f32x4, o);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = f[e] + sum[c][e];
+                o = __builtin_bit_cast(u32x4, f);
+            }
+        }
+        *(u32x4 *)(dst + c * 16) = o;
+    }
+}
+
 // ---------------------------------------------------------------- launches --
 constexpr int64_t kBallotRows = 64;
+constexpr int64_t kSmallA = 128 * 1024;      // elements of an adapter's A, ranks padded
 
 struct LoraSpace {
-    bool plan;
+    bool plan, small;
     int bm, rp, slices, kslice;
     int64_t slots;
     size_t order, tiles, part, terms, end;
@@ -476,6 +603,9 @@ LoraSpace lora_space(int64_t tokens, int64_t adapters, int64_t rank, int64_t k) 
     s.bm = s.plan ? 64 : 16;
     s.rp = rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128;
     s.slots = s.plan ? plan_slots(tokens, adapters + 1, s.bm) : tokens;
+    // one launch while a workgroup reads its A (and as much of x, 16 rows of k) in
+    // less than the second launch takes
+    s.small = !s.plan && s.rp <= 64 && s.rp * k <= kSmallA;
     // about 768 workgroups, each wavefront at least 128 of K
     int64_t want = 768 / s.slots;
     const int64_t most = (k + 511) / 512;
@@ -493,11 +623,20 @@ LoraSpace lora_space(int64_t tokens, int64_t adapters, int64_t rank, int64_t k) 
     };
     s.order = take(s.plan ? (size_t)tokens * 4 : 0);
     s.tiles = take(s.plan ? (size_t)(s.slots + 1) * 16 : 0);
-    s.part = take((size_t)s.slices * s.slots * s.bm * s.rp * 4);
+    s.part = take(s.small ? 0 : (size_t)s.slices * s.slots * s.bm * s.rp * 4);
     // up to three terms, whole steps of 32 ranks
     s.terms = take(s.plan ? (size_t)s.slots * 3 * s.bm * (s.rp < 32 ? 32 : s.rp) * 2 : 0);
-    s.end = at;
+    s.end = at > 0 ? at : 256;      // never empty: a workspace is always given
     return s;
+}
+
+template <bool BF16>
+void launch_lora_small(const LoraArgs &p, int rp, hipStream_t stream) {
+    const dim3 grid((unsigned)p.slots, (unsigned)((p.n + kSmallN - 1) / kSmallN));
+    const dim3 block(64 * kSmallWaves);
+    if (rp == 16) lora_small_kernel<1, BF16><<<grid, block, 0, stream>>>(p);
+    else if (rp == 32) lora_small_kernel<2, BF16><<<grid, block, 0, stream>>>(p);
+    else lora_small_kernel<4, BF16><<<grid, block, 0, stream>>>(p);
 }
 
 template <int RT, bool PLAN, bool BF16>
@@ -574,7 +713,9 @@ hipError_t launch_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, co
     const int64_t tiles = s.plan ? 2 * s.slots : s.slots;
     const int64_t steps = s.plan ? 1 : tiles * ((n + kExpandN - 1) / kExpandN) / 1024;
     p.steps = (int)(steps < 1 ? 1 : steps > 8 ? 8 : steps);
-    if (s.plan && bf16) launch_lora_rank<true, true>(p, s.rp, stream);
+    if (s.small && bf16) launch_lora_small<true>(p, s.rp, stream);
+    else if (s.small) launch_lora_small<false>(p, s.rp, stream);
+    else if (s.plan && bf16) launch_lora_rank<true, true>(p, s.rp, stream);
     else if (s.plan) launch_lora_rank<true, false>(p, s.rp, stream);
     else if (bf16) launch_lora_rank<false, true>(p, s.rp, stream);
     else launch_lora_rank<false, false>(p, s.rp, stream);
