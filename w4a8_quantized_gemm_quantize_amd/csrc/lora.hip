@@ -281,13 +281,23 @@ __global__ __launch_bounds__(256) void lora_terms_kernel(LoraArgs p) {
 // ----------------------------------------------------------------- expand --
 // Workgroup: 16 MT rows of a row tile (part blockIdx.z of the plan's) x `steps`
 // times 256 columns, 64 per wavefront.  The four 16-row operand tiles of a
-// wavefront take the B rows in the order that gives lane (t, q) the 16 consecutive
-// columns 16 q .. 16 q + 15 of row t: y and out move in 16-byte pieces of whole
-// cache lines.  For decode batches the time is instructions and latencies as
+// wavefront take the B rows in the order (b_row) in which a 16-byte piece of the
+// result is 4 consecutive columns of a lane, or 8 of two tiles for bf16, and the four
+// lanes of a row hold 64 consecutive bytes: with 64 bytes of a row in one lane,
+// written 16 at a time, expand of 2047 x 8192 binary32 took 39 us.  For decode batches the time is instructions and latencies as
 // much as bytes (2.4 ns a dependent instruction), so B comes through buffer
 // loads whose bounds replace the tests of rank and columns, and addresses only
 // advance.
 constexpr int kExpandN = 64 * kLoraWaves;
+
+// The B row, of a wavefront's 64, that is row m of its operand tile f.
+template <bool BF16>
+__device__ __forceinline__ int b_row(int f, int m) {
+    return BF16 ? (f >> 1) * 32 + (m >> 2) * 8 + (f & 1) * 4 + (m & 3) : f * 16 + m;
+}
+// Pieces of a row: piece c of lane q starts PER q columns into the row's c-th 64
+// bytes.
+constexpr int kPieceBytes = 64;
 
 template <int RT, int MT, bool PLAN, bool BF16>
 __global__ __launch_bounds__(64 * kLoraWaves) void lora_expand_kernel(LoraArgs p) {
@@ -328,8 +338,8 @@ __global__ __launch_bounds__(64 * kLoraWaves) void lora_expand_kernel(LoraArgs p
     uint8_t *op[MT];
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
-        yp[j] = (const uint8_t *)p.y + ((int64_t)row[j] * p.ldy + n0 + 16 * q) * ES;
-        op[j] = (uint8_t *)p.out + ((int64_t)row[j] * p.ldo + n0 + 16 * q) * ES;
+        yp[j] = (const uint8_t *)p.y + ((int64_t)row[j] * p.ldy + n0 + PER * q) * ES;
+        op[j] = (uint8_t *)p.out + ((int64_t)row[j] * p.ldo + n0 + PER * q) * ES;
     }
     // y of the step's columns; in the row's last, partial step only what is there
     u32x4 yv[MT][YV];
@@ -338,17 +348,19 @@ __global__ __launch_bounds__(64 * kLoraWaves) void lora_expand_kernel(LoraArgs p
 #pragma unroll
             for (int j = 0; j < MT; ++j)
 #pragma unroll
-                for (int c = 0; c < YV; ++c) yv[j][c] = *(const u32x4 *)(yp[j] + c * 16);
+                for (int c = 0; c < YV; ++c)
+                    yv[j][c] = *(const u32x4 *)(yp[j] + c * kPieceBytes);
         } else {
 #pragma unroll
             for (int j = 0; j < MT; ++j)
 #pragma unroll
                 for (int c = 0; c < YV; ++c)
-                    if (n0 + 16 * q + c * PER < n) yv[j][c] = *(const u32x4 *)(yp[j] + c * 16);
+                    if (n0 + (4 * c + q) * PER < n)
+                        yv[j][c] = *(const u32x4 *)(yp[j] + c * kPieceBytes);
         }
     };
     auto store = [&](int j, int c, u32x4 v) {
-        if (n0 + 64 <= n || n0 + 16 * q + c * PER < n) *(u32x4 *)(op[j] + c * 16) = v;
+        if (n0 + 64 <= n || n0 + (4 * c + q) * PER < n) *(u32x4 *)(op[j] + c * kPieceBytes) = v;
     };
     auto advance = [&]() {
         n0 += kExpandN;
@@ -382,7 +394,7 @@ __global__ __launch_bounds__(64 * kLoraWaves) void lora_expand_kernel(LoraArgs p
         for (int f = 0; f < 4; ++f) {
             const int kk = 32 * s + 8 * q;         // rank % 8 == 0: whole vectors
             const uint32_t o =
-                (uint32_t)((n0 + (r >> 2) * 16 + f * 4 + (r & 3)) * p.rank + kk) * 2;
+                (uint32_t)((n0 + b_row<BF16>(f, r)) * p.rank + kk) * 2;
             boff[s][f] = kk < p.rank ? o : 0x80000000u;
         }
     const uint32_t bstep = (uint32_t)(kExpandN * p.rank * 2);
@@ -496,7 +508,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void lora_small_kernel(LoraArgs p
     const int r = lane & 15, q = lane >> 4;
     const int n = (int)p.n;
     const int n0 = (int)blockIdx.y * kSmallN + wave * 64;
-    const int col = n0 + 16 * q;
+    const int col = n0 + PER * q;                  // of piece 0
     const int64_t row = rows[r];
 
     // B: rows past n and ranks past the rank read zero
@@ -510,15 +522,16 @@ __global__ __launch_bounds__(64 * kSmallWaves) void lora_small_kernel(LoraArgs p
             for (int f = 0; f < 4; ++f) {
                 const int kk = 32 * s + 8 * q;     // rank % 8 == 0: whole vectors
                 const uint32_t o =
-                    (uint32_t)((n0 + (r >> 2) * 16 + f * 4 + (r & 3)) * p.rank + kk) * 2;
+                    (uint32_t)((n0 + b_row<BF16>(f, r)) * p.rank + kk) * 2;
                 bv[s][f] = buffer_load16(rb, kk < p.rank ? (int)o : (int)0x80000000u, 0);
             }
     }
     u32x4 yv[YV];
 #pragma unroll
     for (int c = 0; c < YV; ++c)
-        if (col + c * PER < n)
-            yv[c] = *(const u32x4 *)((const uint8_t *)p.y + (row * p.ldy + col + c * PER) * ES);
+        if (col + 4 * c * PER < n)
+            yv[c] = *(const u32x4 *)((const uint8_t *)p.y + (row * p.ldy + col) * ES +
+                                     c * kPieceBytes);
     f32x4 sum[4];
 #pragma unroll
     for (int f = 0; f < 4; ++f) sum[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -565,7 +578,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void lora_small_kernel(LoraArgs p
     uint8_t *dst = (uint8_t *)p.out + (row * p.ldo + col) * ES;
 #pragma unroll
     for (int c = 0; c < YV; ++c) {
-        if (col + c * PER >= n) break;
+        if (col + 4 * c * PER >= n) break;
         u32x4 o = yv[c];
         if (!none) {
             if constexpr (BF16) {
@@ -582,7 +595,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void lora_small_kernel(LoraArgs p
                 o = __builtin_bit_cast(u32x4, f);
             }
         }
-        *(u32x4 *)(dst + c * 16) = o;
+        *(u32x4 *)(dst + c * kPieceBytes) = o;
     }
 }
 
