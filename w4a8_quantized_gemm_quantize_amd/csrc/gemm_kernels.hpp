@@ -791,7 +791,9 @@ __device__ __forceinline__ int act_lds_off(int row, int c16) {
 // SEL: rows that choose weights (see above): the row tiles are the entries of
 // the tile table; per-token scales, K not split.
 template <int WF, int BM, int BN, int WAVES_M, int WAVES_N, int AB = 0, int SEL = kSelNone>
-__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, AB == 64 || AB == 128 ? 2 : 1) void gemm_tiled_kernel(
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N,
+                             SEL != kSelNone && BM == 64 ? 4 : AB == 64 || AB == 128 ? 2 : 1)
+void gemm_tiled_kernel(
     const int8_t *__restrict__ a_q, const float *__restrict__ a_scale,
     const uint8_t *__restrict__ w_packed, const uint8_t *__restrict__ grp_scale,
     const float *__restrict__ ch_scale, int64_t m, int64_t n, int64_t k,
@@ -823,8 +825,11 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, AB == 64 || AB == 128 ? 2 :
     // the weight arrays only stage the epilogue (half the wavefronts each).
     constexpr int kEpiW = (WAVES / 2) * WM * WN * 2;
     __shared__ __attribute__((aligned(16))) uint8_t act2[kRegW ? L::kAct : 16];
-    __shared__ __attribute__((aligned(16))) uint8_t wl0[kRegW ? kEpiW : L::kW];
-    __shared__ __attribute__((aligned(16))) uint8_t wl1[kRegW ? kEpiW : L::kW];
+    // SEL: it is staged in the activation arrays where it fits (42 -> 26 KB for 64 x
+    // 128 tiles, four workgroups per CU instead of three)
+    constexpr bool kEpiAct = kRegW && SEL != kSelNone && kEpiW <= L::kAct;
+    __shared__ __attribute__((aligned(16))) uint8_t wl0[kEpiAct ? 16 : kRegW ? kEpiW : L::kW];
+    __shared__ __attribute__((aligned(16))) uint8_t wl1[kEpiAct ? 16 : kRegW ? kEpiW : L::kW];
     // Per-token scales of the tile's rows and channel scales of its columns,
     // whole 1 KB blocks for the direct-to-LDS loads (per-token scales only).
     constexpr bool kSclLds = AB == 0;
@@ -1383,7 +1388,8 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, AB == 64 || AB == 128 ? 2 :
                       "epilogue tile fits the stage arrays");
         const int which = wave / PER_ARRAY;
         uint8_t *ebuf =
-            kRegW ? (wave < PER_W ? wl0 : wl1) + (wave % PER_W) * (WM * WN * 2)
+            kEpiAct ? (wave < PER_W ? act0 : act1) + (wave % PER_W) * (WM * WN * 2)
+            : kRegW ? (wave < PER_W ? wl0 : wl1) + (wave % PER_W) * (WM * WN * 2)
                   : (which == 0 ? act0 : which == 1 ? act1 : which == 2 ? wl0 : wl1) +
                         (wave % PER_ARRAY) * (WM * WN * 2);
         // the XOR stays inside the row: segs is a power of two, 2 to 16
