@@ -475,8 +475,8 @@ size_t w4a8_moe_ffn_workspace_bytes(int64_t tokens, int32_t experts, int32_t top
  * The result does not depend on timing (no sum is taken by atomics).
  * Requires hidden > 0, inter > 0, both multiples of 64, 1 <= top_k and
  * 1 <= experts (W4A8_ERR_SHAPE); experts <= W4A8_MAX_EXPERTS, top_k <=
- * W4A8_MAX_TOP_K, hidden and inter <= W4A8_K_MAX, tokens * hidden, inter *
- * hidden and tokens * top_k below 2^31, group == 64 (W4A8_ERR_UNSUPPORTED).
+ * W4A8_MAX_TOP_K, hidden and inter <= W4A8_K_MAX, tokens * hidden and inter *
+ * hidden below 2^31, tokens * top_k <= 2^30, group == 64 (W4A8_ERR_UNSUPPORTED).
  * The workspace is caller memory, 16-byte aligned, of at least
  * w4a8_moe_ffn_workspace_bytes(...) bytes (W4A8_ERR_SHAPE); calls that share it
  * must be ordered.  out may not alias x.

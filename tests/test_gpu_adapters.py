@@ -128,6 +128,17 @@ def test_values_that_are_not_numbers_stay_in_their_rows(w, t):
     assert got[5].isnan().all()
 
 
+@pytest.mark.parametrize("t", [3, 70])
+def test_adapters_past_4_gib(w, t):
+    a = torch.zeros((610, 128, 28672), dtype=torch.bfloat16, device="cuda")      # 4.5 GB
+    b = torch.zeros((610, 64, 128), dtype=torch.bfloat16, device="cuda")
+    x, a1, b1, ids, y, s = make(t, 1, 128, 28672, 64, torch.float32, 3, ids=torch.zeros(t))
+    a[609], b[609] = a1[0].cuda(), b1[0].cuda()
+    got = w.lora_add(x.cuda(), a, b, torch.full((t,), 609, dtype=torch.int32, device="cuda"),
+                     y.cuda())
+    check(got, x, a1, b1, ids, y, None)
+
+
 def test_refusals_on_the_device(w):
     v = make(4, 2, 16, 64, 32, torch.bfloat16, 1)
     x, a, b, ids, y, s = (q.cuda() for q in v)

@@ -139,6 +139,8 @@ CASES = [
     (1, 9, 3, 1088, 192),           # few rows: taken one by one
     (2, 64, 8, 320, 4160),
     (3, 128, 20, 128, 2112),
+    (1, 8, 8, 128, 14336),
+    (1, 32, 32, 64 + 64, 16384),
     (30, 8, 1, 512, 2112),          # fused down product, then with codes from memory
     (60, 8, 2, 4160, 1088),
     (20, 10, 2, 192, 8256),
@@ -231,6 +233,37 @@ def test_captured_in_a_graph(w):
         step()
         torch.cuda.synchronize()
         assert torch.equal(got, out), i
+
+
+def test_weights_past_4_gib(w):
+    hidden, inter, e = 4096, 14336, 76               # 4.5 GB of gate and up weights
+    g = torch.Generator(device="cuda").manual_seed(4)
+
+    def stack(n, k):
+        def nibbles():
+            return torch.randint(1, 16, (e * n * k // 2,), generator=g, device="cuda",
+                                 dtype=torch.uint8)
+        packed = nibbles()
+        packed |= nibbles() << 4
+        s = torch.randint(1, 17, (e * n * k // 64,), generator=g, device="cuda",
+                          dtype=torch.uint8)
+        return packed, s, torch.full((e * n,), 5e-4, device="cuda")
+
+    def pick(st, n, k, which):
+        return tuple(torch.cat([t.view(e, -1)[i] for i in which]) for t in st)
+
+    w13, w2 = stack(2 * inter, hidden), stack(hidden, inter)
+    two13, two2 = (pick(st, n, k, (1, e - 1)) for st, n, k in ((w13, 2 * inter, hidden),
+                                                              (w2, hidden, inter)))
+    for t in (1, 12, 80, 900):
+        x = torch.randn((t, hidden), generator=g, device="cuda").to(torch.bfloat16)
+        few = torch.randint(0, 2, (t, 1), generator=g, device="cuda", dtype=torch.int32)
+        wts = torch.rand((t, 1), generator=g, device="cuda")
+        got = w.w4a8_moe_ffn(x, torch.where(few == 0, 1, e - 1).to(torch.int32), wts, w13, w2,
+                             inter, out_dtype=torch.float32)
+        # y is binary32 in both (the two forms of bf16 outputs may round y or not)
+        assert torch.equal(got, w.w4a8_moe_ffn(x, few, wts, two13, two2, inter,
+                                               out_dtype=torch.float32)), t
 
 
 def test_refusals_on_the_device(w):

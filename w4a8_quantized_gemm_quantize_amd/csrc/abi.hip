@@ -140,7 +140,7 @@ w4a8_status check_moe_shape(int64_t tokens, int32_t experts, int32_t top_k, int6
     // 32-bit offsets inside one expert's weights, x and the row indices
     if (experts > W4A8_MAX_EXPERTS || top_k > W4A8_MAX_TOP_K || hidden > W4A8_K_MAX ||
         inter > W4A8_K_MAX || inter * hidden > INT32_MAX || tokens > INT32_MAX / hidden ||
-        tokens > INT32_MAX / top_k)
+        tokens * top_k > (1 << 30))
         return W4A8_ERR_UNSUPPORTED;
     // workgroups of the products: row tiles x 256-column tiles
     const int64_t cols = (2 * inter > hidden ? 2 * inter : hidden) / 256 + 1;
