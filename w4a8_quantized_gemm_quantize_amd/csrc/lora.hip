@@ -481,9 +481,8 @@ __global__ __launch_bounds__(64 * kLoraWaves) void lora_expand_kernel(LoraArgs p
 }
 
 // ------------------------------------------------------------------ small --
-// Both products of a decode batch in one launch, where A of an adapter is small
-// enough to be read by every workgroup of its rows (from L2): a row tile x 512
-// columns, eight wavefronts that split K and then the columns.  B and y are on their
+// Both products of a small decode batch in one launch (one_launch), A of an adapter
+// read by every workgroup of its rows (from L2): a row tile x 512 columns, eight wavefronts that split K and then the columns.  B and y are on their
 // way while v is formed; v never leaves the workgroup.  Latency is all there is: ids,
 // then A, x, B and y side by side, then the result.
 constexpr int kSmallWaves = 8;
@@ -601,10 +600,21 @@ __global__ __launch_bounds__(64 * kSmallWaves) void lora_small_kernel(LoraArgs p
 
 // ---------------------------------------------------------------- launches --
 constexpr int64_t kBallotRows = 64;
-constexpr int64_t kSmallA = 128 * 1024;      // elements of an adapter's A, ranks padded
+
+// One launch (lora_small_kernel) where reading A again in every workgroup costs less
+// than the second launch: by what one workgroup reads (elements of A, ranks padded) and
+// by what all read.  Measured, one launch | two, us per call: 8 rows of rank 16, 4096
+// x 4096 10.4 | 12.5; 1 row, 8904 x 11040 11.4 | 12.5; 8 rows, 8192 x 4096 13.0 | 12.9,
+// 16384 x 4096 22 | 12.7; 32 rows of rank 32, 8192 x 8192 41 | 12.5; 64 rows, 4096 x
+// 14336 53 | 15.
+constexpr int64_t kSmallA = 160 * 1024, kSmallAll = 6 << 20;
+bool one_launch(int64_t tokens, int64_t rp, int64_t k, int64_t n) {
+    return tokens <= kBallotRows && rp <= 64 && rp * k <= kSmallA &&
+           tokens * ((n + kSmallN - 1) / kSmallN) * rp * k <= kSmallAll;
+}
 
 struct LoraSpace {
-    bool plan, small;
+    bool plan;
     int bm, rp, slices, kslice;
     int64_t slots;
     size_t order, tiles, part, terms, end;
@@ -616,9 +626,6 @@ LoraSpace lora_space(int64_t tokens, int64_t adapters, int64_t rank, int64_t k) 
     s.bm = s.plan ? 64 : 16;
     s.rp = rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128;
     s.slots = s.plan ? plan_slots(tokens, adapters + 1, s.bm) : tokens;
-    // one launch while a workgroup reads its A (and as much of x, 16 rows of k) in
-    // less than the second launch takes
-    s.small = !s.plan && s.rp <= 64 && s.rp * k <= kSmallA;
     // about 768 workgroups, each wavefront at least 128 of K
     int64_t want = 768 / s.slots;
     const int64_t most = (k + 511) / 512;
@@ -636,10 +643,10 @@ LoraSpace lora_space(int64_t tokens, int64_t adapters, int64_t rank, int64_t k) 
     };
     s.order = take(s.plan ? (size_t)tokens * 4 : 0);
     s.tiles = take(s.plan ? (size_t)(s.slots + 1) * 16 : 0);
-    s.part = take(s.small ? 0 : (size_t)s.slices * s.slots * s.bm * s.rp * 4);
+    s.part = take((size_t)s.slices * s.slots * s.bm * s.rp * 4);
     // up to three terms, whole steps of 32 ranks
     s.terms = take(s.plan ? (size_t)s.slots * 3 * s.bm * (s.rp < 32 ? 32 : s.rp) * 2 : 0);
-    s.end = at > 0 ? at : 256;      // never empty: a workspace is always given
+    s.end = at;
     return s;
 }
 
@@ -726,8 +733,9 @@ hipError_t launch_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, co
     const int64_t tiles = s.plan ? 2 * s.slots : s.slots;
     const int64_t steps = s.plan ? 1 : tiles * ((n + kExpandN - 1) / kExpandN) / 1024;
     p.steps = (int)(steps < 1 ? 1 : steps > 8 ? 8 : steps);
-    if (s.small && bf16) launch_lora_small<true>(p, s.rp, stream);
-    else if (s.small) launch_lora_small<false>(p, s.rp, stream);
+    const bool small = one_launch(tokens, s.rp, k, n);
+    if (small && bf16) launch_lora_small<true>(p, s.rp, stream);
+    else if (small) launch_lora_small<false>(p, s.rp, stream);
     else if (s.plan && bf16) launch_lora_rank<true, true>(p, s.rp, stream);
     else if (s.plan) launch_lora_rank<true, false>(p, s.rp, stream);
     else if (bf16) launch_lora_rank<false, true>(p, s.rp, stream);
