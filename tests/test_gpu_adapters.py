@@ -61,9 +61,11 @@ CASES = [
     (16, 1, 16, 512, 264),
     (17, 2, 32, 1000, 520),
     (63, 40, 64, 2048, 1032),
-    (60, 7, 16, 4000, 1504),        # two launches for decode batches, by what they read
-    (40, 9, 32, 5000, 1000),
-    (64, 5, 16, 1024, 10000),       # several column steps in a workgroup
+    (60, 7, 16, 4000, 1504),
+    (64, 5, 16, 1024, 10000),
+    (40, 9, 32, 5000, 1000),        # two launches for decode batches, by what they read
+    (60, 7, 16, 9600, 1504),
+    (64, 5, 8, 9600, 8200),         # several column steps in a workgroup
     (64, 2, 128, 776, 248),
     (65, 2, 128, 776, 248),
     (65, 70, 8, 136, 1000),

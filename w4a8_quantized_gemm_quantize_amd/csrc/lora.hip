@@ -602,15 +602,18 @@ __global__ __launch_bounds__(64 * kSmallWaves) void lora_small_kernel(LoraArgs p
 constexpr int64_t kBallotRows = 64;
 
 // One launch (lora_small_kernel) where reading A again in every workgroup costs less
-// than the second launch: by what one workgroup reads (elements of A, ranks padded) and
-// by what all read.  Measured, one launch | two, us per call: 8 rows of rank 16, 4096
-// x 4096 10.4 | 12.5; 1 row, 8904 x 11040 11.4 | 12.5; 8 rows, 8192 x 4096 13.0 | 12.9,
-// 16384 x 4096 22 | 12.7; 32 rows of rank 32, 8192 x 8192 41 | 12.5; 64 rows, 4096 x
-// 14336 53 | 15.
-constexpr int64_t kSmallA = 160 * 1024, kSmallAll = 6 << 20;
-bool one_launch(int64_t tokens, int64_t rp, int64_t k, int64_t n) {
-    return tokens <= kBallotRows && rp <= 64 && rp * k <= kSmallA &&
-           tokens * ((n + kSmallN - 1) / kSmallN) * rp * k <= kSmallAll;
+// than the second launch: by the elements of A (ranks padded) that a CU reads, at
+// about 64 bytes a clock.  Measured, one launch | two, us per call: 8 rows of rank 16,
+// 4096 x 4096 10.4 | 12.5; 1 row, 8904 x 11040 11.4 | 12.5; 20 rows of rank 8, 6384 x
+// 3096 10.9 | 14; 8 rows of rank 16, 8192 x 4096 13.0 | 12.9, 16384 x 4096 22 | 12.7; 32
+// rows of rank 32, 8192 x 8192 41 | 12.5; 64 rows, 4096 x 14336 53 | 15.
+constexpr int64_t kSmallA = 144 * 1024;
+bool one_launch(int64_t tokens, int64_t adapters, int64_t rp, int64_t k, int64_t n) {
+    if (tokens > kBallotRows || rp > 64) return false;
+    const int64_t most = adapters + 1 + tokens / 16;           // row tiles
+    const int64_t wgs = (tokens < most ? tokens : most) * ((n + kSmallN - 1) / kSmallN);
+    const int64_t ncu = device_cu_count();
+    return (wgs + ncu - 1) / ncu * rp * k <= kSmallA;
 }
 
 struct LoraSpace {
@@ -733,7 +736,7 @@ hipError_t launch_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, co
     const int64_t tiles = s.plan ? 2 * s.slots : s.slots;
     const int64_t steps = s.plan ? 1 : tiles * ((n + kExpandN - 1) / kExpandN) / 1024;
     p.steps = (int)(steps < 1 ? 1 : steps > 8 ? 8 : steps);
-    const bool small = one_launch(tokens, s.rp, k, n);
+    const bool small = one_launch(tokens, adapters, s.rp, k, n);
     if (small && bf16) launch_lora_small<true>(p, s.rp, stream);
     else if (small) launch_lora_small<false>(p, s.rp, stream);
     else if (s.plan && bf16) launch_lora_rank<true, true>(p, s.rp, stream);
