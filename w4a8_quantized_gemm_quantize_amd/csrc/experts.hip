@@ -323,7 +323,12 @@ int row_block(int64_t rows, int64_t experts) {
 
 // Whether a batch is taken row by row (kSelDirect, two launches) rather than
 // sorted (four): where the weights that two tokens then read separately cost
-// less than two launches and their gaps, about 10 us.
+// less than two launches and their gaps.  Measured on one box, us, row by row |
+// sorted, by those bytes: 13 MB (4 tokens, 8 of 64 experts 2048 x 768) 20.7 | 25.7;
+// 29 MB (8 tokens, 2 of 8, 2048 x 1024) 17.3 | 23.7; 30 MB (8 tokens, 8 of 128,
+// 2048 x 768) 34.7 | 33.8; 36 MB (4 tokens, 4 of 32, 4096 x 2048) 42.0 | 36.3; 46 MB
+// (2 tokens, 2 of 8, 4096 x 14336) 67.5 | 58.2; 143 MB (8 tokens, 4 of 32, 4096 x
+// 2048) 76.5 | 49.1.
 bool direct_pays(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inter) {
     if (tokens * top_k > 64 || hidden > kFusedRowMax || hidden < kChunkK || inter < kChunkK ||
         inter > kTokenKMax)
@@ -332,7 +337,7 @@ bool direct_pays(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden,
     const double hit = top_k < experts ? (double)top_k / experts : 1.0;
     for (int64_t t = 0; t < tokens; ++t) miss *= 1.0 - hit;
     const double again = (double)(tokens * top_k) - experts * (1.0 - miss);
-    return again * 1.55 * hidden * inter < 50e6;       // bytes of an expert's weights
+    return again * 1.55 * hidden * inter < 30e6;       // bytes of an expert's weights
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
