@@ -469,9 +469,7 @@ size_t w4a8_moe_ffn_workspace_bytes(int64_t tokens, int32_t experts, int32_t top
  *   hq, hs  = codes and scale of the row h, as for x
  *   y       = the w4a8_gemm output (binary32) of w2 of e
  *   out[t]  = sum over used slots, in order, of weights[t, j] * y  (binary32),
- *             rounded to out's type; 0 for a token without used slots.
- * With bf16 outputs and more than 16 slots an expert (tokens * top_k / experts) y
- * is rounded to bf16 before the sum.
+ *             rounded once to out's type; 0 for a token without used slots.
  * The result does not depend on timing (no sum is taken by atomics).
  * Requires hidden > 0, inter > 0, both multiples of 64, 1 <= top_k and
  * 1 <= experts (W4A8_ERR_SHAPE); experts <= W4A8_MAX_EXPERTS, top_k <=

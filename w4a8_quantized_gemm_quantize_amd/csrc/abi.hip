@@ -538,7 +538,7 @@ size_t w4a8_moe_ffn_workspace_bytes(int64_t tokens, int32_t experts, int32_t top
     if (tokens <= 0 || check_moe_shape(tokens, experts, top_k, hidden, inter, W4A8_GROUP,
                                        out_dtype) != W4A8_OK)
         return 0;
-    return w4a8::moe_workspace_bytes(tokens, experts, top_k, hidden, inter, (int)out_dtype);
+    return w4a8::moe_workspace_bytes(tokens, experts, top_k, hidden, inter);
 }
 
 w4a8_status w4a8_moe_ffn(const uint16_t *x, const int32_t *ids, const float *weights,
@@ -557,8 +557,7 @@ w4a8_status w4a8_moe_ffn(const uint16_t *x, const int32_t *ids, const float *wei
         if (!p) return W4A8_ERR_NULL;
     for (const void *p : needed)
         if (!aligned16(p)) return W4A8_ERR_MISALIGNED;
-    if (ws_bytes < w4a8::moe_workspace_bytes(tokens, experts, top_k, hidden, inter,
-                                             (int)out_dtype))
+    if (ws_bytes < w4a8::moe_workspace_bytes(tokens, experts, top_k, hidden, inter))
         return W4A8_ERR_SHAPE;
     st = debug_check_inputs(stream, {{x, (size_t)(tokens * hidden), true},
                                      {weights, (size_t)(tokens * top_k), false},

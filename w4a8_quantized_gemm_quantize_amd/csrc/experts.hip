@@ -16,12 +16,12 @@ namespace {
 // ---------------------------------------------------------------- combine --
 // out[t][c] = sum over the token's slots j, in order, of weights[t][j] *
 // y[t top_k + j][c], in binary32; slots without an expert were never written and
-// are skipped.  A stream over y: 8 columns a thread, four slots' loads in
-// flight.  YBF16: y was rounded to bf16 on its way here (bf16 outputs of large
-// batches, where y is the largest intermediate: two roundings of 2^-8 instead of
-// one, for half of its traffic).
-template <bool YBF16, bool BF16>
-__global__ __launch_bounds__(256) void combine_kernel(const void *__restrict__ y,
+// are skipped.  A stream over y, bound by its bytes: 8 columns a thread, four
+// slots' loads in flight.  y is binary32 for bf16 outputs too: rounded to bf16 it
+// would be half the bytes, but the error of a sum of two to four slots grew from
+// 1.7e-3 to 2.4e-3 of its norm, and a token's bits then depended on the batch.
+template <bool BF16>
+__global__ __launch_bounds__(256) void combine_kernel(const float *__restrict__ y,
                                                       const int32_t *__restrict__ ids,
                                                       const float *__restrict__ weights,
                                                       int64_t tokens, int experts, int top_k,
@@ -37,7 +37,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const void *__restrict__ y
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
     for (int j0 = 0; j0 < top_k; j0 += 4) {
-        u32x4 a[4], b[4];
+        f32x4 a[4], b[4];
         float w[4];
         bool ok[4];
 #pragma unroll
@@ -46,30 +46,17 @@ __global__ __launch_bounds__(256) void combine_kernel(const void *__restrict__ y
             const int id = ids[j];
             ok[jj] = j0 + jj < top_k && id >= 0 && id < experts;
             w[jj] = weights[j];
-            const u32x4 *p = (const u32x4 *)y + (row0 + j) * (YBF16 ? vecs : 2 * vecs);
-            if constexpr (YBF16) {
-                a[jj] = p[v];
-            } else {
-                a[jj] = p[2 * v];
-                b[jj] = p[2 * v + 1];
-            }
+            const f32x4 *p = (const f32x4 *)y + (row0 + j) * 2 * vecs;
+            a[jj] = p[2 * v];
+            b[jj] = p[2 * v + 1];
         }
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
-            float f[8];
-            if constexpr (YBF16) {
-                bf16x8_to_f32(a[jj], f);
-            } else {
-                const f32x4 lo = __builtin_bit_cast(f32x4, a[jj]);
-                const f32x4 hi = __builtin_bit_cast(f32x4, b[jj]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    f[i] = lo[i];
-                    f[4 + i] = hi[i];
-                }
+            for (int i = 0; i < 4; ++i) {
+                acc[i] = ok[jj] ? acc[i] + w[jj] * a[jj][i] : acc[i];
+                acc[4 + i] = ok[jj] ? acc[4 + i] + w[jj] * b[jj][i] : acc[4 + i];
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = ok[jj] ? acc[i] + w[jj] * f[i] : acc[i];
         }
     }
     if constexpr (BF16) {
@@ -348,13 +335,12 @@ struct MoeSpace {
     size_t xq, xs, order, src, tiles, h, hq, hs, y, end;
     MoeForm form;
     int bm;
-    int y_dtype;              // 0 binary32, 1 bf16
     bool fused_down;          // kMoeFew: the down product takes its rows' codes itself
     int64_t slots;
 };
 
-MoeSpace moe_space(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inter,
-                   int out_dtype) {
+MoeSpace moe_space(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden,
+                   int64_t inter) {
     const size_t t = (size_t)tokens, r = (size_t)(tokens * top_k);
     MoeSpace s;
     s.bm = row_block((int64_t)r, experts);
@@ -364,7 +350,6 @@ MoeSpace moe_space(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidde
                                                                    : kMoeTiled;
     s.fused_down = s.form == kMoeFew && inter <= kFusedRowMax && s.bm * (inter + 16) <= 34 * 1024;
     s.slots = plan_slots((int64_t)r, experts, s.bm);
-    s.y_dtype = s.form == kMoeTiled ? out_dtype : 0;
     size_t at = 0;
     auto take = [&](bool used, size_t bytes) {
         const size_t here = at;
@@ -380,7 +365,7 @@ MoeSpace moe_space(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidde
     s.h = take(true, r * inter * 2);
     s.hq = take(sorted && !s.fused_down, r * inter);
     s.hs = take(sorted && !s.fused_down, r * 4);
-    s.y = take(sorted, r * hidden * (s.y_dtype == 1 ? 2 : 4));
+    s.y = take(sorted, r * hidden * 4);
     s.end = at;
     return s;
 }
@@ -388,8 +373,8 @@ MoeSpace moe_space(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidde
 }  // namespace
 
 size_t moe_workspace_bytes(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden,
-                           int64_t inter, int out_dtype) {
-    return moe_space(tokens, experts, top_k, hidden, inter, out_dtype).end;
+                           int64_t inter) {
+    return moe_space(tokens, experts, top_k, hidden, inter).end;
 }
 
 hipError_t launch_moe_ffn(const uint16_t *x, const int32_t *ids, const float *weights,
@@ -397,7 +382,7 @@ hipError_t launch_moe_ffn(const uint16_t *x, const int32_t *ids, const float *we
                           const uint8_t *w2, const uint8_t *g2, const float *c2, int64_t tokens,
                           int32_t experts, int32_t top_k, int64_t hidden, int64_t inter,
                           void *out, int out_dtype, void *workspace, hipStream_t stream) {
-    const MoeSpace s = moe_space(tokens, experts, top_k, hidden, inter, out_dtype);
+    const MoeSpace s = moe_space(tokens, experts, top_k, hidden, inter);
     uint8_t *ws = (uint8_t *)workspace;
     const int64_t rows = tokens * top_k;
     int32_t *order = (int32_t *)(ws + s.order), *src = (int32_t *)(ws + s.src);
@@ -450,7 +435,7 @@ hipError_t launch_moe_ffn(const uint16_t *x, const int32_t *ids, const float *we
     p.k = inter;
     p.out = ws + s.y;
     p.ldo = hidden;
-    p.out_dtype = s.y_dtype;
+    p.out_dtype = 0;
     p.sel.map = order;
     if (s.fused_down) launch_sel_fused<kSelScatter>(p, s.bm, stream);
     else if (s.form == kMoeFew) launch_sel_skinny<kSelScatter, false, 1>(p, s.bm, stream);
@@ -458,10 +443,9 @@ hipError_t launch_moe_ffn(const uint16_t *x, const int32_t *ids, const float *we
     const int64_t gy = tokens < 32768 ? tokens : 32768;
     const dim3 grid((unsigned)((hidden / 8 + 255) / 256), (unsigned)gy,
                     (unsigned)((tokens + gy - 1) / gy));
-    const auto combine = s.y_dtype == 1     ? combine_kernel<true, true>
-                         : out_dtype == 1 ? combine_kernel<false, true>
-                                          : combine_kernel<false, false>;
-    combine<<<grid, 256, 0, stream>>>(ws + s.y, ids, weights, tokens, experts, top_k, hidden, out);
+    const auto combine = out_dtype == 1 ? combine_kernel<true> : combine_kernel<false>;
+    combine<<<grid, 256, 0, stream>>>((const float *)(ws + s.y), ids, weights, tokens, experts,
+                                      top_k, hidden, out);
     return hipGetLastError();
 }
 

@@ -113,7 +113,7 @@ hipError_t launch_plan_quantize(const int32_t *ids, int64_t rows, int32_t groups
 
 // Experts' products (experts.hip), arguments as w4a8_moe_ffn in w4a8.h.
 size_t moe_workspace_bytes(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden,
-                           int64_t inter, int out_dtype);
+                           int64_t inter);
 hipError_t launch_moe_ffn(const uint16_t *x, const int32_t *ids, const float *weights,
                           const uint8_t *w13, const uint8_t *g13, const float *c13,
                           const uint8_t *w2, const uint8_t *g2, const float *c2, int64_t tokens,
