@@ -504,8 +504,8 @@ size_t w4a8_lora_workspace_bytes(int64_t tokens, int32_t adapters, int32_t rank,
  *   y, out [tokens, n], rows ldy / ldo elements apart, both bf16 (W4A8_BF16) or
  *         both binary32 (W4A8_F32); out may be y itself (same pointer and stride)
  * a[l] x[t] is summed in binary32 (parts of k, added in order) and kept so: the
- * product with b takes it as bf16 terms that hold it to 2^-16 (bf16 out) or
- * 2^-24 (binary32 out); the sum with y is binary32, rounded once to out's type.
+ * product with b takes it as bf16 terms that hold it to 2^-24; the sum with y is
+ * binary32, rounded once to out's type.
  * Adapters of lower rank are padded with zero rows of a and columns of b.
  * Requires rank, k, n > 0, rank, k, n, ldx multiples of 8, ldy and ldo multiples
  * of 8 (bf16) or 4 (binary32), ldx >= k, ldy, ldo >= n, adapters >= 1

@@ -9,8 +9,10 @@
 //   expand  sums the parts (in order), folds the adapter's scale in, and
 //           multiplies by B on the matrix cores with y added in the epilogue.
 // v stays binary32 throughout: the matrix cores take bf16, so it is split into
-// bf16 terms (v = hi + lo, error 2^-16, for bf16 outputs; three terms, exact to
-// 2^-24, for binary32 outputs), each multiplied by the same B operand.
+// three bf16 terms, which hold all 24 bits of it, each multiplied by the same B
+// operand.  Two terms hold 16 bits: 1 in 450 to 1850 of the bf16 outputs then
+// differed from the rounded 64-bit ones, with three 1 in 4000 or fewer, for at most
+// 5 % of a call (64 rows, 4096 x 14336, rank 64: 28.3 -> 29.4 us).
 //
 // v_mfma_f32_16x16x32_bf16: lane (r = l % 16, q = l / 16) supplies row r of the
 // first operand and column r of the second, both at k = 8 q .. 8 q + 7 (16
@@ -33,6 +35,8 @@ namespace {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
+constexpr int kTerms = 3;                          // bf16 terms of a binary32 v
+
 __device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
                                                    __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
@@ -45,7 +49,7 @@ struct LoraArgs {
     const void *y;
     void *out;
     float *part;              // [slices][slots][BM][RP]
-    uint16_t *terms;          // plan form: v in bf16 terms [slots][TERMS][BM][32 RK]
+    uint16_t *terms;          // plan form: v in bf16 terms [slots][kTerms][BM][32 RK]
     const int4 *tiles;        // plan form only
     const int32_t *order;
     int64_t ldx, ldy, ldo, k, n;
@@ -226,13 +230,12 @@ __global__ __launch_bounds__(64 * kLoraWaves) void lora_shrink_kernel(LoraArgs p
 }
 
 // ------------------------------------------------------------------ terms --
-// Four ranks of scale * (sum of the parts, in order) as TERMS bf16 terms.
-template <int TERMS>
-__device__ __forceinline__ void split_terms(f32x4 v, float sc, u32x2 (&t)[TERMS]) {
+// Four ranks of scale * (sum of the parts, in order) as bf16 terms.
+__device__ __forceinline__ void split_terms(f32x4 v, float sc, u32x2 (&t)[kTerms]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = v[e] * sc;
 #pragma unroll
-    for (int m = 0; m < TERMS; ++m) {
+    for (int m = 0; m < kTerms; ++m) {
         t[m] = u32x2{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
         v[0] = v[0] - __uint_as_float(t[m].x << 16);
         v[1] = v[1] - __uint_as_float(t[m].x & 0xffff0000u);
@@ -257,9 +260,9 @@ __device__ __forceinline__ f32x4 sum_parts(const float *src, int slices, int64_t
     return v;
 }
 
-template <int RT, bool BF16>
+template <int RT>
 __global__ __launch_bounds__(256) void lora_terms_kernel(LoraArgs p) {
-    constexpr int BM = 64, RP = 16 * RT, RK = (RT + 1) / 2, TERMS = BF16 ? 2 : 3;
+    constexpr int BM = 64, RP = 16 * RT, RK = (RT + 1) / 2;
     constexpr int VEC = 8 * RK;                    // 4-rank pieces of a row
     const int4 tile = p.tiles[blockIdx.x];
     if (tile.z == 0 || tile.x >= p.adapters) return;
@@ -271,11 +274,11 @@ __global__ __launch_bounds__(256) void lora_terms_kernel(LoraArgs p) {
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
     if (c4 < p.rank)
         v = sum_parts(p.part + (int64_t)blockIdx.x * (BM * RP) + t * RP + c4, p.slices, stride);
-    u32x2 w[TERMS];
-    split_terms<TERMS>(v, sc, w);
+    u32x2 w[kTerms];
+    split_terms(v, sc, w);
 #pragma unroll
-    for (int m = 0; m < TERMS; ++m)
-        *(u32x2 *)(p.terms + (((int64_t)blockIdx.x * TERMS + m) * BM + t) * (32 * RK) + c4) = w[m];
+    for (int m = 0; m < kTerms; ++m)
+        *(u32x2 *)(p.terms + (((int64_t)blockIdx.x * kTerms + m) * BM + t) * (32 * RK) + c4) = w[m];
 }
 
 // ----------------------------------------------------------------- expand --
@@ -303,13 +306,12 @@ template <int RT, int MT, bool PLAN, bool BF16>
 __global__ __launch_bounds__(64 * kLoraWaves) void lora_expand_kernel(LoraArgs p) {
     constexpr int BM = 16 * MT, RP = 16 * RT;
     constexpr int RK = (RT + 1) / 2;               // steps of 32 along the rank
-    constexpr int TERMS = BF16 ? 2 : 3;
     constexpr int VS = 32 * RK + 8;                // LDS row stride (bf16)
     constexpr int YV = BF16 ? 2 : 4;               // 16-byte pieces of 16 columns
     constexpr int PER = BF16 ? 8 : 4;              // columns of a piece
     constexpr int ES = BF16 ? 2 : 4;
     __shared__ int rows[PLAN ? 1 : BM];
-    __shared__ __attribute__((aligned(16))) uint16_t vs[PLAN ? 1 : TERMS][PLAN ? 1 : BM][VS];
+    __shared__ __attribute__((aligned(16))) uint16_t vs[PLAN ? 1 : kTerms][PLAN ? 1 : BM][VS];
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int r = lane & 15, q = lane >> 4;
@@ -420,15 +422,15 @@ __global__ __launch_bounds__(64 * kLoraWaves) void lora_expand_kernel(LoraArgs p
             f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
             if (c4 < p.rank)
                 v = sum_parts(part + t * RP + c4, p.slices, (int64_t)p.slots * (BM * RP));
-            u32x2 w[TERMS];
-            split_terms<TERMS>(v, sc, w);
+            u32x2 w[kTerms];
+            split_terms(v, sc, w);
 #pragma unroll
-            for (int m = 0; m < TERMS; ++m) *(u32x2 *)&vs[m][t][c4] = w[m];
+            for (int m = 0; m < kTerms; ++m) *(u32x2 *)&vs[m][t][c4] = w[m];
         }
         lds_barrier();                             // B and y stay in flight
     }
     const uint16_t *terms =
-        p.terms + (int64_t)blockIdx.x * (TERMS * 64 * 32 * RK) + blockIdx.z * (BM * 32 * RK);
+        p.terms + (int64_t)blockIdx.x * (kTerms * 64 * 32 * RK) + blockIdx.z * (BM * 32 * RK);
 #pragma unroll 1
     while (true) {
 #pragma unroll
@@ -441,7 +443,7 @@ __global__ __launch_bounds__(64 * kLoraWaves) void lora_expand_kernel(LoraArgs p
             // other row of the result
             const int t = 16 * j + r < count ? 16 * j + r : count - 1;
 #pragma unroll
-            for (int m = TERMS - 1; m >= 0; --m)   // smallest terms first
+            for (int m = kTerms - 1; m >= 0; --m)   // smallest terms first
 #pragma unroll
                 for (int s = 0; s < RK; ++s) {
                     u32x4 vt;
@@ -490,14 +492,14 @@ constexpr int kSmallN = 64 * kSmallWaves;
 
 template <int RT, bool BF16>
 __global__ __launch_bounds__(64 * kSmallWaves) void lora_small_kernel(LoraArgs p) {
-    constexpr int BM = 16, RK = (RT + 1) / 2, TERMS = BF16 ? 2 : 3;
+    constexpr int BM = 16, RK = (RT + 1) / 2;
     constexpr int VS = 32 * RK + 8;                // LDS row stride (bf16)
     constexpr int YV = BF16 ? 2 : 4;               // 16-byte pieces of 16 columns
     constexpr int PER = BF16 ? 8 : 4;              // columns of a piece
     constexpr int ES = BF16 ? 2 : 4;
     __shared__ int rows[BM];
     __shared__ f32x4 red[kSmallWaves][RT][64];
-    __shared__ __attribute__((aligned(16))) uint16_t vs[TERMS][BM][VS];
+    __shared__ __attribute__((aligned(16))) uint16_t vs[kTerms][BM][VS];
     int count, adapter;
     if (!tile_rows<BM, false>(p, blockIdx.x, rows, count, adapter)) return;
     const bool none = adapter >= p.adapters;
@@ -557,15 +559,15 @@ __global__ __launch_bounds__(64 * kSmallWaves) void lora_small_kernel(LoraArgs p
                     for (int e = 0; e < 4; ++e) v[e] = v[e] + o[e];
                 }
             }
-            u32x2 t[TERMS];
-            split_terms<TERMS>(v, sc, t);
+            u32x2 t[kTerms];
+            split_terms(v, sc, t);
 #pragma unroll
-            for (int m = 0; m < TERMS; ++m)
+            for (int m = 0; m < kTerms; ++m)
                 *(u32x2 *)&vs[m][i & 15][16 * it + 4 * ((i & 63) >> 4)] = t[m];
         }
         lds_barrier();
 #pragma unroll
-        for (int m = TERMS - 1; m >= 0; --m)       // smallest terms first
+        for (int m = kTerms - 1; m >= 0; --m)       // smallest terms first
 #pragma unroll
             for (int s = 0; s < RK; ++s) {
                 const u32x4 vt = *(const u32x4 *)&vs[m][r][32 * s + 8 * q];
@@ -647,8 +649,8 @@ LoraSpace lora_space(int64_t tokens, int64_t adapters, int64_t rank, int64_t k) 
     s.order = take(s.plan ? (size_t)tokens * 4 : 0);
     s.tiles = take(s.plan ? (size_t)(s.slots + 1) * 16 : 0);
     s.part = take((size_t)s.slices * s.slots * s.bm * s.rp * 4);
-    // up to three terms, whole steps of 32 ranks
-    s.terms = take(s.plan ? (size_t)s.slots * 3 * s.bm * (s.rp < 32 ? 32 : s.rp) * 2 : 0);
+    // whole steps of 32 ranks
+    s.terms = take(s.plan ? (size_t)s.slots * kTerms * s.bm * (s.rp < 32 ? 32 : s.rp) * 2 : 0);
     s.end = at;
     return s;
 }
@@ -671,7 +673,7 @@ void launch_lora_form(const LoraArgs &p, hipStream_t stream) {
     if constexpr (PLAN) {
         lora_shrink_kernel<RT, 4, true><<<shrink, block, 0, stream>>>(p);
         constexpr int RK = (RT + 1) / 2;
-        lora_terms_kernel<RT, BF16>
+        lora_terms_kernel<RT>
             <<<dim3((unsigned)p.slots, 64 * 8 * RK / 256), 256, 0, stream>>>(p);
         lora_expand_kernel<RT, 2, true, BF16>
             <<<dim3((unsigned)p.slots, cols, 2), block, 0, stream>>>(p);
