@@ -502,7 +502,8 @@ size_t w4a8_lora_workspace_bytes(int64_t tokens, int32_t adapters, int32_t rank,
  *   scale [adapters] binary32, or NULL (all 1)
  *   ids   [tokens] int32; outside [0, adapters): no adapter, out[t] = y[t]
  *   y, out [tokens, n], rows ldy / ldo elements apart, both bf16 (W4A8_BF16) or
- *         both binary32 (W4A8_F32); out may be y itself (same pointer and stride)
+ *         both binary32 (W4A8_F32); out may be y itself (same pointer and stride) and
+ *         may share memory with x, but with no other row or column of y
  * a[l] x[t] is summed in binary32 (parts of k, added in order) and kept so: the
  * product with b takes it as bf16 terms that hold it to 2^-24; the sum with y is
  * binary32, rounded once to out's type.

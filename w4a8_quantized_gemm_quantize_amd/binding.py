@@ -666,7 +666,8 @@ def lora_add(x, a, b, ids, y, scale=None, out=None, workspace=None, stream=None)
     """out = y + scale[l] * ((x a[l]^T) b[l]^T) with l = ids[t] for each row t (outside the
     adapters: out = y).  x bf16 [tokens, k] and y, out [tokens, n] (both bfloat16 or both
     float32) may have strided rows; a bf16 [adapters, rank, k], b bf16 [adapters, n, rank],
-    ids int32 [tokens], scale float32 [adapters] or None.  out may be y."""
+    ids int32 [tokens], scale float32 [adapters] or None.  out may be y and may share memory
+    with x."""
     fn = "lora_add"
     _dev(a, torch.bfloat16, "a")
     _dev(b, torch.bfloat16, "b")

@@ -618,6 +618,18 @@ bool one_launch(int64_t tokens, int64_t adapters, int64_t rp, int64_t k, int64_t
     return (wgs + ncu - 1) / ncu * rp * k <= kSmallA;
 }
 
+// Whether rows of x (xrow bytes each, xstep apart) and of out share memory.  Views of
+// interleaved columns, one step for both, lie in each other's range and share none.
+bool rows_overlap(const void *x, int64_t xstep, int64_t xrow, const void *out, int64_t ostep,
+                  int64_t orow, int64_t tokens) {
+    const int64_t xa = (int64_t)(uintptr_t)x, oa = (int64_t)(uintptr_t)out;
+    if (xa + (tokens - 1) * xstep + xrow <= oa || oa + (tokens - 1) * ostep + orow <= xa)
+        return false;
+    if (xstep != ostep) return true;
+    const int64_t d = ((oa - xa) % xstep + xstep) % xstep;      // out's row starts this far in
+    return d < xrow || d + orow > xstep;
+}
+
 struct LoraSpace {
     bool plan;
     int bm, rp, slices, kslice;
@@ -738,7 +750,11 @@ hipError_t launch_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, co
     const int64_t tiles = s.plan ? 2 * s.slots : s.slots;
     const int64_t steps = s.plan ? 1 : tiles * ((n + kExpandN - 1) / kExpandN) / 1024;
     p.steps = (int)(steps < 1 ? 1 : steps > 8 ? 8 : steps);
-    const bool small = one_launch(tokens, adapters, s.rp, k, n);
+    // one launch reads x for other columns while it writes out; with two, x is read
+    // before out is written
+    const int64_t es = bf16 ? 2 : 4;
+    const bool small = one_launch(tokens, adapters, s.rp, k, n) &&
+                       !rows_overlap(x, ldx * 2, k * 2, out, ldo * es, n * es, tokens);
     if (small && bf16) launch_lora_small<true>(p, s.rp, stream);
     else if (small) launch_lora_small<false>(p, s.rp, stream);
     else if (s.plan && bf16) launch_lora_rank<true, true>(p, s.rp, stream);
