@@ -80,6 +80,8 @@ struct RouteArgs {
 };
 
 constexpr int kRouteWaves = 4;
+// Tokens of a launch: a grid holds fewer than 2^32 work items, 64 a token.
+constexpr int64_t kRouteLaunch = (int64_t)1 << 25;
 
 // V values at p + i (clamped to the n there are; the lane's own past the end are
 // excluded by the caller).
@@ -335,11 +337,7 @@ hipError_t launch_route(const void *logits, bool bf16, int64_t ld, const float *
                         int32_t groups, int32_t topk_groups, int32_t group_top, bool renorm,
                         float scale, int32_t *ids, float *weights, hipStream_t stream) {
     RouteArgs a;
-    a.logits = logits;
     a.bias = bias;
-    a.ids = ids;
-    a.weights = weights;
-    a.tokens = tokens;
     a.ld = ld;
     a.experts = experts;
     a.top_k = top_k;
@@ -352,9 +350,17 @@ hipError_t launch_route(const void *logits, bool bf16, int64_t ld, const float *
     while ((groups << a.group_shift) > 64) --a.group_shift;
     a.scale = scale;
     a.renorm = renorm;
-    if (sigmoid) launch_route_v<true>(a, bf16, stream);
-    else launch_route_v<false>(a, bf16, stream);
-    return hipGetLastError();
+    for (int64_t t0 = 0; t0 < tokens; t0 += kRouteLaunch) {
+        a.logits = (const uint8_t *)logits + t0 * ld * (bf16 ? 2 : 4);
+        a.ids = ids + t0 * top_k;
+        a.weights = weights + t0 * top_k;
+        a.tokens = tokens - t0 < kRouteLaunch ? tokens - t0 : kRouteLaunch;
+        if (sigmoid) launch_route_v<true>(a, bf16, stream);
+        else launch_route_v<false>(a, bf16, stream);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
 }
 
 }  // namespace w4a8
