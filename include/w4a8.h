@@ -474,7 +474,8 @@ size_t w4a8_moe_ffn_workspace_bytes(int64_t tokens, int32_t experts, int32_t top
  * Requires hidden > 0, inter > 0, both multiples of 64, 1 <= top_k and
  * 1 <= experts (W4A8_ERR_SHAPE); experts <= W4A8_MAX_EXPERTS, top_k <=
  * W4A8_MAX_TOP_K, hidden and inter <= W4A8_K_MAX, tokens * hidden and inter *
- * hidden below 2^31, tokens * top_k <= 2^30, group == 64 (W4A8_ERR_UNSUPPORTED).
+ * hidden below 2^31, tokens * top_k <= 2^30, products of tokens * top_k rows in fewer
+ * than 2^22 tiles of 256 x 256, group == 64 (W4A8_ERR_UNSUPPORTED).
  * The workspace is caller memory, 16-byte aligned, of at least
  * w4a8_moe_ffn_workspace_bytes(...) bytes (W4A8_ERR_SHAPE); calls that share it
  * must be ordered.  out may not alias x.

@@ -142,9 +142,8 @@ w4a8_status check_moe_shape(int64_t tokens, int32_t experts, int32_t top_k, int6
         inter > W4A8_K_MAX || inter * hidden > INT32_MAX || tokens > INT32_MAX / hidden ||
         tokens * top_k > (1 << 30))
         return W4A8_ERR_UNSUPPORTED;
-    // workgroups of the products: row tiles x 256-column tiles
-    const int64_t cols = (2 * inter > hidden ? 2 * inter : hidden) / 256 + 1;
-    if ((tokens * top_k / 16 + experts) * cols > INT32_MAX) return W4A8_ERR_UNSUPPORTED;
+    if (tokens > 0 && !w4a8::moe_fits(tokens, experts, top_k, hidden, inter))
+        return W4A8_ERR_UNSUPPORTED;
     return W4A8_OK;
 }
 

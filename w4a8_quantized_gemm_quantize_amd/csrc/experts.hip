@@ -82,10 +82,15 @@ struct Product {
     SelArgs sel;
 };
 
+// Workgroups of a tiled product: the most tiles there can be, in whole rows of the 8
+// XCDs.
+int64_t tiled_grid(int64_t slots, int64_t n, int bn) {
+    return (slots * ((n + bn - 1) / bn) + 7) / 8 * 8;
+}
+
 template <int BM, int BN, int WM, int WN, int SEL>
 void launch_sel_tiled(const Product &p, hipStream_t stream) {
-    const int64_t most = (int64_t)p.sel.slots * ((p.n + BN - 1) / BN);
-    const int64_t grid = (most + 7) / 8 * 8;             // whole rows of the 8 XCDs
+    const int64_t grid = tiled_grid(p.sel.slots, p.n, BN);
     gemm_tiled_kernel<kW4Sym, BM, BN, WM, WN, 0, SEL>
         <<<dim3((unsigned)grid, 1), 64 * WM * WN, 0, stream>>>(
             (const int8_t *)p.a_q, p.a_s, p.w, p.grp, p.ch, 0, p.n, p.k, p.out, p.ldo,
@@ -371,6 +376,15 @@ MoeSpace moe_space(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidde
 }
 
 }  // namespace
+
+bool moe_fits(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inter) {
+    const MoeSpace s = moe_space(tokens, experts, top_k, hidden, inter);
+    if (s.form != kMoeTiled) return true;
+    const int64_t n = 2 * inter > hidden ? 2 * inter : hidden;
+    const int64_t items = s.bm <= 64 ? tiled_grid(s.slots, n, 128) * 256
+                                     : tiled_grid(s.slots, n, 256) * 1024;
+    return items < (int64_t)1 << 32;
+}
 
 size_t moe_workspace_bytes(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden,
                            int64_t inter) {

@@ -112,6 +112,9 @@ hipError_t launch_plan_quantize(const int32_t *ids, int64_t rows, int32_t groups
                                 float *scales, hipStream_t stream);
 
 // Experts' products (experts.hip), arguments as w4a8_moe_ffn in w4a8.h.
+// moe_fits: every launch holds fewer than 2^32 work items (the runtime runs a larger
+// grid modulo 2^32 and reports no error).
+bool moe_fits(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inter);
 size_t moe_workspace_bytes(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden,
                            int64_t inter);
 hipError_t launch_moe_ffn(const uint16_t *x, const int32_t *ids, const float *weights,

@@ -80,7 +80,8 @@ struct RouteArgs {
 };
 
 constexpr int kRouteWaves = 4;
-// Tokens of a launch: a grid holds fewer than 2^32 work items, 64 a token.
+// Tokens of a launch, 64 work items each: the runtime runs a grid of 2^32 work items or
+// more modulo 2^32 and reports no error.
 constexpr int64_t kRouteLaunch = (int64_t)1 << 25;
 
 // V values at p + i (clamped to the n there are; the lane's own past the end are
