@@ -556,6 +556,12 @@ def _rows(fn, t, dtypes, cols, name):
     return t.stride(0) if t.size(0) > 1 else cols
 
 
+def _addr(t):
+    """A tensor's address; None (a null pointer, refused by the library where a tensor is
+    needed) for None."""
+    return None if t is None else t.data_ptr()
+
+
 def _workspace(stream, need, device):
     """A call's workspace, as _empty; at least 16 bytes."""
     if stream is None:
@@ -587,9 +593,9 @@ def moe_route(logits, top_k: int, bias=None, score: str = "softmax", groups: int
         _sized(fn, weights, _F32, tokens * top_k, "weights")
     _sized(fn, bias, _F32, experts, "bias")
     status = _lib.w4a8_moe_route(
-        logits.data_ptr(), _FLOATS[logits.dtype], ld, None if bias is None else bias.data_ptr(),
-        tokens, experts, top_k, _SCORES[score], groups, topk_groups, group_top,
-        1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), _stream(stream))
+        logits.data_ptr(), _FLOATS[logits.dtype], ld, _addr(bias), tokens, experts, top_k,
+        _SCORES[score], groups, topk_groups, group_top, 1 if renormalize else 0, scale,
+        ids.data_ptr(), weights.data_ptr(), _stream(stream))
     if status:
         raise W4A8Error(fn, status)
     return ids, weights
@@ -623,6 +629,8 @@ def w4a8_moe_ffn(x, ids, weights, w13, w2, inter: int, out_dtype=torch.bfloat16,
     top_k = ids.shape[1]
     p13, g13, c13 = w13
     p2, g2, c2 = w2
+    if c13 is None:                    # the number of experts is its size
+        raise W4A8Error(fn, ERR_NULL)
     if inter <= 0 or c13.numel() % (2 * inter):
         raise W4A8SizeError(fn, "w13 ch_scale", c13.numel(), 2 * inter)
     experts = c13.numel() // (2 * inter)
@@ -648,10 +656,9 @@ def w4a8_moe_ffn(x, ids, weights, w13, w2, inter: int, out_dtype=torch.bfloat16,
     else:
         _sized(fn, workspace, _U8, 0, "workspace")
     status = _lib.w4a8_moe_ffn(
-        x.data_ptr(), ids.data_ptr(), weights.data_ptr(), p13.data_ptr(), g13.data_ptr(),
-        c13.data_ptr(), p2.data_ptr(), g2.data_ptr(), c2.data_ptr(), tokens, experts, top_k,
-        hidden, inter, group, out.data_ptr(), code, workspace.data_ptr(), workspace.numel(),
-        _stream(stream))
+        x.data_ptr(), ids.data_ptr(), _addr(weights), _addr(p13), _addr(g13), c13.data_ptr(),
+        _addr(p2), _addr(g2), _addr(c2), tokens, experts, top_k, hidden, inter, group,
+        out.data_ptr(), code, workspace.data_ptr(), workspace.numel(), _stream(stream))
     if status:
         raise W4A8Error(fn, status)
     return out
@@ -700,9 +707,9 @@ def lora_add(x, a, b, ids, y, scale=None, out=None, workspace=None, stream=None)
     else:
         _sized(fn, workspace, _U8, 0, "workspace")
     status = _lib.w4a8_lora_add(
-        x.data_ptr(), ldx, a.data_ptr(), b.data_ptr(), None if scale is None else scale.data_ptr(),
-        ids.data_ptr(), tokens, adapters, rank, k, n, y.data_ptr(), ldy, out.data_ptr(), ldo,
-        _FLOATS[y.dtype], workspace.data_ptr(), workspace.numel(), _stream(stream))
+        x.data_ptr(), ldx, a.data_ptr(), b.data_ptr(), _addr(scale), _addr(ids), tokens, adapters,
+        rank, k, n, y.data_ptr(), ldy, out.data_ptr(), ldo, _FLOATS[y.dtype],
+        workspace.data_ptr(), workspace.numel(), _stream(stream))
     if status:
         raise W4A8Error(fn, status)
     return out
