@@ -425,7 +425,8 @@ typedef enum {
  *               else x[t, e] itself (the score is monotone in it)
  *   groups > 1: the experts are `groups` equal runs; only the topk_groups groups
  *               with the largest sum of their group_top (1 or 2) largest keys
- *               stay (ties to the lower group)
+ *               stay (ties to the lower group); experts that are never chosen
+ *               (below) add nothing, and a group of such experts alone comes last
  *   ids[t, j]   the top_k largest keys, ties to the lower expert
  *   weights[t, j] = s / (sum of the chosen s) * scale with renormalize (0 where
  *               that sum is 0), else s * scale

@@ -216,12 +216,11 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
             for (int off = 1; off < lanes; off <<= 1)
                 merge2(m1, m2, [off](uint32_t w) { return (uint32_t)__shfl_xor((int)w, off); });
         }
-        // the sum of the group's largest keys; a key that is missing adds nothing
+        // The sum of the group's largest keys; a key that is missing adds nothing.  No
+        // key is -inf or NaN, so the sum is no NaN; one that falls to -inf (two keys
+        // near the lowest value) still ranks above a group without any, which is 0.
         uint32_t rank_key = m1;
-        if (a.group_top == 2) {
-            const float both = key_value(m1) + key_value(m2);
-            rank_key = m2 ? order_key(both, choosable(both)) : m1;
-        }
+        if (a.group_top == 2 && m2) rank_key = order_key(key_value(m1) + key_value(m2), true);
         // Groups that beat this lane's: a larger sum, or an equal one of a lower
         // group.  Which lanes belong to higher groups is a scalar mask.
         int beaten = 0;
