@@ -115,14 +115,15 @@ void launch_sel_skinny(const Product &p, int bm, hipStream_t stream) {
                                             (int64_t)device_cu_count(), p.sel);
 }
 
-// FUSED: the row vectors a lane holds, for rows of up to kFusedRowMax.
-constexpr int64_t kFusedRowMax = 8192;
+// FUSED: the row vectors a lane holds, for rows of up to kFusedRowMax (kSelDirect) or
+// kFusedDownMax (kSelScatter).
+constexpr int64_t kFusedRowMax = 8192, kFusedDownMax = 2160;
 template <int SEL>
 void launch_sel_fused(const Product &p, int bm, hipStream_t stream) {
     if (p.k <= 1024) launch_sel_skinny<SEL, true, 2>(p, bm, stream);
     else if (p.k <= 2048) launch_sel_skinny<SEL, true, 4>(p, bm, stream);
-    else if (p.k <= 4096) launch_sel_skinny<SEL, true, 8>(p, bm, stream);
-    else launch_sel_skinny<SEL, true, 16>(p, bm, stream);
+    else if (SEL == kSelScatter || p.k <= 4096) launch_sel_skinny<SEL, true, 8>(p, bm, stream);
+    else if constexpr (SEL == kSelDirect) launch_sel_skinny<SEL, true, 16>(p, bm, stream);
 }
 
 // ----------------------------------------------------- down, token by token --
@@ -300,17 +301,33 @@ void launch_sel(const Product &p, int bm, hipStream_t stream) {
     else launch_sel_tiled<256, 256, 4, 4, SEL>(p, stream);
 }
 
+// Rows an expert has on average, of those that can have any.
+int64_t rows_an_expert(int64_t rows, int64_t experts) {
+    return rows / (rows < experts ? rows : experts);
+}
+
 // Row block of the products for `rows` rows over `experts` experts, by the rows
-// an expert has on average.  Measured on one box, gate-up + down, us, for blocks of
-// 64 | 128 (128 x 256 tiles) | 256:
+// an expert has on average.  Up to 16: the skinny kernel, whose operand tile has 16
+// rows.  Above, measured on one box, gate-up + down, us, for blocks of 64 | 128 (128 x
+// 256 tiles) | 256:
 //   4096 x 1408, 32 experts: 65 rows an expert 107 | 121 | 151, 160 rows 179 | 186 |
 //   189, 256 rows 252 | 256 | 246, 375 rows 362 | 305 | 290, 512 rows 482 | 425 | 375;
 //   2048 x 1024, 64 experts: 131 rows 124 | 147 | 164, 253 rows 202 | 194 | 179;
 //   4096 x 14336, 8 experts: 1024 rows 2124 | 1683 | 1524.
 int row_block(int64_t rows, int64_t experts) {
-    const int64_t met = rows < experts ? rows : experts;
-    const int64_t avg = rows / met;
-    return avg <= 4 ? 8 : avg <= 16 ? 16 : avg <= 200 ? 64 : 256;
+    const int64_t avg = rows_an_expert(rows, experts);
+    return avg <= 16 ? 16 : avg <= 200 ? 64 : 256;
+}
+
+// Whether the skinny down product takes the codes of its rows itself: a launch less, but
+// each of a tile's hidden / 32 workgroups repeats them and holds 16 rows of K in LDS (34
+// KB at kFusedDownMax, four workgroups per CU).  Measured on one box, us a call, codes taken
+// here | from memory, by rows an expert and K: 2 x 768 36.8 | 39.8; 15 x 1024 24.0 | 27.1;
+// 10 x 1600 35.5 | 36.4; 2 x 2048 63.7 | 63.4; 4 x 2048 77.8 | 75.8; 6 x 2048 32.1 | 33.7; 10
+// x 2112 41.2 | 38.4; 16 x 2048 69.4 | 66.3; with more LDS 2 x 4096 66.8 | 67.2; 15 x 4096
+// 46.4 | 43.1; 2 x 8192 82.8 | 75.9; 4 x 8192 93.2 | 81.3.
+bool fused_down_pays(int64_t rows, int64_t experts, int64_t inter) {
+    return inter <= kFusedDownMax && rows_an_expert(rows, experts) * inter <= 16384;
 }
 
 // Whether a batch is taken row by row (kSelDirect, two launches) rather than
@@ -353,7 +370,7 @@ MoeSpace moe_space(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidde
     s.form = direct_pays(tokens, experts, top_k, hidden, inter)    ? kMoeDirect
              : s.bm <= 16 && hidden >= kChunkK && inter >= kChunkK ? kMoeFew
                                                                    : kMoeTiled;
-    s.fused_down = s.form == kMoeFew && inter <= kFusedRowMax && s.bm * (inter + 16) <= 34 * 1024;
+    s.fused_down = s.form == kMoeFew && fused_down_pays((int64_t)r, experts, inter);
     s.slots = plan_slots((int64_t)r, experts, s.bm);
     size_t at = 0;
     auto take = [&](bool used, size_t bytes) {
