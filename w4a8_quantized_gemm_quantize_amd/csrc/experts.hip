@@ -308,15 +308,16 @@ int64_t rows_an_expert(int64_t rows, int64_t experts) {
 
 // Row block of the products for `rows` rows over `experts` experts, by the rows
 // an expert has on average.  Up to 16: the skinny kernel, whose operand tile has 16
-// rows.  Above, measured on one box, gate-up + down, us, for blocks of 64 | 128 (128 x
-// 256 tiles) | 256:
-//   4096 x 1408, 32 experts: 65 rows an expert 107 | 121 | 151, 160 rows 179 | 186 |
-//   189, 256 rows 252 | 256 | 246, 375 rows 362 | 305 | 290, 512 rows 482 | 425 | 375;
-//   2048 x 1024, 64 experts: 131 rows 124 | 147 | 164, 253 rows 202 | 194 | 179;
-//   4096 x 14336, 8 experts: 1024 rows 2124 | 1683 | 1524.
+// rows.  Above, measured on one box, us a call, for blocks of 64 | 256:
+//   4096 x 1408, 32 experts: 65 rows an expert 123 | 172, 160 rows 218 | 221, 200 rows
+//   253 | 232, 225 rows 279 | 238, 256 rows 307 | 300, 512 rows 565 | 459;
+//   2048 x 1024, 64 experts: 131 rows 159 | 195, 187 rows 202 | 207, 212 rows 225 | 216,
+//   253 rows 258 | 229;
+//   4096 x 14336, 8 experts: 200 rows 554 | 493, 1024 rows 2322 | 1586.
+// (128 x 256 tiles were never ahead of both.)
 int row_block(int64_t rows, int64_t experts) {
     const int64_t avg = rows_an_expert(rows, experts);
-    return avg <= 16 ? 16 : avg <= 200 ? 64 : 256;
+    return avg <= 16 ? 16 : avg < 190 ? 64 : 256;
 }
 
 // Whether the skinny down product takes the codes of its rows itself: a launch less, but
@@ -333,11 +334,11 @@ bool fused_down_pays(int64_t rows, int64_t experts, int64_t inter) {
 // Whether a batch is taken row by row (kSelDirect, two launches) rather than
 // sorted (four): where the weights that two tokens then read separately cost
 // less than two launches and their gaps.  Measured on one box, us, row by row |
-// sorted, by those bytes: 13 MB (4 tokens, 8 of 64 experts 2048 x 768) 20.7 | 25.7;
-// 29 MB (8 tokens, 2 of 8, 2048 x 1024) 17.3 | 23.7; 30 MB (8 tokens, 8 of 128,
-// 2048 x 768) 34.7 | 33.8; 36 MB (4 tokens, 4 of 32, 4096 x 2048) 42.0 | 36.3; 46 MB
-// (2 tokens, 2 of 8, 4096 x 14336) 67.5 | 58.2; 143 MB (8 tokens, 4 of 32, 4096 x
-// 2048) 76.5 | 49.1.
+// sorted, by those bytes: 13 MB (4 tokens, 8 of 64 experts 2048 x 768) 21.3 | 26.8;
+// 26 MB (2 tokens, 4 of 16, 4096 x 4096) 41.8 | 44.6; 29 MB (8 tokens, 2 of 8, 2048 x
+// 1024) 18.6 | 24.8; 30 MB (8 tokens, 8 of 128, 2048 x 768) 35.1 | 34.5; 36 MB (4
+// tokens, 4 of 32, 4096 x 2048) 42.3 | 36.5; 46 MB (2 tokens, 2 of 8, 4096 x 14336) 67.4
+// | 58.9; 143 MB (8 tokens, 4 of 32, 4096 x 2048) 77.3 | 50.7.
 bool direct_pays(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inter) {
     if (tokens * top_k > 64 || hidden > kFusedRowMax || hidden < kChunkK || inter < kChunkK ||
         inter > kTokenKMax)
