@@ -471,7 +471,8 @@ size_t w4a8_moe_ffn_workspace_bytes(int64_t tokens, int32_t experts, int32_t top
  *   y       = the w4a8_gemm output (binary32) of w2 of e
  *   out[t]  = sum over used slots, in order, of weights[t, j] * y  (binary32),
  *             rounded once to out's type; 0 for a token without used slots.
- * The result does not depend on timing (no sum is taken by atomics).
+ * The result does not depend on timing (the only sums taken by atomics are of
+ * integers, and exact).
  * Requires hidden > 0, inter > 0, both multiples of 64, 1 <= top_k and
  * 1 <= experts (W4A8_ERR_SHAPE); experts <= W4A8_MAX_EXPERTS, top_k <=
  * W4A8_MAX_TOP_K, hidden and inter <= W4A8_K_MAX, tokens * hidden and inter *

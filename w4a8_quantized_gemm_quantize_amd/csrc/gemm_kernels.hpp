@@ -216,8 +216,9 @@ struct WeightBatch {
 // KF: the fused prologue keeps the widened activations in registers between its
 // maximum and its codes (fewer VALU instructions, more registers: used when one
 // workgroup per CU is all the grid has, so occupancy does not matter).
-// SEL: rows that choose weights (see above; non-fused, per-token scales only):
-// workgroup (x, y) takes tile y of the table.
+// SEL: rows that choose weights (see above; per-token scales only): workgroup (x, y)
+// takes tile y of the table, or row y itself.  kSelDirect is always FUSED, kSelScatter
+// may be, kSelGateUp is not.
 template <int WF, int MT, int NT, int WAVES, int D, bool FUSED, int AV, int AB = 0,
           bool KF = false, int SEL = kSelNone>
 __global__ __launch_bounds__(64 * WAVES) void gemm_skinny_kernel(

@@ -287,10 +287,10 @@ __global__ __launch_bounds__(256) void lora_terms_kernel(LoraArgs p) {
 // wavefront take the B rows in the order (b_row) in which a 16-byte piece of the
 // result is 4 consecutive columns of a lane, or 8 of two tiles for bf16, and the four
 // lanes of a row hold 64 consecutive bytes: with 64 bytes of a row in one lane,
-// written 16 at a time, expand of 2047 x 8192 binary32 took 39 us.  For decode batches the time is instructions and latencies as
-// much as bytes (2.4 ns a dependent instruction), so B comes through buffer
-// loads whose bounds replace the tests of rank and columns, and addresses only
-// advance.
+// written 16 at a time, expand of 2047 x 8192 binary32 took 39 us.  For decode
+// batches the time is instructions and latencies as much as bytes (2.4 ns a dependent
+// instruction), so B comes through buffer loads whose bounds replace the tests of
+// rank and columns, and addresses only advance.
 constexpr int kExpandN = 64 * kLoraWaves;
 
 // The B row, of a wavefront's 64, that is row m of its operand tile f.
@@ -484,9 +484,10 @@ __global__ __launch_bounds__(64 * kLoraWaves) void lora_expand_kernel(LoraArgs p
 
 // ------------------------------------------------------------------ small --
 // Both products of a small decode batch in one launch (one_launch), A of an adapter
-// read by every workgroup of its rows (from L2): a row tile x 512 columns, eight wavefronts that split K and then the columns.  B and y are on their
-// way while v is formed; v never leaves the workgroup.  Latency is all there is: ids,
-// then A, x, B and y side by side, then the result.
+// read by every workgroup of its rows (from L2): a row tile x 512 columns, eight
+// wavefronts that split K and then the columns.  B and y are on their way while v is
+// formed; v never leaves the workgroup.  Latency is all there is: ids, then A, x, B and
+// y side by side, then the result.
 constexpr int kSmallWaves = 8;
 constexpr int kSmallN = 64 * kSmallWaves;
 
@@ -605,10 +606,11 @@ constexpr int64_t kBallotRows = 64;
 
 // One launch (lora_small_kernel) where reading A again in every workgroup costs less
 // than the second launch: by the elements of A (ranks padded) that a CU reads, at
-// about 64 bytes a clock.  Measured, one launch | two, us per call: 8 rows of rank 16,
-// 4096 x 4096 10.4 | 12.5; 1 row, 8904 x 11040 11.4 | 12.5; 20 rows of rank 8, 6384 x
-// 3096 10.9 | 14; 8 rows of rank 16, 8192 x 4096 13.0 | 12.9, 16384 x 4096 22 | 12.7; 32
-// rows of rank 32, 8192 x 8192 41 | 12.5; 64 rows, 4096 x 14336 53 | 15.
+// about 64 bytes a clock.  Measured, one launch | two, us per call (two are bound by the
+// host at 14.7): 8 rows of rank 16, 4096 x 4096 12.1 | 15.2; 1 row, 8904 x 11040 11.9 |
+// 14.9; 20 rows of rank 8, 6384 x 3096 12.2 | 14.8; 8 rows of rank 16, 8192 x 4096 14.2 |
+// 14.6, 16384 x 4096 23.6 | 14.8; 4 rows of rank 64, 4096 x 4096 20.9 | 14.8; 32 rows of
+// rank 32, 8192 x 8192 43 | 14.8; 64 rows of rank 16, 4096 x 14336 54 | 15.8.
 constexpr int64_t kSmallA = 144 * 1024;
 bool one_launch(int64_t tokens, int64_t adapters, int64_t rp, int64_t k, int64_t n) {
     if (tokens > kBallotRows || rp > 64) return false;

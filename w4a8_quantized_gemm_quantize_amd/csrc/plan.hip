@@ -126,8 +126,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs p) {
 
 // The plan in workgroups 0 .. groups, then the rows' codes and scales
 // (act_scale_pair_rcp), a wavefront per row: neither depends on the other, and
-// side by side they cost one launch and the longer of the two.  V vectors (8 elements) per lane stay in registers;
-// longer rows are read a second time.
+// side by side they cost one launch and the longer of the two.  V vectors (8
+// elements) per lane stay in registers; longer rows are read a second time.
 template <int V>
 __global__ __launch_bounds__(kPlanThreads) void plan_quantize_kernel(
     PlanArgs p, const u32x4 *__restrict__ x, int64_t xrows, int vecs, u32x2 *__restrict__ q,
