@@ -524,6 +524,136 @@ w4a8_status w4a8_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, con
                           void *workspace, size_t ws_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Attention over an 8-bit cache: norms and rotation of queries and keys, a
+ * paged cache of int8 codes with a scale per page and head that they are
+ * written to and read from, and the attention that reads it.
+ *
+ * The cache:
+ *   kv       [pages, kv_heads, 2, page, head_dim] bytes: keys, then values of a
+ *            page and head, in operand order inside (opaque, layout V1)
+ *   kv_scale [pages, kv_heads, 2] binary32: of the keys, of the values
+ * A batch of `seqs` sequences names its tokens by
+ *   block_table [seqs] x blocks int32, rows `ldb` entries apart: the page of each
+ *            run of `page` tokens; an entry outside [0, pages) is no page: its
+ *            tokens are not written, read as zeros and not attended to
+ *   lens     [seqs] int32: tokens of each sequence, the batch's own among them
+ *   row_start [seqs + 1] int32, non-decreasing, or NULL: rows row_start[s] ..
+ *            row_start[s + 1] - 1 of the batch belong to sequence s, rows behind
+ *            row_start[seqs] to none; NULL: one row a sequence, rows == seqs
+ * The n rows of a sequence are its last tokens: row i is token lens[s] - n + i (a
+ * row whose token would be negative has none).  These three arrays need only their
+ * own 4-byte alignment.  Tensors of rows are [rows, heads, head_dim], heads
+ * contiguous, rows `ld` elements apart (columns of a fused projection's output).
+ * Common rules: head_dim a multiple of 32, kv_heads >= 1, blocks >= 0, ldb >= blocks,
+ * ld at least a row and a multiple of 8 (bf16) or 4 (binary32) (W4A8_ERR_SHAPE);
+ * head_dim <= 256, page 16, 32, 64 or 128, kv_heads <= 1024, rows, seqs and blocks * page
+ * at most 2^30, pages below 2^31, and fewer than 2^24 workgroups (W4A8_ERR_UNSUPPORTED).
+ * ------------------------------------------------------------------------ */
+
+#define W4A8_KV_LAYOUT_V1 1
+#define W4A8_HEAD_DIM_MAX 256
+#define W4A8_KV_HEADS_MAX 1024
+
+/*
+ * Norms of queries and keys per head, and the rotation by position, in one pass.
+ *   q [tokens, q_heads, head_dim], k [tokens, kv_heads, head_dim], rows ldq, ldk
+ *            apart, both binary32 or both bf16 (in_dtype)
+ *   q_weight, k_weight [head_dim] binary32, or NULL: that tensor is not normed
+ *   cos_sin  [max_pos, rot] binary32: rot / 2 cosines, then rot / 2 sines
+ *   positions [tokens] int32 (4-byte aligned)
+ *   q_out, k_out of out_dtype (binary32 or bf16); each may be its input (same pointer,
+ *            type and stride), and overlap no input otherwise
+ *   y = x * (1 / sqrt(sum x^2 / head_dim + eps)) * w;  of the first `rot` elements the
+ *   pairs (a, b) = (y[j], y[j + rot / 2]), or (y[2 j], y[2 j + 1]) with `interleaved`,
+ *   become (a c - b s, b c + a s), c and s entry j of the position's row.
+ * Binary32 throughout, one rounding at the end.  A row whose position is outside
+ * [0, max_pos) is left as it was.  rot == 0: no rotation (cos_sin and positions unused).
+ * Requires q_heads, kv_heads >= 0 with a head in all, head_dim a positive multiple of 8,
+ * 0 <= rot <= head_dim, rot a multiple of 8, max_pos >= 0 (W4A8_ERR_SHAPE); head_dim <=
+ * 256, fewer than 2^24 workgroups (tokens * heads / 8 at most) (W4A8_ERR_UNSUPPORTED).
+ */
+w4a8_status w4a8_qk_norm_rope(const void *q, int64_t ldq, const void *k, int64_t ldk,
+                              w4a8_dtype in_dtype, const float *q_weight, const float *k_weight,
+                              float eps, const float *cos_sin, const int32_t *positions,
+                              int64_t max_pos, int32_t rot, int32_t interleaved, int64_t tokens,
+                              int32_t q_heads, int32_t kv_heads, int32_t head_dim, void *q_out,
+                              int64_t ldqo, void *k_out, int64_t ldko, w4a8_dtype out_dtype,
+                              hipStream_t stream);
+
+/*
+ * Quantizes new keys and values as they are written into the cache.
+ *   k, v  [rows, kv_heads, head_dim], both binary32 or both bf16
+ * Per page written to and head, for keys and for values:
+ *   a = max |x| over the page's new tokens, s = a / 127;
+ *   a page that also holds older tokens of the sequence (before its first row) keeps its
+ *   scale s_old unless s > s_old, and then the older codes become
+ *   clamp(round_half_even(code * (s_old / s)), -127, 127);
+ *   new codes clamp(round_half_even(x * inv), -127, 127), inv = 1 / scale (0 where the
+ *   scale is 0), each operation rounded to binary32.
+ * A page's older tokens lose at most half a step of its scale each time that grows.
+ * Tokens behind the last are left as they were.  A page must not be written for two
+ * sequences in one call (a shared page that is not full is the caller's to copy).
+ */
+w4a8_status w4a8_kv8_write(const void *k, int64_t ldk, const void *v, int64_t ldv,
+                           w4a8_dtype dtype, const int32_t *block_table, int64_t ldb,
+                           int32_t blocks, const int32_t *lens, const int32_t *row_start,
+                           int64_t seqs, int64_t rows, int32_t kv_heads, int32_t head_dim,
+                           int32_t page, int64_t pages, uint8_t *kv, float *kv_scale,
+                           hipStream_t stream);
+
+/*
+ * Reads the last row_start[s + 1] - row_start[s] tokens of each sequence back:
+ *   k, v  [rows, kv_heads, head_dim], both binary32 or both bf16: code * scale (one
+ *         binary32 product), rounded to bf16; zeros for tokens without a page.
+ * Rows of no token (behind the last sequence, before a sequence's start) are left as
+ * they were.
+ */
+w4a8_status w4a8_kv8_read(const uint8_t *kv, const float *kv_scale, const int32_t *block_table,
+                          int64_t ldb, int32_t blocks, const int32_t *lens,
+                          const int32_t *row_start, int64_t seqs, int64_t rows,
+                          int32_t kv_heads, int32_t head_dim, int32_t page, int64_t pages,
+                          void *k, int64_t ldk, void *v, int64_t ldv, w4a8_dtype dtype,
+                          hipStream_t stream);
+
+/* Bytes of workspace w4a8_attn_kv8 needs for these sizes (0: none, or sizes it refuses);
+ * `ragged` is whether row_start is given. */
+size_t w4a8_attn_kv8_workspace_bytes(int64_t rows, int64_t seqs, int32_t ragged,
+                                     int64_t max_rows, int32_t blocks, int32_t q_heads,
+                                     int32_t kv_heads, int32_t head_dim, int32_t page);
+
+/*
+ * Attention of a batch's rows over the cache (which holds their own tokens already).
+ *   q    [rows, q_heads, head_dim] bf16; query head h reads cache head
+ *        h / (q_heads / kv_heads)
+ *   out  [rows, q_heads, head_dim] bf16;  lse [rows, q_heads] binary32, or NULL
+ * Row i of the n of a sequence sits at p = lens[s] - n + i and sees the tokens j in
+ * [0, lens[s]) that have a page, with j <= p where `causal`, and j > p - window where
+ * window > 0:
+ *   S_j = scale * sum_d q_d k_jd,  out = sum_j exp(S_j) v_j / sum_j exp(S_j),
+ *   lse = ln sum_j exp(S_j);  a row that sees nothing: out 0, lse -inf.
+ * k_j and v_j are code * scale.  Products are exact and summed in binary32, exp(S_j)
+ * enters the sum over v_j rounded to 11 bits, the statistics are binary32, and out is
+ * rounded once.  The result does not depend on timing.
+ * max_rows bounds a sequence's rows: of one with more only the first max_rows are
+ * computed, the rest left as they were, like rows behind the last sequence.
+ * Requires q_heads a positive multiple of kv_heads, max_rows >= 1, window >= 0
+ * (W4A8_ERR_SHAPE); q_heads / kv_heads <= 64, rows * q_heads / kv_heads and window at
+ * most 2^30 (W4A8_ERR_UNSUPPORTED).
+ * out may not alias q.
+ * The workspace (16-byte aligned caller memory of at least
+ * w4a8_attn_kv8_workspace_bytes(...) bytes, W4A8_ERR_SHAPE) is needed where that is
+ * not 0; calls that share it must be ordered.
+ */
+w4a8_status w4a8_attn_kv8(const uint16_t *q, int64_t ldq, const uint8_t *kv,
+                          const float *kv_scale, const int32_t *block_table, int64_t ldb,
+                          int32_t blocks, const int32_t *lens, const int32_t *row_start,
+                          int64_t seqs, int64_t rows, int64_t max_rows, int32_t q_heads,
+                          int32_t kv_heads, int32_t head_dim, int32_t page, int64_t pages,
+                          int32_t causal, int32_t window, float scale, uint16_t *out,
+                          int64_t ldo, float *lse, void *workspace, size_t ws_bytes,
+                          hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Measurement aid (not part of the method): the int8 matrix-core reference
  * that the GEMMs' utilisation is compared with, and the shader clock.
  * ------------------------------------------------------------------------ */

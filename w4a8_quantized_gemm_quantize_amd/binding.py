@@ -74,6 +74,18 @@ _SIGS = {
     "w4a8_lora_workspace_bytes": ([_I64, _I32, _I32, _I64], ctypes.c_size_t),
     "w4a8_lora_add": ([_P, _I64, _P, _P, _P, _P, _I64, _I32, _I32, _I64, _I64, _P, _I64, _P,
                        _I64, ctypes.c_int, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "w4a8_qk_norm_rope": ([_P, _I64, _P, _I64, ctypes.c_int, _P, _P, ctypes.c_float, _P, _P, _I64,
+                           _I32, _I32, _I64, _I32, _I32, _I32, _P, _I64, _P, _I64, ctypes.c_int,
+                           _P], ctypes.c_int),
+    "w4a8_kv8_write": ([_P, _I64, _P, _I64, ctypes.c_int, _P, _I64, _I32, _P, _P, _I64, _I64, _I32,
+                        _I32, _I32, _I64, _P, _P, _P], ctypes.c_int),
+    "w4a8_kv8_read": ([_P, _P, _P, _I64, _I32, _P, _P, _I64, _I64, _I32, _I32, _I32, _I64, _P, _I64,
+                       _P, _I64, ctypes.c_int, _P], ctypes.c_int),
+    "w4a8_attn_kv8_workspace_bytes": ([_I64, _I64, _I32, _I64, _I32, _I32, _I32, _I32, _I32],
+                                      ctypes.c_size_t),
+    "w4a8_attn_kv8": ([_P, _I64, _P, _P, _P, _I64, _I32, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32,
+                       _I32, _I64, _I32, _I32, ctypes.c_float, _P, _I64, _P, _P, ctypes.c_size_t,
+                       _P], ctypes.c_int),
     "w4a8_gemm_bf16act_noalloc": ([_P, _P, _P, _P, _I64, _I64, _I64, _I32, _P, ctypes.c_int, _P],
                                   ctypes.c_int),
 }
@@ -713,6 +725,240 @@ def lora_add(x, a, b, ids, y, scale=None, out=None, workspace=None, stream=None)
     if status:
         raise W4A8Error(fn, status)
     return out
+
+
+# --------------------------------------- attention over an 8-bit cache --
+
+def _heads(fn, t, dtypes, name, rows=None, heads=None, dim=None):
+    """A 3-D CUDA tensor [rows, heads, head_dim] of one of `dtypes` (of these sizes where
+    given) whose rows are contiguous; returns the elements from one row to the next."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{fn}: {name} must be a [rows, heads, head_dim] CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{fn}: {name} must be of dtype {' or '.join(map(str, dtypes))}, "
+                         f"not {t.dtype}")
+    r, h, d = t.shape
+    for have, need, what in ((r, rows, "rows"), (h, heads, "heads"), (d, dim, "head_dim")):
+        if need is not None and have != need:
+            raise W4A8SizeError(fn, f"{name} ({what})", have, need)
+    if t.is_contiguous():
+        return h * d
+    sr, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (h > 1 and sh != d):
+        raise ValueError(f"{fn}: rows of {name} must be contiguous")
+    return sr if r > 1 else h * d
+
+
+def _here(fn, device, *tensors):
+    """A launch goes to the current device: its tensors must be there."""
+    at = _raw_device() if _raw_device is not None else torch.cuda.current_device()
+    if device.index != at:
+        raise ValueError(f"{fn}: tensors are on {device}, the current device is cuda:{at}")
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"{fn}: tensors are on {device} and on {t.device}")
+
+
+_I32T = (torch.int32,)
+
+
+def qk_norm_rope(q, k, cos_sin=None, positions=None, q_weight=None, k_weight=None,
+                 eps: float = 1e-6, interleaved: bool = False, out_dtype=None, q_out=None,
+                 k_out=None, stream=None):
+    """RMS norms per head and the rotation by position of q [tokens, q_heads, head_dim] and k
+    [tokens, kv_heads, head_dim] (both float32 or both bfloat16; rows may be strided, e.g.
+    columns of a fused projection) -> (q_out, k_out), out_dtype (default: the inputs').
+
+    q_weight and k_weight float32 [head_dim], None: not normed; cos_sin float32 [max_pos,
+    rot] (rot / 2 cosines, then rot / 2 sines; None: no rotation) and positions int32
+    [tokens]; a row whose position is outside the table is left as it was.  Pairs are rot / 2
+    apart, or neighbours where interleaved.  q_out and k_out may be q and k."""
+    fn = "qk_norm_rope"
+    ldq = _heads(fn, q, _FLOATS, "q")
+    tokens, q_heads, dim = q.shape
+    ldk = _heads(fn, k, (q.dtype,), "k", tokens, None, dim)
+    kv_heads = k.size(1)
+    if out_dtype is None:
+        out_dtype = (q_out if q_out is not None else k_out if k_out is not None else q).dtype
+    if out_dtype not in _FLOATS:
+        raise ValueError(f"{fn}: out_dtype must be float32 or bfloat16")
+    if q_out is None:
+        q_out, ldqo = _empty(stream, (tokens, q_heads, dim), out_dtype, q.device), q_heads * dim
+    else:
+        ldqo = _heads(fn, q_out, (out_dtype,), "q_out", tokens, q_heads, dim)
+    if k_out is None:
+        k_out, ldko = _empty(stream, (tokens, kv_heads, dim), out_dtype, q.device), kv_heads * dim
+    else:
+        ldko = _heads(fn, k_out, (out_dtype,), "k_out", tokens, kv_heads, dim)
+    _sized(fn, q_weight, _F32, dim, "q_weight")
+    _sized(fn, k_weight, _F32, dim, "k_weight")
+    max_pos = rot = 0
+    if cos_sin is not None:
+        _sized(fn, cos_sin, _F32, 0, "cos_sin")
+        if cos_sin.dim() != 2:
+            raise ValueError(f"{fn}: cos_sin must be [max_pos, rot]")
+        max_pos, rot = cos_sin.shape
+        _sized(fn, positions, _I32T, tokens, "positions")
+    else:
+        positions = None
+    _here(fn, q.device, k, cos_sin, positions, q_weight, k_weight, q_out, k_out)
+    status = _lib.w4a8_qk_norm_rope(
+        q.data_ptr(), ldq, k.data_ptr(), ldk, _FLOATS[q.dtype], _addr(q_weight), _addr(k_weight),
+        eps, _addr(cos_sin), _addr(positions), max_pos, rot, 1 if interleaved else 0, tokens,
+        q_heads, kv_heads, dim, q_out.data_ptr(), ldqo, k_out.data_ptr(), ldko,
+        _FLOATS[out_dtype], _stream(stream))
+    if status:
+        raise W4A8Error(fn, status)
+    return q_out, k_out
+
+
+def kv8_cache(pages: int, kv_heads: int, head_dim: int, page: int, device="cuda"):
+    """An empty paged 8-bit cache: (kv uint8 [pages, kv_heads, 2, page, head_dim], opaque
+    inside; kv_scale float32 [pages, kv_heads, 2])."""
+    kv = torch.zeros((pages, kv_heads, 2, page, head_dim), dtype=torch.uint8, device=device)
+    return kv, torch.zeros((pages, kv_heads, 2), dtype=torch.float32, device=device)
+
+
+def _kv_args(fn, kv, kv_scale, block_table, lens, row_start, rows):
+    """Checks what the calls on the cache share; (ldb, blocks, seqs, rows)."""
+    if not isinstance(kv, torch.Tensor) or kv.dim() != 5 or kv.size(2) != 2:
+        raise ValueError(f"{fn}: kv must be [pages, kv_heads, 2, page, head_dim]")
+    _sized(fn, kv, (torch.uint8,), 0, "kv")
+    if not isinstance(kv_scale, torch.Tensor):
+        raise ValueError(f"{fn}: kv_scale must be [pages, kv_heads, 2]")
+    _sized(fn, kv_scale, _F32, kv.size(0) * kv.size(1) * 2, "kv_scale")
+    if not isinstance(lens, torch.Tensor) or lens.dim() != 1:
+        raise ValueError(f"{fn}: lens must be [seqs]")
+    _sized(fn, lens, _I32T, 0, "lens")
+    seqs = lens.size(0)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError(f"{fn}: block_table must be [seqs, blocks]")
+    blocks = block_table.size(1)
+    ldb = _rows(fn, block_table, _I32T, blocks, "block_table")
+    if block_table.size(0) != seqs:
+        raise W4A8SizeError(fn, "block_table (rows)", block_table.size(0), seqs)
+    if row_start is not None:
+        _sized(fn, row_start, _I32T, seqs + 1, "row_start")
+    elif rows is None:
+        rows = seqs
+    _here(fn, kv.device, kv_scale, block_table, lens, row_start)
+    return ldb, blocks, seqs, rows
+
+
+def kv8_write(k, v, kv, kv_scale, block_table, lens, row_start=None, stream=None):
+    """Quantizes new rows k and v [rows, kv_heads, head_dim] (both float32 or both bfloat16,
+    rows may be strided) into the cache: sequence s's rows row_start[s] .. row_start[s + 1] - 1
+    (row_start None: its one row s) are its last tokens, lens int32 [seqs] counts all of them,
+    block_table int32 [seqs, blocks] names the page of each run of `page` tokens (-1: none).
+    One scale per page and head: older codes of a page are taken over to a scale that grew."""
+    fn = "kv8_write"
+    ldk = _heads(fn, k, _FLOATS, "k")
+    rows, heads, dim = k.shape
+    ldv = _heads(fn, v, (k.dtype,), "v", rows, heads, dim)
+    ldb, blocks, seqs, _ = _kv_args(fn, kv, kv_scale, block_table, lens, row_start, rows)
+    pages, kv_heads, _, page, kv_dim = kv.shape
+    if heads != kv_heads or dim != kv_dim:
+        raise W4A8SizeError(fn, "a row of k", heads * dim, kv_heads * kv_dim)
+    _here(fn, kv.device, k, v)
+    status = _lib.w4a8_kv8_write(
+        k.data_ptr(), ldk, v.data_ptr(), ldv, _FLOATS[k.dtype], block_table.data_ptr(), ldb, blocks,
+        lens.data_ptr(), _addr(row_start), seqs, rows, kv_heads, dim, page, pages, kv.data_ptr(),
+        kv_scale.data_ptr(), _stream(stream))
+    if status:
+        raise W4A8Error(fn, status)
+
+
+def kv8_read(kv, kv_scale, block_table, lens, row_start=None, tokens=None,
+             out_dtype=torch.bfloat16, k=None, v=None, stream=None):
+    """The last row_start[s + 1] - row_start[s] tokens of each sequence out of the cache
+    (row_start None: the last one) -> (k, v) [tokens, kv_heads, head_dim], float32 or bfloat16;
+    `tokens` is row_start's last entry.  Tokens without a page read as zeros, rows of no
+    token are left as they were."""
+    fn = "kv8_read"
+    if tokens is None and row_start is not None:
+        if k is None:
+            raise ValueError(f"{fn}: tokens (or k and v) must be given with row_start")
+        tokens = k.size(0)
+    ldb, blocks, seqs, tokens = _kv_args(fn, kv, kv_scale, block_table, lens, row_start, tokens)
+    pages, kv_heads, _, page, dim = kv.shape
+    if k is not None:
+        out_dtype = k.dtype
+    elif v is not None:
+        out_dtype = v.dtype
+    if out_dtype not in _FLOATS:
+        raise ValueError(f"{fn}: out_dtype must be float32 or bfloat16")
+    if k is None:
+        k, ldk = _empty(stream, (tokens, kv_heads, dim), out_dtype, kv.device), kv_heads * dim
+    else:
+        ldk = _heads(fn, k, (out_dtype,), "k", tokens, kv_heads, dim)
+    if v is None:
+        v, ldv = _empty(stream, (tokens, kv_heads, dim), out_dtype, kv.device), kv_heads * dim
+    else:
+        ldv = _heads(fn, v, (out_dtype,), "v", tokens, kv_heads, dim)
+    _here(fn, kv.device, k, v)
+    status = _lib.w4a8_kv8_read(
+        kv.data_ptr(), kv_scale.data_ptr(), block_table.data_ptr(), ldb, blocks, lens.data_ptr(),
+        _addr(row_start), seqs, tokens, kv_heads, dim, page, pages, k.data_ptr(), ldk, v.data_ptr(),
+        ldv, _FLOATS[out_dtype], _stream(stream))
+    if status:
+        raise W4A8Error(fn, status)
+    return k, v
+
+
+@functools.lru_cache(maxsize=4096)
+def attn_kv8_workspace_bytes(rows: int, seqs: int, ragged: bool, max_rows: int, blocks: int,
+                             q_heads: int, kv_heads: int, head_dim: int, page: int) -> int:
+    """Workspace of attn_kv8 for `rows` query rows of `seqs` sequences (at most max_rows each,
+    `ragged`: with row_start) whose block tables hold `blocks` pages; 0: none."""
+    return int(_lib.w4a8_attn_kv8_workspace_bytes(rows, seqs, 1 if ragged else 0, max_rows, blocks,
+                                                  q_heads, kv_heads, head_dim, page))
+
+
+def attn_kv8(q, kv, kv_scale, block_table, lens, row_start=None, max_rows=None,
+             causal: bool = True, window: int = 0, scale=None, want_lse: bool = False, out=None,
+             lse=None, workspace=None, stream=None):
+    """Attention of q bfloat16 [rows, q_heads, head_dim] (rows may be strided) over the cache
+    -> out bfloat16 [rows, q_heads, head_dim], and with want_lse (or lse given) also the
+    logarithm of the softmax's sum, float32 [rows, q_heads].
+
+    Sequence s's rows row_start[s] .. row_start[s + 1] - 1 (None: its one row s) are its last
+    tokens; they must be in the cache already (kv8_write).  max_rows bounds a sequence's rows
+    (default: all rows).  scale defaults to head_dim ** -0.5; window > 0: only the last
+    `window` tokens up to the row's own.  A row that sees nothing gives 0 and -inf."""
+    fn = "attn_kv8"
+    ldq = _heads(fn, q, (torch.bfloat16,), "q")
+    rows, q_heads, dim = q.shape
+    ldb, blocks, seqs, _ = _kv_args(fn, kv, kv_scale, block_table, lens, row_start, rows)
+    pages, kv_heads, _, page, kv_dim = kv.shape
+    if dim != kv_dim:
+        raise W4A8SizeError(fn, "a head of q", dim, kv_dim)
+    if max_rows is None:
+        max_rows = 1 if row_start is None else max(rows, 1)
+    if out is None:
+        out, ldo = _empty(stream, (rows, q_heads, dim), torch.bfloat16, q.device), q_heads * dim
+    else:
+        ldo = _heads(fn, out, (torch.bfloat16,), "out", rows, q_heads, dim)
+    if lse is not None:
+        _sized(fn, lse, _F32, rows * q_heads, "lse")
+    elif want_lse:
+        lse = _empty(stream, (rows, q_heads), torch.float32, q.device)
+    if workspace is None:
+        need = attn_kv8_workspace_bytes(rows, seqs, row_start is not None, max_rows, blocks,
+                                        q_heads, kv_heads, dim, page)
+        if need:
+            workspace = _workspace(stream, need, q.device)
+    else:
+        _sized(fn, workspace, _U8, 0, "workspace")
+    _here(fn, kv.device, q, out, lse, workspace)
+    status = _lib.w4a8_attn_kv8(
+        q.data_ptr(), ldq, kv.data_ptr(), kv_scale.data_ptr(), block_table.data_ptr(), ldb, blocks,
+        lens.data_ptr(), _addr(row_start), seqs, rows, max_rows, q_heads, kv_heads, dim, page, pages,
+        1 if causal else 0, window, dim ** -0.5 if scale is None else scale, out.data_ptr(), ldo,
+        _addr(lse), _addr(workspace), 0 if workspace is None else workspace.numel(),
+        _stream(stream))
+    if status:
+        raise W4A8Error(fn, status)
+    return out if lse is None else (out, lse)
 
 
 # -------------------------------------------------------- measurement aid --

@@ -19,7 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libw4a8.so")
 SOURCES = ["abi.hip", "quantize.hip", "pack.hip", "gemm_w4.hip", "gemm_lqq.hip", "gemm_w8.hip", "equarx.hip", "gemm_blockact.hip", "probe.hip", "noalloc.hip",
-           "plan.hip", "route.hip", "experts.hip", "lora.hip"]
+           "plan.hip", "route.hip", "experts.hip", "lora.hip", "rope.hip",
+           "kv8.hip", "attn.hip"]
 ARCH = "gfx950"
 
 

@@ -178,6 +178,58 @@ w4a8_status split_workspace(void *workspace, size_t ws_bytes, int64_t m, int64_t
     return W4A8_OK;
 }
 
+bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+
+// Workgroups of 256 of one launch: fewer than 2^32 work items (the runtime runs a larger
+// grid modulo 2^32 and reports no error).
+constexpr int64_t kMaxGrid = (int64_t)1 << 24;
+
+// What the calls on the paged cache share.
+w4a8_status check_kv_call(const w4a8::KvCall &c, int64_t seqs, int64_t pages) {
+    if (c.rows < 0 || seqs < 0 || pages < 0 || c.blocks < 0 || c.ldb < c.blocks || c.kv_heads < 1 ||
+        c.dim <= 0 || c.dim % 32 != 0 || c.page <= 0)
+        return W4A8_ERR_SHAPE;
+    if (c.dim > W4A8_HEAD_DIM_MAX || c.kv_heads > W4A8_KV_HEADS_MAX ||
+        (c.page != 16 && c.page != 32 && c.page != 64 && c.page != 128) ||
+        c.rows > (1 << 30) || seqs > (1 << 30) || pages > INT32_MAX ||
+        (int64_t)c.blocks * c.page > (1 << 30))
+        return W4A8_ERR_UNSUPPORTED;
+    if (!c.start && c.rows != seqs) return W4A8_ERR_SHAPE;
+    return W4A8_OK;
+}
+w4a8_status check_attn_shape(const w4a8::KvCall &c, int64_t seqs, int64_t max_rows,
+                             int32_t q_heads) {
+    if (max_rows < 1 || q_heads < 1 || q_heads % c.kv_heads != 0) return W4A8_ERR_SHAPE;
+    if (q_heads / c.kv_heads > 64 || c.rows * (q_heads / c.kv_heads) > (1 << 30))
+        return W4A8_ERR_UNSUPPORTED;
+    if (w4a8::attn_grid(c.rows, seqs, c.start != nullptr, max_rows, (int64_t)c.blocks * c.page,
+                        q_heads, c.kv_heads) >= kMaxGrid)
+        return W4A8_ERR_UNSUPPORTED;
+    return W4A8_OK;
+}
+// Rows of `heads` heads, `ld` elements apart.
+bool row_stride_ok(int64_t ld, int64_t heads, int64_t dim, bool bf16) {
+    return ld >= heads * dim && ld % (bf16 ? 8 : 4) == 0;
+}
+w4a8_status check_kv_pointers(const w4a8::KvCall &c, const void *kv, const void *kv_scale) {
+    if (!c.lens || (c.blocks > 0 && !c.table) || (c.pages > 0 && (!kv || !kv_scale)))
+        return W4A8_ERR_NULL;
+    if (!aligned4(c.lens) || !aligned4(c.table) || !aligned4(c.start) || !aligned16(kv) ||
+        !aligned16(kv_scale))
+        return W4A8_ERR_MISALIGNED;
+    return W4A8_OK;
+}
+// Debug mode: the rows of a strided tensor.
+w4a8_status debug_check_rows(hipStream_t stream, const void *p, int64_t rows, int64_t ld,
+                             int64_t cols, bool bf16) {
+    w4a8_status st = W4A8_OK;
+    if (debug_sync_enabled())
+        for (int64_t t = 0; t < rows && st == W4A8_OK; ++t)
+            st = debug_check_inputs(
+                stream, {{(const uint8_t *)p + t * ld * (bf16 ? 2 : 4), (size_t)cols, bf16}});
+    return st;
+}
+
 }  // namespace
 
 extern "C" {
@@ -608,6 +660,154 @@ w4a8_status w4a8_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, con
     }
     return finish(w4a8::launch_lora_add(x, ldx, a, b, ids, scale, tokens, adapters, rank, k, n, y,
                                         ldy, out, ldo, dtype == W4A8_BF16, workspace, stream),
+                  stream);
+}
+
+/* ------------------------------------- attention over the 8-bit cache */
+
+w4a8_status w4a8_qk_norm_rope(const void *q, int64_t ldq, const void *k, int64_t ldk,
+                              w4a8_dtype in_dtype, const float *q_weight, const float *k_weight,
+                              float eps, const float *cos_sin, const int32_t *positions,
+                              int64_t max_pos, int32_t rot, int32_t interleaved, int64_t tokens,
+                              int32_t q_heads, int32_t kv_heads, int32_t head_dim, void *q_out,
+                              int64_t ldqo, void *k_out, int64_t ldko, w4a8_dtype out_dtype,
+                              hipStream_t stream) {
+    const bool in = in_dtype == W4A8_BF16, out = out_dtype == W4A8_BF16;
+    if (tokens < 0 || q_heads < 0 || kv_heads < 0 || (int64_t)q_heads + kv_heads < 1 ||
+        head_dim <= 0 || head_dim % 8 != 0 || rot < 0 || rot > head_dim || rot % 8 != 0 ||
+        max_pos < 0)
+        return W4A8_ERR_SHAPE;
+    if ((!in && in_dtype != W4A8_F32) || (!out && out_dtype != W4A8_F32) ||
+        head_dim > W4A8_HEAD_DIM_MAX || (int64_t)q_heads + kv_heads > (1 << 20) ||
+        tokens >= kMaxGrid ||
+        w4a8::qk_norm_rope_grid(tokens, q_heads + kv_heads, head_dim) >= kMaxGrid)
+        return W4A8_ERR_UNSUPPORTED;
+    if ((q_heads && (!row_stride_ok(ldq, q_heads, head_dim, in) ||
+                     !row_stride_ok(ldqo, q_heads, head_dim, out))) ||
+        (kv_heads && (!row_stride_ok(ldk, kv_heads, head_dim, in) ||
+                      !row_stride_ok(ldko, kv_heads, head_dim, out))))
+        return W4A8_ERR_SHAPE;
+    if ((q && q == q_out && q_heads && (ldq != ldqo || in != out)) ||
+        (k && k == k_out && kv_heads && (ldk != ldko || in != out)))
+        return W4A8_ERR_SHAPE;
+    if (tokens == 0) return W4A8_OK;
+    if ((q_heads && (!q || !q_out)) || (kv_heads && (!k || !k_out)) ||
+        (rot && (!positions || (max_pos && !cos_sin))))
+        return W4A8_ERR_NULL;
+    if ((q_heads && (!aligned16(q) || !aligned16(q_out))) ||
+        (kv_heads && (!aligned16(k) || !aligned16(k_out))) || !aligned16(q_weight) ||
+        !aligned16(k_weight) || (rot && (!aligned4(positions) || !aligned16(cos_sin))))
+        return W4A8_ERR_MISALIGNED;
+    w4a8_status st = debug_check_inputs(stream, {{q_weight, (size_t)head_dim, false},
+                                                 {k_weight, (size_t)head_dim, false}});
+    if (st == W4A8_OK && q_heads)
+        st = debug_check_rows(stream, q, tokens, ldq, (int64_t)q_heads * head_dim, in);
+    if (st == W4A8_OK && kv_heads)
+        st = debug_check_rows(stream, k, tokens, ldk, (int64_t)kv_heads * head_dim, in);
+    if (st != W4A8_OK) return st;
+    return finish(w4a8::launch_qk_norm_rope(q, ldq, k, ldk, in, q_weight, k_weight, eps, cos_sin,
+                                            positions, max_pos, rot, interleaved != 0, tokens,
+                                            q_heads, kv_heads, head_dim, q_out, ldqo, k_out, ldko,
+                                            out, stream),
+                  stream);
+}
+
+w4a8_status w4a8_kv8_write(const void *k, int64_t ldk, const void *v, int64_t ldv,
+                           w4a8_dtype dtype, const int32_t *block_table, int64_t ldb,
+                           int32_t blocks, const int32_t *lens, const int32_t *row_start,
+                           int64_t seqs, int64_t rows, int32_t kv_heads, int32_t head_dim,
+                           int32_t page, int64_t pages, uint8_t *kv, float *kv_scale,
+                           hipStream_t stream) {
+    const w4a8::KvCall c{block_table, ldb, lens, row_start, blocks, (int32_t)seqs, (int32_t)pages,
+                         page, kv_heads, head_dim, rows};
+    w4a8_status st = check_kv_call(c, seqs, pages);
+    if (st != W4A8_OK) return st;
+    const bool bf16 = dtype == W4A8_BF16;
+    if ((!bf16 && dtype != W4A8_F32) ||
+        w4a8::kv8_page_items(rows, seqs, row_start, page) * kv_heads >= kMaxGrid)
+        return W4A8_ERR_UNSUPPORTED;
+    if (!row_stride_ok(ldk, kv_heads, head_dim, bf16) ||
+        !row_stride_ok(ldv, kv_heads, head_dim, bf16))
+        return W4A8_ERR_SHAPE;
+    if (rows == 0 || seqs == 0) return W4A8_OK;
+    if (!k || !v) return W4A8_ERR_NULL;
+    if (!aligned16(k) || !aligned16(v)) return W4A8_ERR_MISALIGNED;
+    st = check_kv_pointers(c, kv, kv_scale);
+    if (st == W4A8_OK) st = debug_check_rows(stream, k, rows, ldk, (int64_t)kv_heads * head_dim, bf16);
+    if (st == W4A8_OK) st = debug_check_rows(stream, v, rows, ldv, (int64_t)kv_heads * head_dim, bf16);
+    if (st != W4A8_OK) return st;
+    return finish(w4a8::launch_kv8_write(c, k, ldk, v, ldv, bf16, kv, kv_scale, stream), stream);
+}
+
+w4a8_status w4a8_kv8_read(const uint8_t *kv, const float *kv_scale, const int32_t *block_table,
+                          int64_t ldb, int32_t blocks, const int32_t *lens,
+                          const int32_t *row_start, int64_t seqs, int64_t rows,
+                          int32_t kv_heads, int32_t head_dim, int32_t page, int64_t pages,
+                          void *k, int64_t ldk, void *v, int64_t ldv, w4a8_dtype dtype,
+                          hipStream_t stream) {
+    const w4a8::KvCall c{block_table, ldb, lens, row_start, blocks, (int32_t)seqs, (int32_t)pages,
+                         page, kv_heads, head_dim, rows};
+    w4a8_status st = check_kv_call(c, seqs, pages);
+    if (st != W4A8_OK) return st;
+    const bool bf16 = dtype == W4A8_BF16;
+    if ((!bf16 && dtype != W4A8_F32) ||
+        w4a8::kv8_page_items(rows, seqs, row_start, page) * kv_heads >= kMaxGrid)
+        return W4A8_ERR_UNSUPPORTED;
+    if (!row_stride_ok(ldk, kv_heads, head_dim, bf16) ||
+        !row_stride_ok(ldv, kv_heads, head_dim, bf16))
+        return W4A8_ERR_SHAPE;
+    if (rows == 0 || seqs == 0) return W4A8_OK;
+    if (!k || !v) return W4A8_ERR_NULL;
+    if (!aligned16(k) || !aligned16(v)) return W4A8_ERR_MISALIGNED;
+    st = check_kv_pointers(c, kv, kv_scale);
+    if (st != W4A8_OK) return st;
+    return finish(w4a8::launch_kv8_read(c, kv, kv_scale, k, ldk, v, ldv, bf16, stream), stream);
+}
+
+size_t w4a8_attn_kv8_workspace_bytes(int64_t rows, int64_t seqs, int32_t ragged,
+                                     int64_t max_rows, int32_t blocks, int32_t q_heads,
+                                     int32_t kv_heads, int32_t head_dim, int32_t page) {
+    static const int32_t some = 0;
+    const w4a8::KvCall c{nullptr, blocks, nullptr, ragged ? &some : nullptr, blocks, 0, 0, page,
+                         kv_heads, head_dim, rows};
+    if (rows == 0 || seqs == 0 || check_kv_call(c, seqs, 0) != W4A8_OK ||
+        check_attn_shape(c, seqs, max_rows, q_heads) != W4A8_OK)
+        return 0;
+    return w4a8::attn_workspace_bytes(rows, seqs, ragged != 0, max_rows, (int64_t)blocks * page,
+                                      q_heads, kv_heads, head_dim);
+}
+
+w4a8_status w4a8_attn_kv8(const uint16_t *q, int64_t ldq, const uint8_t *kv,
+                          const float *kv_scale, const int32_t *block_table, int64_t ldb,
+                          int32_t blocks, const int32_t *lens, const int32_t *row_start,
+                          int64_t seqs, int64_t rows, int64_t max_rows, int32_t q_heads,
+                          int32_t kv_heads, int32_t head_dim, int32_t page, int64_t pages,
+                          int32_t causal, int32_t window, float scale, uint16_t *out,
+                          int64_t ldo, float *lse, void *workspace, size_t ws_bytes,
+                          hipStream_t stream) {
+    const w4a8::KvCall c{block_table, ldb, lens, row_start, blocks, (int32_t)seqs, (int32_t)pages,
+                         page, kv_heads, head_dim, rows};
+    w4a8_status st = check_kv_call(c, seqs, pages);
+    if (st != W4A8_OK) return st;
+    st = check_attn_shape(c, seqs, max_rows, q_heads);
+    if (st != W4A8_OK) return st;
+    if (window < 0 || !row_stride_ok(ldq, q_heads, head_dim, true) ||
+        !row_stride_ok(ldo, q_heads, head_dim, true))
+        return W4A8_ERR_SHAPE;
+    if (window > (1 << 30)) return W4A8_ERR_UNSUPPORTED;
+    if (rows == 0 || seqs == 0) return W4A8_OK;
+    const size_t need = w4a8::attn_workspace_bytes(rows, seqs, row_start != nullptr, max_rows,
+                                                   (int64_t)blocks * page, q_heads, kv_heads,
+                                                   head_dim);
+    if (!q || !out || (need && !workspace)) return W4A8_ERR_NULL;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || (need && !aligned16(workspace)))
+        return W4A8_ERR_MISALIGNED;
+    if (ws_bytes < need) return W4A8_ERR_SHAPE;
+    st = check_kv_pointers(c, kv, kv_scale);
+    if (st == W4A8_OK) st = debug_check_rows(stream, q, rows, ldq, (int64_t)q_heads * head_dim, true);
+    if (st != W4A8_OK) return st;
+    return finish(w4a8::launch_attn(c, q, ldq, kv, kv_scale, max_rows, q_heads, causal != 0, window,
+                                    scale, out, ldo, lse, workspace, stream),
                   stream);
 }
 

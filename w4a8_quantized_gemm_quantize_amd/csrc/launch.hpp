@@ -131,4 +131,37 @@ hipError_t launch_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, co
                            int64_t ldy, void *out, int64_t ldo, bool bf16, void *workspace,
                            hipStream_t stream);
 
+// Norms and rotation of queries and keys (rope.hip), arguments as w4a8_qk_norm_rope in
+// w4a8.h; the grid is its workgroups of 256.
+int64_t qk_norm_rope_grid(int64_t tokens, int32_t heads, int32_t dim);
+hipError_t launch_qk_norm_rope(const void *q, int64_t ldq, const void *k, int64_t ldk, bool bf16_in,
+                               const float *qw, const float *kw, float eps, const float *table,
+                               const int32_t *pos, int64_t max_pos, int32_t rot, bool interleaved,
+                               int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t dim,
+                               void *qo, int64_t ldqo, void *ko, int64_t ldko, bool bf16_out,
+                               hipStream_t stream);
+
+// The paged 8-bit cache (kv8.hip) and attention over it (attn.hip), arguments as
+// w4a8_kv8_write, w4a8_kv8_read and w4a8_attn_kv8 in w4a8.h.
+struct KvCall {
+    const int32_t *table;
+    int64_t ldb;
+    const int32_t *lens, *start;
+    int32_t blocks, seqs, pages, page, kv_heads, dim;
+    int64_t rows;
+};
+int64_t kv8_page_items(int64_t rows, int64_t seqs, bool ragged, int page);
+hipError_t launch_kv8_write(const KvCall &c, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                            bool bf16, uint8_t *kv, float *scale, hipStream_t stream);
+hipError_t launch_kv8_read(const KvCall &c, const uint8_t *kv, const float *scale, void *k,
+                           int64_t ldk, void *v, int64_t ldv, bool bf16, hipStream_t stream);
+size_t attn_workspace_bytes(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows,
+                            int64_t max_tokens, int q_heads, int kv_heads, int dim);
+int64_t attn_grid(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows, int64_t max_tokens,
+                  int q_heads, int kv_heads);
+hipError_t launch_attn(const KvCall &c, const uint16_t *q, int64_t ldq, const uint8_t *kv,
+                       const float *kv_scale, int64_t max_rows, int32_t q_heads, bool causal,
+                       int32_t window, float scale, uint16_t *out, int64_t ldo, float *lse,
+                       void *workspace, hipStream_t stream);
+
 }  // namespace w4a8
