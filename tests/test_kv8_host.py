@@ -148,7 +148,7 @@ def attn(lib, **kw):
     (dict(q_heads=13), SHAPE),
     (dict(q_heads=4 * 65, ldq=1 << 16, ldo=1 << 16), UNSUPPORTED),
     (dict(rows=1 << 29, q_heads=64, ldq=1 << 16, ldo=1 << 16), UNSUPPORTED),
-    (dict(rows=1 << 27, max_rows=1 << 27), UNSUPPORTED),                    # workgroups
+    (dict(rows=1 << 28, max_rows=1 << 28), UNSUPPORTED),                    # workgroups
     (dict(max_rows=0), SHAPE),
     (dict(window=-1), SHAPE),
     (dict(window=(1 << 30) + 1), UNSUPPORTED),

@@ -203,7 +203,7 @@ w4a8_status check_attn_shape(const w4a8::KvCall &c, int64_t seqs, int64_t max_ro
     if (q_heads / c.kv_heads > 64 || c.rows * (q_heads / c.kv_heads) > (1 << 30))
         return W4A8_ERR_UNSUPPORTED;
     if (w4a8::attn_grid(c.rows, seqs, c.start != nullptr, max_rows, (int64_t)c.blocks * c.page,
-                        q_heads, c.kv_heads) >= kMaxGrid)
+                        q_heads, c.kv_heads, c.dim) >= kMaxGrid / 2)
         return W4A8_ERR_UNSUPPORTED;
     return W4A8_OK;
 }

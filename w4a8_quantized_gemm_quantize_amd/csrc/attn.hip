@@ -102,7 +102,7 @@ constexpr int kWaves = 4;
 // range; the four partial results are joined in LDS.  K and V go from memory straight to
 // the registers they are multiplied from, the next run's while this one is worked on.
 template <int C, bool HALF>                      // full chunks of 64 elements, and a half one
-__global__ __launch_bounds__(kWaves * 64, 64 * C + 32 * HALF <= 64 ? 4 : C == 2 && !HALF ? 3 : 2)
+__global__ __launch_bounds__(kWaves * 64, 64 * C + 32 * HALF <= 96 ? 4 : C == 2 && !HALF ? 3 : 2)
 void attn_rows_kernel(AttnArgs a) {
     constexpr int kDim = 64 * C + (HALF ? 32 : 0), kTiles = kDim / 16, kSteps = kDim / 32;
     constexpr int kStride = kDim + 4;
@@ -147,14 +147,15 @@ void attn_rows_kernel(AttnArgs a) {
             for (int x = 0; x < 8; ++x) q[k][x] = (_Float16)(f[x] * up);
         }
     }
-    // tokens this row sees: [see_lo, see_hi)
+    // tokens this row sees, [see_lo, see_hi), and those that every row sees
     const int pos = from + i;
-    int see_hi = a.causal ? min(t.hi, pos + 1) : t.hi;
+    const int see_hi = a.causal ? min(t.hi, pos + 1) : t.hi;
     const int see_lo = a.window ? max(0, pos - a.window + 1) : 0;
-    if (!live) see_hi = 0;
+    const int all_hi = a.causal ? min(t.hi, from + t.row0 / a.group + 1) : t.hi;
+    const int all_lo = a.window ? from + (t.row0 + t.rows - 1) / a.group - a.window + 1 : 0;
 
     const int u_first = t.lo >> 5, u_all = ((t.hi + 31) >> 5) - u_first;
-    const int u0 = u_first + (int)((int64_t)u_all * split / a.splits);
+    const int u0 = u_first + (int)((int64_t)u_all * split / a.splits) + wave;
     const int u1 = u_first + (int)((int64_t)u_all * (split + 1) / a.splits);
 
     f32x4 o[kTiles];
@@ -162,104 +163,147 @@ void attn_rows_kernel(AttnArgs a) {
     for (int d = 0; d < kTiles; ++d) o[d] = f32x4{0, 0, 0, 0};
     float m = -1e30f, l = 0.0f;
 
+    // Lane x: of this wavefront's run n_in + x, for its two tiles of 16 tokens the place of
+    // their keys and the page's terms, 64 runs at a time.  Without a page the place is the
+    // cache's first and the weights are 0.
+    int n_in = 0;
+    int64_t at_in[2];
+    f32x4 terms_in[2];
+    auto look_up = [&](int n) {
+        n_in = n;
+        const int64_t u = u0 + (int64_t)(n + lane) * kWaves;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t at = u * 32 + h * 16;
+            const int page = u < u1 && at < t.hi ? kv_page(a.b, t.s, at >> a.b.page_shift) : -1;
+            at_in[h] = 0;
+            float sk = 0.0f, sv = -1.0f;
+            if (page >= 0) {
+                const int64_t ph = (int64_t)page * a.heads + head;
+                at_in[h] = ((ph * 2 << a.b.page_shift) + (at & ((1 << a.b.page_shift) - 1))) * kDim;
+                sk = a.kv_scale[ph * 2];
+                sv = a.kv_scale[ph * 2 + 1];
+            }
+            terms_in[h] = page_terms(sk, sv);
+        }
+    };
+    const int64_t to_values = (int64_t)kDim << a.b.page_shift;
     struct Run {
         u32x4 k[2][C ? C : 1], v[2][C ? C : 1];
         u32x2 kh[2], vh[2];
-        float sk[2], sv[2];
+    } x;
+    auto lane_value = [](float v, int at) {
+        return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), at));
     };
-    const int page_mask = (1 << a.b.page_shift) - 1;
-    auto load = [&](int u, Run &x) {
+    auto place = [&](int n, int h) {
+        const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)at_in[h], n - n_in);
+        const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(at_in[h] >> 32), n - n_in);
+        return (int64_t)(((uint64_t)hi << 32) | lo);
+    };
+    auto load_keys = [&](int n) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int at = u * 32 + h * 16;
-            const int page = at < t.hi ? kv_page(a.b, t.s, at >> a.b.page_shift) : -1;
-            if (page >= 0) {
-                const int64_t ph = (int64_t)page * a.heads + head;
-                const uint8_t *kp = a.kv + (ph * 2 << a.b.page_shift) * kDim + (at & page_mask) * kDim;
-                const uint8_t *vp = kp + ((int64_t)kDim << a.b.page_shift);
+            const uint8_t *p = a.kv + place(n, h);
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    x.k[h][c] = *(const u32x4 *)(kp + c * 1024 + lane * 16);
-                    x.v[h][c] = *(const u32x4 *)(vp + c * 1024 + lane * 16);
-                }
-                if constexpr (HALF) {
-                    x.kh[h] = *(const u32x2 *)(kp + C * 1024 + lane * 8);
-                    x.vh[h] = *(const u32x2 *)(vp + C * 1024 + lane * 8);
-                }
-                x.sk[h] = a.kv_scale[ph * 2];
-                x.sv[h] = a.kv_scale[ph * 2 + 1];
-            } else {
-                const u32x4 z = {0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u};
-#pragma unroll
-                for (int c = 0; c < C; ++c) x.k[h][c] = x.v[h][c] = z;
-                if constexpr (HALF) x.kh[h] = x.vh[h] = u32x2{z.x, z.x};
-                x.sk[h] = 0.0f;
-                x.sv[h] = -1.0f;                 // no page: masked
-            }
+            for (int c = 0; c < C; ++c) x.k[h][c] = __builtin_nontemporal_load((const u32x4 *)(p + c * 1024 + lane * 16));
+            if constexpr (HALF) x.kh[h] = __builtin_nontemporal_load((const u32x2 *)(p + C * 1024 + lane * 8));
         }
     };
-
-    Run x;
-    if (u0 + wave < u1) load(u0 + wave, x);
-    for (int u = u0 + wave; u < u1; u += kWaves) {
+    auto load_values = [&](int n) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint8_t *p = a.kv + place(n, h) + to_values;
+#pragma unroll
+            for (int c = 0; c < C; ++c) x.v[h][c] = __builtin_nontemporal_load((const u32x4 *)(p + c * 1024 + lane * 16));
+            if constexpr (HALF) x.vh[h] = __builtin_nontemporal_load((const u32x2 *)(p + C * 1024 + lane * 8));
+        }
+    };
+    auto work = [&](int n) {
+        const int first = (u0 + n * kWaves) * 32;
+        float sk[2], log_sv[2], inv_sv[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            sk[h] = lane_value(terms_in[h].x, n - n_in);
+            log_sv[h] = lane_value(terms_in[h].y, n - n_in);
+            inv_sv[h] = lane_value(terms_in[h].z, n - n_in);
+        }
         // scores of two tiles of 16 tokens
         f32x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                s[h] = mfma16(codes8h(x.k[h][c].x, x.k[h][c].y), q[2 * c], s[h]);
-                s[h] = mfma16(codes8h(x.k[h][c].z, x.k[h][c].w), q[2 * c + 1], s[h]);
-            }
-            if constexpr (HALF) s[h] = mfma16(codes8h(x.kh[h].x, x.kh[h].y), q[2 * C], s[h]);
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    s[h] = mfma16(codes8h(x.k[h][c][2 * k], x.k[h][c][2 * k + 1]), q[2 * c + k], s[h]);
+        if constexpr (HALF) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) s[h] = mfma16(codes8h(x.kh[h].x, x.kh[h].y), q[2 * C], s[h]);
         }
-        float tv[2][4], inv[2];
-        float best = -1e30f;
+        if (n + 1 - n_in == 64) look_up(n + 1);
+        load_keys(n + 1);
+        if (first + 32 > all_hi || first < all_lo) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const f32x4 pt = page_terms(x.sk[h], x.sv[h]);
-            const float f = qfac * pt.x;
-            inv[h] = pt.z;
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int j = u * 32 + h * 16 + 4 * g + e;
-                tv[h][e] = j >= see_lo && j < see_hi ? __builtin_fmaf(s[h][e], f, pt.y)
-                                                     : -__builtin_inff();
-                best = fmaxf(best, tv[h][e]);
-            }
+                for (int e = 0; e < 4; ++e) {
+                    const int j = first + h * 16 + 4 * g + e;
+                    if (j < see_lo || j >= see_hi) s[h][e] = -__builtin_inff();
+                }
         }
-        if (__any(best > m + 8.0f)) {
-            const float n = fmaxf(m, quad_max(best));
-            const float down = __builtin_amdgcn_exp2f(m - n);
-            m = n;
+        float f[2], sum[2];
+        half8_t p;
+        auto weights = [&]() {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                f[h] = fmaxf(qfac * sk[h], 1e-30f);
+                const float off = log_sv[h] - m;
+                sum[h] = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[h][e], f[h], off));
+                    sum[h] += w;
+                    p[4 * h + e] = (_Float16)w;
+                }
+            }
+        };
+        weights();
+        if (__any(!(fmaxf(sum[0], sum[1]) <= 0x1p14f))) {
+            float best = -1e30f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    best = fmaxf(best, __builtin_fmaf(s[h][e], f[h], log_sv[h]));
+            const float top = fmaxf(m, quad_max(best) - 4.0f);
+            const float down = __builtin_amdgcn_exp2f(m - top);
+            m = top;
             l *= down;
 #pragma unroll
             for (int d = 0; d < kTiles; ++d) o[d] *= down;
+            weights();
         }
-        half8_t p;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float w = __builtin_amdgcn_exp2f(tv[h][e] - m);
-                sum += w;
-                p[4 * h + e] = (_Float16)w;
-            }
-            l = __builtin_fmaf(sum, inv[h], l);
-        }
-        const Run y = x;
-        if (u + kWaves < u1) load(u + kWaves, x);
+        for (int h = 0; h < 2; ++h) l = __builtin_fmaf(sum[h], inv_sv[h], l);
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                o[4 * c + j] = mfma16(codes8h(y.v[0][c][j], y.v[1][c][j]), p, o[4 * c + j]);
+                o[4 * c + j] = mfma16(codes8h(x.v[0][c][j], x.v[1][c][j]), p, o[4 * c + j]);
         if constexpr (HALF) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                o[4 * C + j] = mfma16(codes8h(y.vh[0][j], y.vh[1][j]), p, o[4 * C + j]);
+                o[4 * C + j] = mfma16(codes8h(x.vh[0][j], x.vh[1][j]), p, o[4 * C + j]);
         }
+        load_values(n + 1);
+    };
+
+    const int runs = u0 < u1 ? (u1 - u0 + kWaves - 1) / kWaves : 0;
+    if (runs) {
+        look_up(0);
+        load_keys(0);
+        load_values(0);
+        for (int n = 0; n < runs; ++n) work(n);
     }
     l = quad_sum(l);
 #pragma unroll
@@ -313,9 +357,9 @@ void attn_rows_kernel(AttnArgs a) {
     }
 }
 
-// ---- many rows: 128 packed rows a workgroup, 32 a wavefront ----
+// ---- many rows: 32 a wavefront, 128 or 256 packed rows a workgroup ----
 //
-// Four wavefronts share 64 tokens at a time, converted once to halves in LDS in the order of
+// The wavefronts share 64 tokens at a time, converted once to halves in LDS in the order of
 // the operands of v_mfma_f32_32x32x16_f16 (A: lane l holds 8 of row l % 32, k = 8 (l / 32) ..;
 // result element i of lane l: row 8 (i / 4) + 4 (l / 32) + i % 4, column l % 32):
 //   keys    [16 tokens][chunk][half of the record][lane] 16 bytes: step (chunk, s, half) reads
@@ -328,14 +372,21 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ f32x16 mfma32(half8_t a, half8_t b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
-constexpr int kTileShift = 7;                    // packed rows of a tile: 128
+constexpr int min_of(int a, int b) { return a < b ? a : b; }
+// Wavefronts of a workgroup, by registers: eight are two on a SIMD, four three (up to 64
+// elements a head) or one.
+constexpr int tile_waves(int dim) { return dim > 64 && dim <= 128 ? 8 : 4; }
+
+constexpr int tile_groups(int dim) { return dim <= 64 ? 3 : 1; }   // workgroups of a compute unit
 
 template <int C, bool HALF>
-__global__ __launch_bounds__(256, (64 * C + 32 * HALF) <= 128 ? 2 : 1) void attn_tile_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * tile_waves(64 * C + 32 * HALF), tile_waves(64 * C + 32 * HALF) / 4 * tile_groups(64 * C + 32 * HALF))
+void attn_tile_kernel(AttnArgs a) {
     constexpr int kDim = 64 * C + (HALF ? 32 : 0), kSteps = kDim / 16, kBlocks = kDim / 32;
+    constexpr int kTW = tile_waves(kDim), kTileShift = kTW == 8 ? 8 : 7;
     constexpr int kSub = 16 * kDim;              // halves of 16 tokens
     __shared__ __attribute__((aligned(16))) _Float16 kbuf[2][4 * kSub], vbuf[2][4 * kSub];
-    __shared__ f32x4 page[2][4];                 // of 16 tokens: key scale, log2 value scale, 1 / it
+    __shared__ f32x4 page[4][4];                 // of 16 tokens: page_terms
     const int head = blockIdx.x % a.heads;
     const int split = blockIdx.x / a.heads % a.splits;
     const int64_t item = a.items - 1 - blockIdx.x / a.heads / a.splits;
@@ -375,12 +426,12 @@ __global__ __launch_bounds__(256, (64 * C + 32 * HALF) <= 128 ? 2 : 1) void attn
         }
     }
     const int pos = from + i;
-    const int see_hi = live ? a.causal ? min(t.hi, pos + 1) : t.hi : 0;
+    const int see_hi = a.causal ? min(t.hi, pos + 1) : t.hi;
     const int see_lo = a.window ? max(0, pos - a.window + 1) : 0;
     // tokens that every row of the wavefront sees
-    const bool whole = wave * 32 + 32 <= t.rows;
-    const int all_hi = whole ? a.causal ? min(t.hi, from + (t.row0 + wave * 32) / a.group + 1) : t.hi : 0;
-    const int all_lo = a.window ? from + (t.row0 + wave * 32 + 31) / a.group - a.window + 1 : 0;
+    const int row1 = t.row0 + wave * 32, row2 = max(row1, t.row0 + min(t.rows, wave * 32 + 32) - 1);
+    const int all_hi = a.causal ? min(t.hi, from + row1 / a.group + 1) : t.hi;
+    const int all_lo = a.window ? from + row2 / a.group - a.window + 1 : 0;
 
     const int j_first = t.lo >> 6, j_all = ((t.hi + 63) >> 6) - j_first;
     const int j0 = j_first + (int)((int64_t)j_all * split / a.splits);
@@ -393,145 +444,246 @@ __global__ __launch_bounds__(256, (64 * C + 32 * HALF) <= 128 ? 2 : 1) void attn
         for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
     float m = -1e30f, l = 0.0f;
 
-    // this wavefront's 16 of a run of 64 tokens
-    u32x4 kr[C ? C : 1], vr[C ? C : 1];
-    u32x2 kh, vh;
-    float sk, sv;
-    const int page_mask = (1 << a.b.page_shift) - 1;
-    auto load = [&](int j) {
-        const int at = j * 64 + wave * 16;
-        const int pg = at < t.hi ? kv_page(a.b, t.s, at >> a.b.page_shift) : -1;
+    // A wavefront stages 16 tokens of each run of 64: their keys, their values (the upper
+    // four of eight wavefronts), or both.
+    const int sub = wave & 3;
+    const bool does_keys = kTW == 4 || wave < 4, does_values = kTW == 4 || wave >= 4;
+    // Lane x: of the tokens of run j_in + x the place of their keys and the page's terms, 64
+    // runs at a time (as in attn_rows_kernel).
+    int j_in = j0;
+    int64_t at_in = 0;
+    f32x4 terms_in;
+    auto look_up = [&](int j) {
+        j_in = j;
+        const int64_t at = (int64_t)(j + lane) * 64 + sub * 16;
+        const int pg = j + lane < j1 && at < t.hi ? kv_page(a.b, t.s, at >> a.b.page_shift) : -1;
+        at_in = 0;
+        float sk = 0.0f, sv = -1.0f;
         if (pg >= 0) {
             const int64_t ph = (int64_t)pg * a.heads + head;
-            const uint8_t *kp = a.kv + (ph * 2 << a.b.page_shift) * kDim + (at & page_mask) * kDim;
-            const uint8_t *vp = kp + ((int64_t)kDim << a.b.page_shift);
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                kr[c] = *(const u32x4 *)(kp + c * 1024 + lane * 16);
-                vr[c] = *(const u32x4 *)(vp + c * 1024 + lane * 16);
-            }
-            if constexpr (HALF) {
-                kh = *(const u32x2 *)(kp + C * 1024 + lane * 8);
-                vh = *(const u32x2 *)(vp + C * 1024 + lane * 8);
-            }
+            at_in = ((ph * 2 << a.b.page_shift) + (at & ((1 << a.b.page_shift) - 1))) * kDim;
             sk = a.kv_scale[ph * 2];
             sv = a.kv_scale[ph * 2 + 1];
-        } else {
-            const u32x4 z = {0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u};
-#pragma unroll
-            for (int c = 0; c < C; ++c) kr[c] = vr[c] = z;
-            if constexpr (HALF) kh = vh = u32x2{z.x, z.x};
-            sk = 0.0f;
-            sv = -1.0f;
         }
+        terms_in = page_terms(sk, sv);
     };
-    auto store = [&](int buf) {
-        _Float16 *kb = kbuf[buf] + wave * kSub, *vb = vbuf[buf] + wave * kSub;
-        const int g = lane >> 4, e = lane & 15;
-        _Float16 *vl = vb + (g & 1) * 256 + e * 8 + (g >> 1) * 4;
+    auto part_of = [&](int j) -> int64_t {
+        const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)at_in, j - j_in);
+        const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(at_in >> 32), j - j_in);
+        return (int64_t)(((uint64_t)hi << 32) | lo);
+    };
+    struct Raw {
+        u32x4 r[C ? C : 1];
+        u32x2 h;
+    };
+    Raw kraw, vraw;
+    f32x4 terms;
+    auto load = [&](int64_t at, Raw &x) {
+        const uint8_t *p = a.kv + at;
+#pragma unroll
+        for (int c = 0; c < C; ++c) x.r[c] = *(const u32x4 *)(p + c * 1024 + lane * 16);
+        if constexpr (HALF) x.h = *(const u32x2 *)(p + C * 1024 + lane * 8);
+    };
+    auto lane_value = [](float v, int at) {
+        return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), at));
+    };
+    const int64_t to_values = (int64_t)kDim << a.b.page_shift;
+    auto load_keys = [&](int j) {
+        load(part_of(j), kraw);
+        terms = f32x4{lane_value(terms_in.x, j - j_in), lane_value(terms_in.y, j - j_in),
+                      lane_value(terms_in.z, j - j_in), 0.0f};
+    };
+    auto load_values = [&](int j) { load(part_of(j) + to_values, vraw); };
+    auto store_keys = [&](int j) {
+        _Float16 *kb = kbuf[j & 1] + sub * kSub;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            *(half8_t *)(kb + (c * 2) * 512 + lane * 8) = codes8h(kr[c].x, kr[c].y);
-            *(half8_t *)(kb + (c * 2 + 1) * 512 + lane * 8) = codes8h(kr[c].z, kr[c].w);
+            *(half8_t *)(kb + (c * 2) * 512 + lane * 8) = codes8h(kraw.r[c].x, kraw.r[c].y);
+            *(half8_t *)(kb + (c * 2 + 1) * 512 + lane * 8) = codes8h(kraw.r[c].z, kraw.r[c].w);
+        }
+        if constexpr (HALF) *(half8_t *)(kb + (C * 2) * 512 + lane * 8) = codes8h(kraw.h.x, kraw.h.y);
+        page[j & 3][sub] = terms;
+    };
+    auto store_values = [&](int j) {
+        const int g = lane >> 4, e = lane & 15;
+        _Float16 *vl = vbuf[j & 1] + sub * kSub + (g & 1) * 256 + e * 8 + (g >> 1) * 4;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 uint32_t lo, hi;
-                codes4(vr[c][x], lo, hi);
+                codes4(vraw.r[c][x], lo, hi);
                 *(u32x2 *)(vl + (c * 2 + (x >> 1)) * 512 + (x & 1) * 128) = u32x2{lo, hi};
             }
-        }
         if constexpr (HALF) {
-            *(half8_t *)(kb + (C * 2) * 512 + lane * 8) = codes8h(kh.x, kh.y);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 uint32_t lo, hi;
-                codes4(vh[x], lo, hi);
+                codes4(vraw.h[x], lo, hi);
                 *(u32x2 *)(vl + C * 2 * 512 + x * 128) = u32x2{lo, hi};
             }
         }
-        if (lane == 0) page[buf][wave] = page_terms(sk, sv);
     };
-
-    if (j0 < j1) {
-        load(j0);
-        store(j0 & 1);
-        if (j0 + 1 < j1) load(j0 + 1);
-    }
-    __syncthreads();
-    for (int j = j0; j < j1; ++j) {
-        if (j + 1 < j1) {
-            store((j + 1) & 1);
-            if (j + 2 < j1) load(j + 2);
+    const int sub_lane = (lane & 31) >> 4, rec = (h * 16 + (lane & 15)) * 8;
+    auto key_operand = [&](int j, int half, int k) {
+        const int at = k < 4 * C ? ((k >> 2) * 2 + (k & 1)) * 512 + (k >> 1 & 1) * 256
+                                 : C * 1024 + (k & 1) * 256;
+        return *(const half8_t *)(kbuf[j & 1] + (2 * half + sub_lane) * kSub + rec + at);
+    };
+    auto value_operand = [&](int j, int x, int d) {
+        return *(const half8_t *)(vbuf[j & 1] + x * kSub + d * 512 + lane * 8);
+    };
+    // Half a run: the weights p of 32 tokens from their scores s, and beside them, on the
+    // matrix cores, the scores `next` of the 32 after and the products of the 32 before.
+    auto step = [&](int j, int half, f32x16 &s, f32x16 &next, half8_t (&before)[2], half8_t (&p)[2]) {
+        const int first = j * 64 + half * 32;
+        if (first + 32 > all_hi || first < all_lo) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int at = first + 8 * (e >> 2) + 4 * h + (e & 3);
+                if (at < see_lo || at >= see_hi) s[e] = -__builtin_inff();
+            }
         }
-        const _Float16 *kb = kbuf[j & 1], *vb = vbuf[j & 1];
-        f32x16 s[2];
+        f32x4 pt[2];
+        float f[2], sum[2];
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) s[b][e] = 0.0f;
-        const int sub_lane = (lane & 31) >> 4, rec = (h * 16 + (lane & 15)) * 8;
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-            const int at = k < 4 * C ? ((k >> 2) * 2 + (k & 1)) * 512 + (k >> 1 & 1) * 256
-                                     : C * 1024 + (k & 1) * 256;
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-                s[b] = mfma32(*(const half8_t *)(kb + (2 * b + sub_lane) * kSub + at + rec), q[k], s[b]);
-        }
-        if (j * 64 + 64 > all_hi || j * 64 < all_lo) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int at = j * 64 + b * 32 + 8 * (e >> 2) + 4 * h + (e & 3);
-                    if (at < see_lo || at >= see_hi) s[b][e] = -__builtin_inff();
-                }
-        }
-        f32x4 pt[4];
-        float f[4], best = -1e30f;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            pt[x] = page[j & 1][x];
+        for (int x = 0; x < 2; ++x) {
+            pt[x] = page[j & 3][2 * half + x];
             f[x] = fmaxf(qfac * pt[x].x, 1e-30f);
-            float top = s[x >> 1][8 * (x & 1)];
-#pragma unroll
-            for (int e = 1; e < 8; ++e) top = fmaxf(top, s[x >> 1][8 * (x & 1) + e]);
-            best = fmaxf(best, __builtin_fmaf(top, f[x], pt[x].y));
         }
-        if (__any(best > m + 8.0f)) {
-            const float n = fmaxf(m, fmaxf(best, __shfl_xor(best, 32)));
+        auto weights = [&]() {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float off = pt[x].y - m;
+                sum[x] = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[8 * x + e], f[x], off));
+                    sum[x] += w;
+                    p[x][e] = (_Float16)w;
+                }
+            }
+        };
+        // One product at a time with its share of the weights' steps, in this order: the
+        // scheduler left to itself puts the products first and the weights behind them.
+        constexpr int kProducts = 2 * kBlocks, kAll = kSteps + kProducts, kAhead = 4;
+        auto operand = [&](int n) {              // products in turn: a score's, a sum's
+            const bool score = n < 2 * min_of(kSteps, kProducts) ? n % 2 == 0 : kSteps > kProducts;
+            const int k = n < 2 * min_of(kSteps, kProducts) ? n / 2 : n - min_of(kSteps, kProducts);
+            return score ? key_operand(j + half, 1 - half, k)
+                         : value_operand(j - 1 + half, 2 * (1 - half) + k / kBlocks, k % kBlocks);
+        };
+        half8_t ring[kAhead];
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n) ring[n] = operand(n);
+        const float off[2] = {pt[0].y - m, pt[1].y - m};
+        float u[16], w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) next[e] = 0.0f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) sum[x] = 0.0f;
+#pragma unroll
+        for (int n = 0; n < kAll + 2; ++n) {
+            if (n < kAll) {
+                const bool score = n < 2 * min_of(kSteps, kProducts) ? n % 2 == 0 : kSteps > kProducts;
+                const int k = n < 2 * min_of(kSteps, kProducts) ? n / 2 : n - min_of(kSteps, kProducts);
+                if (score) next = mfma32(ring[n % kAhead], q[k], next);
+                else o[k % kBlocks] = mfma32(ring[n % kAhead], before[k / kBlocks], o[k % kBlocks]);
+                if (n + kAhead < kAll) ring[n % kAhead] = operand(n + kAhead);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                if (e * kAll / 16 == n) u[e] = __builtin_fmaf(s[e], f[e >> 3], off[e >> 3]);
+                if (e * kAll / 16 == n - 1) w[e] = __builtin_amdgcn_exp2f(u[e]);
+                if (e * kAll / 16 == n - 2) {
+                    sum[e >> 3] += w[e];
+                    if (e & 1) {
+                        const half2_t c = __builtin_convertvector(f32x2_t{w[e - 1], w[e]}, half2_t);
+                        p[e >> 3][(e & 7) - 1] = c[0];
+                        p[e >> 3][e & 7] = c[1];
+                    }
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        const float most = fmaxf(sum[0], sum[1]);
+        if (kTW == 4 && half) {
+            store_keys(j + 2);
+            store_values(j + 1);
+        }
+        if (__any(!(most <= 0x1p14f))) {
+            float best = -1e30f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) best = fmaxf(best, __builtin_fmaf(s[e], f[e >> 3], pt[e >> 3].y));
+            const float n = fmaxf(m, fmaxf(best, __shfl_xor(best, 32)) - 4.0f);
             const float down = __builtin_amdgcn_exp2f(m - n);
             m = n;
             l *= down;
 #pragma unroll
             for (int d = 0; d < kBlocks; ++d) o[d] *= down;
-        }
-        half8_t p[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const float off = pt[x].y - m;
-            float sum = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x >> 1][8 * (x & 1) + e], f[x], off));
-                sum += w;
-                p[x][e] = (_Float16)w;
-            }
-            l = __builtin_fmaf(sum, pt[x].z, l);
+            weights();
         }
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int d = 0; d < kBlocks; ++d)
-                o[d] = mfma32(*(const half8_t *)(vb + x * kSub + d * 512 + lane * 8), p[x], o[d]);
+        for (int x = 0; x < 2; ++x) l = __builtin_fmaf(sum[x], pt[x].z, l);
+    };
+
+    f32x16 s0, s1;
+    half8_t p0[2], p1[2];
+    if (j0 < j1) {
+        look_up(j0);
+        if (does_keys) {
+            load_keys(j0);
+            store_keys(j0);
+            load_keys(j0 + 1);
+            store_keys(j0 + 1);
+            load_keys(j0 + 2);
+        }
+        if (does_values) {
+            load_values(j0);
+            store_values(j0);
+            // what the first step multiplies by 0
+            for (int x = lane; x < kSub / 8; x += 64)
+                *(u32x4 *)(vbuf[(j0 + 1) & 1] + sub * kSub + x * 8) = u32x4{0, 0, 0, 0};
+            load_values(j0 + 1);
+        }
         __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s0[e] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) s0 = mfma32(key_operand(j0, 0, k), q[k], s0);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p1[x][e] = (_Float16)0.0f;
+    }
+    auto load_next = [&](int j) {
+        if (does_values) load_values(j + 2);
+        if (j + 3 - j_in == 64) look_up(j + 3);
+        if (does_keys) load_keys(j + 3);
+    };
+    for (int j = j0; j < j1; ++j) {
+        step(j, 0, s0, s1, p1, p0);
+        __syncthreads();
+        if (kTW == 8) {
+            if (does_keys) store_keys(j + 2);
+            else store_values(j + 1);
+            load_next(j);
+        }
+        step(j, 1, s1, s0, p0, p1);
+        if (kTW == 4) load_next(j);
+    }
+    if (j0 < j1) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int d = 0; d < kBlocks; ++d) o[d] = mfma32(value_operand(j1 - 1, 2 + x, d), p1[x], o[d]);
     }
     l += __shfl_xor(l, 32);
     const int qh = head * a.group + r - i * a.group;
     const int64_t orow = t.seq.first_row + i;
     if (a.part) {
         if (!live) return;
-        float *part = a.part + (((item * a.heads + head) * a.splits + split) * 128 + wave * 32 + col) *
+        float *part = a.part + ((((item * a.heads + head) * a.splits + split) << kTileShift) + wave * 32 + col) *
                                    (kDim + 4);
         if (h == 0) {
             part[kDim] = m;
@@ -560,70 +712,111 @@ __global__ __launch_bounds__(256, (64 * C + 32 * HALF) <= 128 ? 2 : 1) void attn
                       bf16x2_rne(o[d][4 * x + 2] * by, o[d][4 * x + 3] * by)};
 }
 
-// Joins the splits of a tile: 16 threads a row.
+// Joins the splits of a tile, one wavefront a row: lane z holds the factors of splits z and
+// z + 64, then groups of dim / 4 lanes sum every group-th split's row.  (16 lanes a row, one
+// split after the other: 126 us for 86 splits of 3 x 8 tiles, where the attention took 136.)
+constexpr int kMaxSplits = 128;
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int dim, int shift) {
-    const int slabs = 1 << (shift - 4), height = 1 << shift;
-    const int head = blockIdx.x / slabs % a.heads;
-    const int64_t item = blockIdx.x / slabs / a.heads;
+    const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);     // item, head, row
+    const int row = (int)(at & ((1 << shift) - 1)), lane = threadIdx.x & 63;
+    const int64_t slot = at >> shift, item = slot / a.heads;
+    const int head = (int)(slot - item * a.heads);
     KvTile t;
-    if (!find_tile(a, item, shift, t)) return;
-    const int row = (int)(blockIdx.x % slabs) * 16 + (threadIdx.x >> 4), at = (threadIdx.x & 15) * 4;
-    if (row >= t.rows) return;
-    const int64_t step = (int64_t)height * (dim + 4);
-    const float *p = a.part + ((item * a.heads + head) * a.splits * height + row) * (dim + 4);
-    float mm = -1e30f;
-    for (int z = 0; z < a.splits; ++z) mm = fmaxf(mm, p[z * step + dim]);
-    float ll = 0.0f;
-    for (int z = 0; z < a.splits; ++z)
-        ll = __builtin_fmaf(__builtin_amdgcn_exp2f(p[z * step + dim] - mm), p[z * step + dim + 1], ll);
-    const float by = ll > 0.0f ? 1.0f / ll : 0.0f;
+    if (item >= a.items || !find_tile(a, item, shift, t) || row >= t.rows) return;
+    const int64_t step = (int64_t)(dim + 4) << shift;
+    const float *p = a.part + slot * a.splits * step + row * (dim + 4);
+    float m[2], l[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int z = lane + 64 * x;
+        m[x] = z < a.splits ? p[z * step + dim] : -1e30f;
+        l[x] = z < a.splits ? p[z * step + dim + 1] : 0.0f;
+    }
+    float mm = fmaxf(m[0], m[1]);
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) mm = fmaxf(mm, __shfl_xor(mm, x));
+    const float f0 = __builtin_amdgcn_exp2f(m[0] - mm), f1 = __builtin_amdgcn_exp2f(m[1] - mm);
+    float ll = __builtin_fmaf(f0, l[0], f1 * l[1]);
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) ll += __shfl_xor(ll, x);
     const int rr = t.row0 + row, ri = rr / a.group, qh = head * a.group + rr - ri * a.group;
     const int64_t orow = t.seq.first_row + ri;
-    if (at == 0 && a.lse)
+    if (lane == 0 && a.lse)
         a.lse[orow * a.heads * a.group + qh] =
             ll > 0.0f ? kLn2 * (mm + __builtin_amdgcn_logf(ll)) : -__builtin_inff();
-    for (int d = at; d < dim; d += 64) {
-        f32x4 sum = {0, 0, 0, 0};
-        for (int z = 0; z < a.splits; ++z) {
-            const float f = __builtin_amdgcn_exp2f(p[z * step + dim] - mm);
+    const int cols = dim >> 2, groups = 64 / cols, g = lane / cols, d = (lane - g * cols) * 4;
+    f32x4 sum = {0, 0, 0, 0};
+    for (int z0 = 0; z0 < a.splits; z0 += groups) {
+        const int z = z0 + g;
+        const float f = __shfl(z0 < 64 ? f0 : f1, z & 63);
+        const float f_next = __shfl(f1, z & 63);        // a round of groups may reach over 64
+        if (g < groups && z < a.splits) {
             const f32x4 v = *(const f32x4 *)(p + z * step + d);
+            const float w = z0 < 64 && z >= 64 ? f_next : f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(f, v[e], sum[e]);
+            for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(w, v[e], sum[e]);
         }
-        *(u32x2 *)(a.out + orow * a.ldo + (int64_t)qh * dim + d) =
-            u32x2{bf16x2_rne(sum[0] * by, sum[1] * by), bf16x2_rne(sum[2] * by, sum[3] * by)};
     }
+    f32x4 all = sum;
+    for (int x = 1; x < groups; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) all[e] += __shfl(sum[e], (lane + x * cols) & 63);
+    if (g > 0) return;
+    const float by = ll > 0.0f ? 1.0f / ll : 0.0f;
+    *(u32x2 *)(a.out + orow * a.ldo + (int64_t)qh * dim + d) =
+        u32x2{bf16x2_rne(all[0] * by, all[1] * by), bf16x2_rne(all[2] * by, all[3] * by)};
 }
 
 template <int C, bool HALF>
 void launch_dim(const AttnArgs &a, int shift, hipStream_t stream) {
     const dim3 grid((uint32_t)(a.items * a.heads * a.splits));
     if (shift == 4) attn_rows_kernel<C, HALF><<<grid, kWaves * 64, 0, stream>>>(a);
-    else attn_tile_kernel<C, HALF><<<grid, 256, 0, stream>>>(a);
+    else attn_tile_kernel<C, HALF><<<grid, 64 * tile_waves(64 * C + 32 * HALF), 0, stream>>>(a);
 }
 
 struct Plan {
     int64_t items;
     int tiles, splits, shift;
 };
-// The kernel by the packed rows of a sequence, and over how many workgroups the tokens of a
-// tile are split: enough of them for the card, at least 256 tokens each.
+// The kernel by the packed rows of a sequence: up to 64 go 16 a workgroup, that is, through
+// the cache up to four times, from the L2 after the first (32 x 4000 tokens, 8 heads of 128
+// with 32, 40, 64 and 80 rows: 67, 127, 132 and 200 us, where a 256-row tile takes 179, 181,
+// 183 and 185; 4 x 4000 tokens: 20, 23, 25 and 29 for 35, 36, 37 and 37).  Then over how many workgroups the tokens of a
+// tile are split: the least of a cost in microseconds,
+//   rounds of workgroups over the card x tokens each x what one takes a token
+//   + for more than one split its partial results and the second launch that joins them.
+// Few rows: two workgroups a compute unit draw all that memory gives (64 x 8192 tokens, 8
+// heads of 128: 183 us unsplit, 203, 197 and 200 us in 2, 3 and 4).  A workgroup alone takes
+// 5.5 ns a token (one sequence, 8 heads of 128: 8.0, 16.3 and 27.4 us for 500, 2000 and 4000
+// tokens), the join 3.5 us and 0.18 us a split (2000 tokens: 14.5, 12.2, 11.6, 12.3 and 15.5
+// us in 2, 4, 8, 16 and 32).
 Plan attn_plan(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows, int64_t max_tokens,
-               int q_heads, int kv_heads) {
+               int q_heads, int kv_heads, int dim) {
     const int64_t group = q_heads / kv_heads;
     max_rows = !ragged ? 1 : max_rows < rows ? max_rows : rows;
     Plan p;
-    p.shift = max_rows * group <= 32 ? 4 : kTileShift;
+    p.shift = max_rows * group <= 64 ? 4 : tile_waves(dim) == 8 ? 8 : 7;
     const int64_t height = 1 << p.shift;
     const int64_t tiles = (max_rows * group + height - 1) / height;
     const int64_t loose = kv_tile_items(rows, seqs, group, p.shift);
     p.tiles = !ragged || seqs * tiles <= loose ? (int)tiles : 0;
     p.items = p.tiles ? seqs * tiles : loose;
-    const int64_t work = p.items * kv_heads, most = (max_tokens + 255) / 256;
-    const int64_t want = p.shift == 4 ? 2048 : 512;
-    int64_t splits = work ? (want + work - 1) / work : 1;
-    splits = splits < most ? splits : most;
-    p.splits = (int)(splits < 1 ? 1 : splits > 128 ? 128 : splits);
+    const int64_t work = p.items * kv_heads, most = (max_tokens + 127) / 128;
+    const int64_t places = device_cu_count() * (p.shift == 4 ? 2 : tile_groups(dim));
+    const double token = (p.shift == 4 ? 5.5e-3 : 3.0e-2) * dim / 128;
+    // partial results are written and read at about 4 TB/s
+    const double join = p.shift == 4 ? 3.5 : 9.0;
+    const double each = 0.18 + 2e-6 * (double)(work << p.shift) * (dim + 4);
+    double best = 0;
+    p.splits = 1;
+    for (int z = 1; z <= kMaxSplits && (z == 1 || z <= most); ++z) {
+        const double rounds = (double)((work * z + places - 1) / places);
+        const double cost = rounds * token * max_tokens / z + (z > 1 ? join + each * z : 0);
+        if (z == 1 || cost < best) {
+            best = cost;
+            p.splits = z;
+        }
+    }
     return p;
 }
 
@@ -631,15 +824,14 @@ Plan attn_plan(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows, int64_
 
 size_t attn_workspace_bytes(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows,
                             int64_t max_tokens, int q_heads, int kv_heads, int dim) {
-    const Plan p = attn_plan(rows, seqs, ragged, max_rows, max_tokens, q_heads, kv_heads);
+    const Plan p = attn_plan(rows, seqs, ragged, max_rows, max_tokens, q_heads, kv_heads, dim);
     return p.splits > 1 ? ((size_t)p.items * kv_heads * p.splits << p.shift) * (dim + 4) * 4 : 0;
 }
 
 int64_t attn_grid(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows, int64_t max_tokens,
-                  int q_heads, int kv_heads) {
-    const Plan p = attn_plan(rows, seqs, ragged, max_rows, max_tokens, q_heads, kv_heads);
-    const int64_t slabs = 1 << (p.shift - 4);
-    return p.items * kv_heads * (p.splits > slabs ? p.splits : slabs);
+                  int q_heads, int kv_heads, int dim) {
+    const Plan p = attn_plan(rows, seqs, ragged, max_rows, max_tokens, q_heads, kv_heads, dim);
+    return p.items * kv_heads * (p.splits == 1 ? 1 : p.splits > 1 << p.shift ? p.splits : 1 << p.shift);
 }
 
 hipError_t launch_attn(const KvCall &c, const uint16_t *q, int64_t ldq, const uint8_t *kv,
@@ -647,7 +839,7 @@ hipError_t launch_attn(const KvCall &c, const uint16_t *q, int64_t ldq, const ui
                        int32_t window, float scale, uint16_t *out, int64_t ldo, float *lse,
                        void *workspace, hipStream_t stream) {
     const Plan p = attn_plan(c.rows, c.seqs, c.start != nullptr, max_rows,
-                             (int64_t)c.blocks * c.page, q_heads, c.kv_heads);
+                             (int64_t)c.blocks * c.page, q_heads, c.kv_heads, c.dim);
     AttnArgs a;
     a.b = KvBatch{c.start, c.lens, c.table, c.ldb, c.seqs, c.blocks, c.pages, (int32_t)c.rows,
                   __builtin_ctz(c.page)};
@@ -680,8 +872,8 @@ hipError_t launch_attn(const KvCall &c, const uint16_t *q, int64_t ldq, const ui
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    attn_join_kernel<<<dim3((uint32_t)(p.items * c.kv_heads << (p.shift - 4))), 256, 0, stream>>>(
-        a, c.dim, p.shift);
+    const int64_t joins = (p.items * c.kv_heads << p.shift) / 4;
+    attn_join_kernel<<<dim3((uint32_t)joins), 256, 0, stream>>>(a, c.dim, p.shift);
     return hipGetLastError();
 }
 

@@ -147,7 +147,8 @@ KV_INLINE bool kv_tile(const KvBatch &b, int64_t item, int tiles, int group, int
     t.rows = (int)kv_min((int64_t)1 << shift, all - row0);
     const int from = t.seq.len - t.seq.n;
     const int64_t first = from + t.row0 / group, last = from + (t.row0 + t.rows - 1) / group;
-    const int64_t cap = kv_min((int64_t)t.seq.len, (int64_t)b.blocks << b.page_shift);
+    // without a page nothing is seen; with one, its first bytes may always be read
+    const int64_t cap = b.pages > 0 ? kv_min((int64_t)t.seq.len, (int64_t)b.blocks << b.page_shift) : 0;
     t.hi = (int)kv_max((int64_t)0, causal ? kv_min(cap, last + 1) : cap);
     t.lo = window ? (int)kv_max((int64_t)0, kv_min((int64_t)t.hi, first - window + 1)) : 0;
     return true;

@@ -158,7 +158,7 @@ hipError_t launch_kv8_read(const KvCall &c, const uint8_t *kv, const float *scal
 size_t attn_workspace_bytes(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows,
                             int64_t max_tokens, int q_heads, int kv_heads, int dim);
 int64_t attn_grid(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows, int64_t max_tokens,
-                  int q_heads, int kv_heads);
+                  int q_heads, int kv_heads, int dim);
 hipError_t launch_attn(const KvCall &c, const uint16_t *q, int64_t ldq, const uint8_t *kv,
                        const float *kv_scale, int64_t max_rows, int32_t q_heads, bool causal,
                        int32_t window, float scale, uint16_t *out, int64_t ldo, float *lse,
