@@ -71,6 +71,7 @@ CASES = [(1, 32, 8, 128, 128, False, BF, BF), (7, 14, 2, 96, 32, True, F, BF),
          (5, 9, 3, 256, 256, True, BF, BF), (5, 9, 3, 256, 64, False, F, F),
          (4, 17, 1, 192, 192, False, BF, BF), (4, 2, 2, 80, 40, False, BF, BF),
          (4, 33, 4, 72, 16, True, F, BF), (300, 64, 8, 128, 128, False, BF, BF),
+         (601, 37, 3, 64, 64, False, BF, BF), (500, 13, 6, 256, 64, True, F, BF),
          (1, 1, 8, 128, 8, False, BF, BF)]
 
 

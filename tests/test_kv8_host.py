@@ -52,7 +52,7 @@ def rope(lib, **kw):
     (dict(in_dtype=I32), UNSUPPORTED),
     (dict(out_dtype=I32), UNSUPPORTED),
     (dict(tokens=1 << 24), UNSUPPORTED),
-    (dict(tokens=1 << 22, q_heads=64, ldq=16384, ldqo=8192), UNSUPPORTED),
+    (dict(tokens=1 << 23, q_heads=64, ldq=16384, ldqo=8192), UNSUPPORTED),
     (dict(q=MIS), MISALIGNED), (dict(k=MIS), MISALIGNED), (dict(qo=MIS), MISALIGNED),
     (dict(ko=MIS), MISALIGNED), (dict(qw=MIS), MISALIGNED), (dict(kw=MIS), MISALIGNED),
     (dict(table=MIS), MISALIGNED), (dict(pos=ODD), MISALIGNED),

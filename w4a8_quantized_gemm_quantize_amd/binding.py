@@ -729,37 +729,57 @@ def lora_add(x, a, b, ids, y, scale=None, out=None, workspace=None, stream=None)
 
 # --------------------------------------- attention over an 8-bit cache --
 
-def _heads(fn, t, dtypes, name, rows=None, heads=None, dim=None):
-    """A 3-D CUDA tensor [rows, heads, head_dim] of one of `dtypes` (of these sizes where
-    given) whose rows are contiguous; returns the elements from one row to the next."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
-        raise ValueError(f"{fn}: {name} must be a [rows, heads, head_dim] CUDA tensor")
+def _misplaced(fn, t, name, dev):
+    """What is wrong with a tensor argument that is not on the current device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{fn}: {name} must be a CUDA tensor")
+    raise ValueError(f"{fn}: {name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _device_of(fn, t, name):
+    """The index of a tensor's device, which has to be the current one: launches go there."""
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
+        _misplaced(fn, t, name, -1)
+    dev = _raw_device() if _raw_device is not None else torch.cuda.current_device()
+    if t.get_device() != dev:
+        _misplaced(fn, t, name, dev)
+    return dev
+
+
+def _heads(fn, t, dtypes, name, dev, rows=None, heads=None, dim=None):
+    """A tensor [rows, heads, head_dim] on the current device `dev` of one of `dtypes` (of
+    these sizes where given) whose rows are contiguous; returns its sizes and the elements
+    from one row to the next."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _misplaced(fn, t, name, dev)
     if t.dtype not in dtypes:
         raise ValueError(f"{fn}: {name} must be of dtype {' or '.join(map(str, dtypes))}, "
                          f"not {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{fn}: {name} must be [rows, heads, head_dim]")
     r, h, d = t.shape
-    for have, need, what in ((r, rows, "rows"), (h, heads, "heads"), (d, dim, "head_dim")):
-        if need is not None and have != need:
-            raise W4A8SizeError(fn, f"{name} ({what})", have, need)
+    if (rows is not None and r != rows) or (heads is not None and h != heads) or \
+            (dim is not None and d != dim):
+        for have, need, what in ((r, rows, "rows"), (h, heads, "heads"), (d, dim, "head_dim")):
+            if need is not None and have != need:
+                raise W4A8SizeError(fn, f"{name} ({what})", have, need)
     if t.is_contiguous():
-        return h * d
+        return r, h, d, h * d
     sr, sh, sd = t.stride()
     if (d > 1 and sd != 1) or (h > 1 and sh != d):
         raise ValueError(f"{fn}: rows of {name} must be contiguous")
-    return sr if r > 1 else h * d
+    return r, h, d, sr if r > 1 else h * d
 
 
-def _here(fn, device, *tensors):
-    """A launch goes to the current device: its tensors must be there."""
-    at = _raw_device() if _raw_device is not None else torch.cuda.current_device()
-    if device.index != at:
-        raise ValueError(f"{fn}: tensors are on {device}, the current device is cuda:{at}")
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"{fn}: tensors are on {device} and on {t.device}")
-
-
-_I32T = (torch.int32,)
+def _flat(fn, t, dtype, need, name, dev):
+    """A contiguous tensor of `dtype` on the current device `dev` with at least `need`
+    elements."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _misplaced(fn, t, name, dev)
+    if t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor")
+    if t.numel() < need:
+        raise W4A8SizeError(fn, name, t.numel(), need)
 
 
 def qk_norm_rope(q, k, cos_sin=None, positions=None, q_weight=None, k_weight=None,
@@ -774,10 +794,9 @@ def qk_norm_rope(q, k, cos_sin=None, positions=None, q_weight=None, k_weight=Non
     [tokens]; a row whose position is outside the table is left as it was.  Pairs are rot / 2
     apart, or neighbours where interleaved.  q_out and k_out may be q and k."""
     fn = "qk_norm_rope"
-    ldq = _heads(fn, q, _FLOATS, "q")
-    tokens, q_heads, dim = q.shape
-    ldk = _heads(fn, k, (q.dtype,), "k", tokens, None, dim)
-    kv_heads = k.size(1)
+    dev = _device_of(fn, q, "q")
+    tokens, q_heads, dim, ldq = _heads(fn, q, _FLOATS, "q", dev)
+    _, kv_heads, _, ldk = _heads(fn, k, (q.dtype,), "k", dev, tokens, None, dim)
     if out_dtype is None:
         out_dtype = (q_out if q_out is not None else k_out if k_out is not None else q).dtype
     if out_dtype not in _FLOATS:
@@ -785,23 +804,25 @@ def qk_norm_rope(q, k, cos_sin=None, positions=None, q_weight=None, k_weight=Non
     if q_out is None:
         q_out, ldqo = _empty(stream, (tokens, q_heads, dim), out_dtype, q.device), q_heads * dim
     else:
-        ldqo = _heads(fn, q_out, (out_dtype,), "q_out", tokens, q_heads, dim)
+        ldqo = _heads(fn, q_out, (out_dtype,), "q_out", dev, tokens, q_heads, dim)[3]
     if k_out is None:
         k_out, ldko = _empty(stream, (tokens, kv_heads, dim), out_dtype, q.device), kv_heads * dim
     else:
-        ldko = _heads(fn, k_out, (out_dtype,), "k_out", tokens, kv_heads, dim)
-    _sized(fn, q_weight, _F32, dim, "q_weight")
-    _sized(fn, k_weight, _F32, dim, "k_weight")
+        ldko = _heads(fn, k_out, (out_dtype,), "k_out", dev, tokens, kv_heads, dim)[3]
+    if q_weight is not None:
+        _flat(fn, q_weight, torch.float32, dim, "q_weight", dev)
+    if k_weight is not None:
+        _flat(fn, k_weight, torch.float32, dim, "k_weight", dev)
     max_pos = rot = 0
     if cos_sin is not None:
-        _sized(fn, cos_sin, _F32, 0, "cos_sin")
+        _flat(fn, cos_sin, torch.float32, 0, "cos_sin", dev)
         if cos_sin.dim() != 2:
             raise ValueError(f"{fn}: cos_sin must be [max_pos, rot]")
         max_pos, rot = cos_sin.shape
-        _sized(fn, positions, _I32T, tokens, "positions")
+        if positions is not None:            # the library refuses a missing one itself
+            _flat(fn, positions, torch.int32, tokens, "positions", dev)
     else:
         positions = None
-    _here(fn, q.device, k, cos_sin, positions, q_weight, k_weight, q_out, k_out)
     status = _lib.w4a8_qk_norm_rope(
         q.data_ptr(), ldq, k.data_ptr(), ldk, _FLOATS[q.dtype], _addr(q_weight), _addr(k_weight),
         eps, _addr(cos_sin), _addr(positions), max_pos, rot, 1 if interleaved else 0, tokens,
@@ -819,30 +840,34 @@ def kv8_cache(pages: int, kv_heads: int, head_dim: int, page: int, device="cuda"
     return kv, torch.zeros((pages, kv_heads, 2), dtype=torch.float32, device=device)
 
 
-def _kv_args(fn, kv, kv_scale, block_table, lens, row_start, rows):
-    """Checks what the calls on the cache share; (ldb, blocks, seqs, rows)."""
-    if not isinstance(kv, torch.Tensor) or kv.dim() != 5 or kv.size(2) != 2:
+def _kv_args(fn, kv, kv_scale, block_table, lens, row_start, dev):
+    """Checks what the calls on the cache share; (the cache's sizes, ldb, blocks, seqs)."""
+    _flat(fn, kv, torch.uint8, 0, "kv", dev)
+    if kv.dim() != 5 or kv.size(2) != 2:
         raise ValueError(f"{fn}: kv must be [pages, kv_heads, 2, page, head_dim]")
-    _sized(fn, kv, (torch.uint8,), 0, "kv")
-    if not isinstance(kv_scale, torch.Tensor):
-        raise ValueError(f"{fn}: kv_scale must be [pages, kv_heads, 2]")
-    _sized(fn, kv_scale, _F32, kv.size(0) * kv.size(1) * 2, "kv_scale")
-    if not isinstance(lens, torch.Tensor) or lens.dim() != 1:
+    pages, kv_heads, _, page, dim = kv.shape
+    _flat(fn, kv_scale, torch.float32, pages * kv_heads * 2, "kv_scale", dev)
+    _flat(fn, lens, torch.int32, 0, "lens", dev)
+    if lens.dim() != 1:
         raise ValueError(f"{fn}: lens must be [seqs]")
-    _sized(fn, lens, _I32T, 0, "lens")
     seqs = lens.size(0)
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
-        raise ValueError(f"{fn}: block_table must be [seqs, blocks]")
-    blocks = block_table.size(1)
-    ldb = _rows(fn, block_table, _I32T, blocks, "block_table")
-    if block_table.size(0) != seqs:
-        raise W4A8SizeError(fn, "block_table (rows)", block_table.size(0), seqs)
+    if not isinstance(block_table, torch.Tensor) or block_table.get_device() != dev:
+        _misplaced(fn, block_table, "block_table", dev)
+    if block_table.dtype != torch.int32 or block_table.dim() != 2:
+        raise ValueError(f"{fn}: block_table must be int32 [seqs, blocks]")
+    have, blocks = block_table.shape
+    if have != seqs:
+        raise W4A8SizeError(fn, "block_table (rows)", have, seqs)
+    ldb = blocks
+    if not block_table.is_contiguous():
+        ldb, step = block_table.stride()
+        if blocks > 1 and step != 1:
+            raise ValueError(f"{fn}: rows of block_table must be contiguous")
+        if seqs <= 1:
+            ldb = blocks
     if row_start is not None:
-        _sized(fn, row_start, _I32T, seqs + 1, "row_start")
-    elif rows is None:
-        rows = seqs
-    _here(fn, kv.device, kv_scale, block_table, lens, row_start)
-    return ldb, blocks, seqs, rows
+        _flat(fn, row_start, torch.int32, seqs + 1, "row_start", dev)
+    return (pages, kv_heads, page, dim), ldb, blocks, seqs
 
 
 def kv8_write(k, v, kv, kv_scale, block_table, lens, row_start=None, stream=None):
@@ -852,14 +877,11 @@ def kv8_write(k, v, kv, kv_scale, block_table, lens, row_start=None, stream=None
     block_table int32 [seqs, blocks] names the page of each run of `page` tokens (-1: none).
     One scale per page and head: older codes of a page are taken over to a scale that grew."""
     fn = "kv8_write"
-    ldk = _heads(fn, k, _FLOATS, "k")
-    rows, heads, dim = k.shape
-    ldv = _heads(fn, v, (k.dtype,), "v", rows, heads, dim)
-    ldb, blocks, seqs, _ = _kv_args(fn, kv, kv_scale, block_table, lens, row_start, rows)
-    pages, kv_heads, _, page, kv_dim = kv.shape
-    if heads != kv_heads or dim != kv_dim:
-        raise W4A8SizeError(fn, "a row of k", heads * dim, kv_heads * kv_dim)
-    _here(fn, kv.device, k, v)
+    dev = _device_of(fn, kv, "kv")
+    (pages, kv_heads, page, dim), ldb, blocks, seqs = _kv_args(fn, kv, kv_scale, block_table, lens,
+                                                               row_start, dev)
+    rows, _, _, ldk = _heads(fn, k, _FLOATS, "k", dev, None, kv_heads, dim)
+    ldv = _heads(fn, v, (k.dtype,), "v", dev, rows, kv_heads, dim)[3]
     status = _lib.w4a8_kv8_write(
         k.data_ptr(), ldk, v.data_ptr(), ldv, _FLOATS[k.dtype], block_table.data_ptr(), ldb, blocks,
         lens.data_ptr(), _addr(row_start), seqs, rows, kv_heads, dim, page, pages, kv.data_ptr(),
@@ -875,12 +897,16 @@ def kv8_read(kv, kv_scale, block_table, lens, row_start=None, tokens=None,
     `tokens` is row_start's last entry.  Tokens without a page read as zeros, rows of no
     token are left as they were."""
     fn = "kv8_read"
-    if tokens is None and row_start is not None:
-        if k is None:
+    dev = _device_of(fn, kv, "kv")
+    (pages, kv_heads, page, dim), ldb, blocks, seqs = _kv_args(fn, kv, kv_scale, block_table, lens,
+                                                               row_start, dev)
+    if tokens is None:
+        if row_start is None:
+            tokens = seqs
+        elif k is not None:
+            tokens = k.size(0)
+        else:
             raise ValueError(f"{fn}: tokens (or k and v) must be given with row_start")
-        tokens = k.size(0)
-    ldb, blocks, seqs, tokens = _kv_args(fn, kv, kv_scale, block_table, lens, row_start, tokens)
-    pages, kv_heads, _, page, dim = kv.shape
     if k is not None:
         out_dtype = k.dtype
     elif v is not None:
@@ -890,12 +916,11 @@ def kv8_read(kv, kv_scale, block_table, lens, row_start=None, tokens=None,
     if k is None:
         k, ldk = _empty(stream, (tokens, kv_heads, dim), out_dtype, kv.device), kv_heads * dim
     else:
-        ldk = _heads(fn, k, (out_dtype,), "k", tokens, kv_heads, dim)
+        ldk = _heads(fn, k, (out_dtype,), "k", dev, tokens, kv_heads, dim)[3]
     if v is None:
         v, ldv = _empty(stream, (tokens, kv_heads, dim), out_dtype, kv.device), kv_heads * dim
     else:
-        ldv = _heads(fn, v, (out_dtype,), "v", tokens, kv_heads, dim)
-    _here(fn, kv.device, k, v)
+        ldv = _heads(fn, v, (out_dtype,), "v", dev, tokens, kv_heads, dim)[3]
     status = _lib.w4a8_kv8_read(
         kv.data_ptr(), kv_scale.data_ptr(), block_table.data_ptr(), ldb, blocks, lens.data_ptr(),
         _addr(row_start), seqs, tokens, kv_heads, dim, page, pages, k.data_ptr(), ldk, v.data_ptr(),
@@ -926,20 +951,18 @@ def attn_kv8(q, kv, kv_scale, block_table, lens, row_start=None, max_rows=None,
     (default: all rows).  scale defaults to head_dim ** -0.5; window > 0: only the last
     `window` tokens up to the row's own.  A row that sees nothing gives 0 and -inf."""
     fn = "attn_kv8"
-    ldq = _heads(fn, q, (torch.bfloat16,), "q")
-    rows, q_heads, dim = q.shape
-    ldb, blocks, seqs, _ = _kv_args(fn, kv, kv_scale, block_table, lens, row_start, rows)
-    pages, kv_heads, _, page, kv_dim = kv.shape
-    if dim != kv_dim:
-        raise W4A8SizeError(fn, "a head of q", dim, kv_dim)
+    dev = _device_of(fn, kv, "kv")
+    (pages, kv_heads, page, dim), ldb, blocks, seqs = _kv_args(fn, kv, kv_scale, block_table, lens,
+                                                               row_start, dev)
+    rows, q_heads, _, ldq = _heads(fn, q, (torch.bfloat16,), "q", dev, None, None, dim)
     if max_rows is None:
         max_rows = 1 if row_start is None else max(rows, 1)
     if out is None:
         out, ldo = _empty(stream, (rows, q_heads, dim), torch.bfloat16, q.device), q_heads * dim
     else:
-        ldo = _heads(fn, out, (torch.bfloat16,), "out", rows, q_heads, dim)
+        ldo = _heads(fn, out, (torch.bfloat16,), "out", dev, rows, q_heads, dim)[3]
     if lse is not None:
-        _sized(fn, lse, _F32, rows * q_heads, "lse")
+        _flat(fn, lse, torch.float32, rows * q_heads, "lse", dev)
     elif want_lse:
         lse = _empty(stream, (rows, q_heads), torch.float32, q.device)
     if workspace is None:
@@ -948,8 +971,7 @@ def attn_kv8(q, kv, kv_scale, block_table, lens, row_start=None, max_rows=None,
         if need:
             workspace = _workspace(stream, need, q.device)
     else:
-        _sized(fn, workspace, _U8, 0, "workspace")
-    _here(fn, kv.device, q, out, lse, workspace)
+        _flat(fn, workspace, torch.uint8, 0, "workspace", dev)
     status = _lib.w4a8_attn_kv8(
         q.data_ptr(), ldq, kv.data_ptr(), kv_scale.data_ptr(), block_table.data_ptr(), ldb, blocks,
         lens.data_ptr(), _addr(row_start), seqs, rows, max_rows, q_heads, kv_heads, dim, page, pages,

@@ -74,21 +74,45 @@ KV_INLINE int kv_page(const KvBatch &b, int s, int64_t at) {
     return p >= 0 && p < b.pages ? p : -1;
 }
 
+// How many of the 64 lanes hold: a ballot on the device (every lane of the wavefront calls
+// it), a loop on the host.
+template <class F>
+KV_INLINE int kv_count64(F holds) {
+#ifdef __HIP_DEVICE_COMPILE__
+    return __popcll(__ballot(holds((int)__lane_id())));
+#else
+    int n = 0;
+    for (int lane = 0; lane < 64; ++lane) n += holds(lane) ? 1 : 0;
+    return n;
+#endif
+}
+
 // Work items of ragged sequences without a table of them: sequence s takes the items from
 // base(s) = (start[s] * num >> shift) + extra * s on, `extra` enough that base(s + 1) -
 // base(s) covers what its rows need; a launch holds base(seqs) of them with start[seqs] =
-// rows.  Returns the last sequence with base(s) <= item.
+// rows.  Returns the last sequence with base(s) <= item, 64 candidates at a time: one load
+// deep for 64 sequences, where a bisection is six dependent ones.
+KV_INLINE int64_t kv_base(const KvBatch &b, int s, int num, int shift, int extra) {
+    const int64_t st = b.start ? kv_max(0, kv_min(b.start[s], b.rows)) : s;
+    return ((st * num) >> shift) + (int64_t)extra * s;
+}
 KV_INLINE int kv_find_seq(const KvBatch &b, int64_t item, int num, int shift, int extra,
                           int64_t &base) {
-    int lo = 0, hi = b.seqs - 1;
-    while (lo < hi) {
-        const int mid = (int)(((int64_t)lo + hi + 1) >> 1);
-        const int64_t st = b.start ? kv_max(0, kv_min(b.start[mid], b.rows)) : mid;
-        if (((st * num) >> shift) + (int64_t)extra * mid <= item) lo = mid;
-        else hi = mid - 1;
+    int lo = 0, n = b.seqs;
+    while (n > 1) {
+        const int step = (int)(((int64_t)n + 63) / 64);
+        int below = kv_count64([&](int lane) {
+            const int64_t at = (int64_t)lane * step;
+            return at < n && kv_base(b, lo + (int)at, num, shift, extra) <= item;
+        });
+        below = kv_max(below, 1) - 1;
+        lo += below * step;
+        n = kv_min(step, n - below * step);
     }
-    const int64_t st = b.start ? kv_max(0, kv_min(b.start[lo], b.rows)) : lo;
-    base = ((st * num) >> shift) + (int64_t)extra * lo;
+#ifdef __HIP_DEVICE_COMPILE__
+    lo = __builtin_amdgcn_readfirstlane(lo);
+#endif
+    base = kv_base(b, lo, num, shift, extra);
     return lo;
 }
 
