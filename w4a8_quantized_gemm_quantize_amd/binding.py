@@ -729,16 +729,19 @@ def lora_add(x, a, b, ids, y, scale=None, out=None, workspace=None, stream=None)
 
 # --------------------------------------- attention over an 8-bit cache --
 
+_Tensor = torch.Tensor
+
+
 def _misplaced(fn, t, name, dev):
     """What is wrong with a tensor argument that is not on the current device."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise ValueError(f"{fn}: {name} must be a CUDA tensor")
     raise ValueError(f"{fn}: {name} is on {t.device}, the current device is cuda:{dev}")
 
 
 def _device_of(fn, t, name):
     """The index of a tensor's device, which has to be the current one: launches go there."""
-    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
+    if not isinstance(t, _Tensor) or t.get_device() < 0:
         _misplaced(fn, t, name, -1)
     dev = _raw_device() if _raw_device is not None else torch.cuda.current_device()
     if t.get_device() != dev:
@@ -746,11 +749,21 @@ def _device_of(fn, t, name):
     return dev
 
 
+def _new(stream, like, dtype, *sizes):
+    """A new tensor on the device of `like`, for a call enqueued on `stream` (as _empty; sizes
+    one by one are 0.4 us faster than as a tuple)."""
+    if stream is not None:
+        return _empty(stream, sizes, dtype, like.device)
+    if dtype is like.dtype:
+        return like.new_empty(*sizes)
+    return torch.empty(*sizes, dtype=dtype, device=like.device)
+
+
 def _heads(fn, t, dtypes, name, dev, rows=None, heads=None, dim=None):
     """A tensor [rows, heads, head_dim] on the current device `dev` of one of `dtypes` (of
     these sizes where given) whose rows are contiguous; returns its sizes and the elements
     from one row to the next."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+    if not isinstance(t, _Tensor) or t.get_device() != dev:
         _misplaced(fn, t, name, dev)
     if t.dtype not in dtypes:
         raise ValueError(f"{fn}: {name} must be of dtype {' or '.join(map(str, dtypes))}, "
@@ -774,7 +787,7 @@ def _heads(fn, t, dtypes, name, dev, rows=None, heads=None, dim=None):
 def _flat(fn, t, dtype, need, name, dev):
     """A contiguous tensor of `dtype` on the current device `dev` with at least `need`
     elements."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+    if not isinstance(t, _Tensor) or t.get_device() != dev:
         _misplaced(fn, t, name, dev)
     if t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor")
@@ -802,11 +815,11 @@ def qk_norm_rope(q, k, cos_sin=None, positions=None, q_weight=None, k_weight=Non
     if out_dtype not in _FLOATS:
         raise ValueError(f"{fn}: out_dtype must be float32 or bfloat16")
     if q_out is None:
-        q_out, ldqo = _empty(stream, (tokens, q_heads, dim), out_dtype, q.device), q_heads * dim
+        q_out, ldqo = _new(stream, q, out_dtype, tokens, q_heads, dim), q_heads * dim
     else:
         ldqo = _heads(fn, q_out, (out_dtype,), "q_out", dev, tokens, q_heads, dim)[3]
     if k_out is None:
-        k_out, ldko = _empty(stream, (tokens, kv_heads, dim), out_dtype, q.device), kv_heads * dim
+        k_out, ldko = _new(stream, q, out_dtype, tokens, kv_heads, dim), kv_heads * dim
     else:
         ldko = _heads(fn, k_out, (out_dtype,), "k_out", dev, tokens, kv_heads, dim)[3]
     if q_weight is not None:
@@ -851,7 +864,7 @@ def _kv_args(fn, kv, kv_scale, block_table, lens, row_start, dev):
     if lens.dim() != 1:
         raise ValueError(f"{fn}: lens must be [seqs]")
     seqs = lens.size(0)
-    if not isinstance(block_table, torch.Tensor) or block_table.get_device() != dev:
+    if not isinstance(block_table, _Tensor) or block_table.get_device() != dev:
         _misplaced(fn, block_table, "block_table", dev)
     if block_table.dtype != torch.int32 or block_table.dim() != 2:
         raise ValueError(f"{fn}: block_table must be int32 [seqs, blocks]")
@@ -914,11 +927,11 @@ def kv8_read(kv, kv_scale, block_table, lens, row_start=None, tokens=None,
     if out_dtype not in _FLOATS:
         raise ValueError(f"{fn}: out_dtype must be float32 or bfloat16")
     if k is None:
-        k, ldk = _empty(stream, (tokens, kv_heads, dim), out_dtype, kv.device), kv_heads * dim
+        k, ldk = _new(stream, kv, out_dtype, tokens, kv_heads, dim), kv_heads * dim
     else:
         ldk = _heads(fn, k, (out_dtype,), "k", dev, tokens, kv_heads, dim)[3]
     if v is None:
-        v, ldv = _empty(stream, (tokens, kv_heads, dim), out_dtype, kv.device), kv_heads * dim
+        v, ldv = _new(stream, kv, out_dtype, tokens, kv_heads, dim), kv_heads * dim
     else:
         ldv = _heads(fn, v, (out_dtype,), "v", dev, tokens, kv_heads, dim)[3]
     status = _lib.w4a8_kv8_read(
@@ -958,13 +971,13 @@ def attn_kv8(q, kv, kv_scale, block_table, lens, row_start=None, max_rows=None,
     if max_rows is None:
         max_rows = 1 if row_start is None else max(rows, 1)
     if out is None:
-        out, ldo = _empty(stream, (rows, q_heads, dim), torch.bfloat16, q.device), q_heads * dim
+        out, ldo = _new(stream, q, torch.bfloat16, rows, q_heads, dim), q_heads * dim
     else:
         ldo = _heads(fn, out, (torch.bfloat16,), "out", dev, rows, q_heads, dim)[3]
     if lse is not None:
         _flat(fn, lse, torch.float32, rows * q_heads, "lse", dev)
     elif want_lse:
-        lse = _empty(stream, (rows, q_heads), torch.float32, q.device)
+        lse = _new(stream, kv_scale, torch.float32, rows, q_heads)
     if workspace is None:
         need = attn_kv8_workspace_bytes(rows, seqs, row_start is not None, max_rows, blocks,
                                         q_heads, kv_heads, dim, page)

@@ -223,10 +223,9 @@ w4a8_status check_kv_pointers(const w4a8::KvCall &c, const void *kv, const void 
 w4a8_status debug_check_rows(hipStream_t stream, const void *p, int64_t rows, int64_t ld,
                              int64_t cols, bool bf16) {
     w4a8_status st = W4A8_OK;
-    if (debug_sync_enabled())
-        for (int64_t t = 0; t < rows && st == W4A8_OK; ++t)
-            st = debug_check_inputs(
-                stream, {{(const uint8_t *)p + t * ld * (bf16 ? 2 : 4), (size_t)cols, bf16}});
+    for (int64_t t = 0; t < rows && st == W4A8_OK; ++t)
+        st = debug_check_inputs(
+            stream, {{(const uint8_t *)p + t * ld * (bf16 ? 2 : 4), (size_t)cols, bf16}});
     return st;
 }
 
@@ -698,13 +697,15 @@ w4a8_status w4a8_qk_norm_rope(const void *q, int64_t ldq, const void *k, int64_t
         (kv_heads && (!aligned16(k) || !aligned16(k_out))) || !aligned16(q_weight) ||
         !aligned16(k_weight) || (rot && (!aligned4(positions) || !aligned16(cos_sin))))
         return W4A8_ERR_MISALIGNED;
-    w4a8_status st = debug_check_inputs(stream, {{q_weight, (size_t)head_dim, false},
-                                                 {k_weight, (size_t)head_dim, false}});
-    if (st == W4A8_OK && q_heads)
-        st = debug_check_rows(stream, q, tokens, ldq, (int64_t)q_heads * head_dim, in);
-    if (st == W4A8_OK && kv_heads)
-        st = debug_check_rows(stream, k, tokens, ldk, (int64_t)kv_heads * head_dim, in);
-    if (st != W4A8_OK) return st;
+    if (debug_sync_enabled()) {
+        w4a8_status st = debug_check_inputs(stream, {{q_weight, (size_t)head_dim, false},
+                                                     {k_weight, (size_t)head_dim, false}});
+        if (st == W4A8_OK && q_heads)
+            st = debug_check_rows(stream, q, tokens, ldq, (int64_t)q_heads * head_dim, in);
+        if (st == W4A8_OK && kv_heads)
+            st = debug_check_rows(stream, k, tokens, ldk, (int64_t)kv_heads * head_dim, in);
+        if (st != W4A8_OK) return st;
+    }
     return finish(w4a8::launch_qk_norm_rope(q, ldq, k, ldk, in, q_weight, k_weight, eps, cos_sin,
                                             positions, max_pos, rot, interleaved != 0, tokens,
                                             q_heads, kv_heads, head_dim, q_out, ldqo, k_out, ldko,
@@ -733,8 +734,11 @@ w4a8_status w4a8_kv8_write(const void *k, int64_t ldk, const void *v, int64_t ld
     if (!k || !v) return W4A8_ERR_NULL;
     if (!aligned16(k) || !aligned16(v)) return W4A8_ERR_MISALIGNED;
     st = check_kv_pointers(c, kv, kv_scale);
-    if (st == W4A8_OK) st = debug_check_rows(stream, k, rows, ldk, (int64_t)kv_heads * head_dim, bf16);
-    if (st == W4A8_OK) st = debug_check_rows(stream, v, rows, ldv, (int64_t)kv_heads * head_dim, bf16);
+    if (st == W4A8_OK && debug_sync_enabled()) {
+        st = debug_check_rows(stream, k, rows, ldk, (int64_t)kv_heads * head_dim, bf16);
+        if (st == W4A8_OK)
+            st = debug_check_rows(stream, v, rows, ldv, (int64_t)kv_heads * head_dim, bf16);
+    }
     if (st != W4A8_OK) return st;
     return finish(w4a8::launch_kv8_write(c, k, ldk, v, ldv, bf16, kv, kv_scale, stream), stream);
 }
@@ -804,7 +808,8 @@ w4a8_status w4a8_attn_kv8(const uint16_t *q, int64_t ldq, const uint8_t *kv,
         return W4A8_ERR_MISALIGNED;
     if (ws_bytes < need) return W4A8_ERR_SHAPE;
     st = check_kv_pointers(c, kv, kv_scale);
-    if (st == W4A8_OK) st = debug_check_rows(stream, q, rows, ldq, (int64_t)q_heads * head_dim, true);
+    if (st == W4A8_OK && debug_sync_enabled())
+        st = debug_check_rows(stream, q, rows, ldq, (int64_t)q_heads * head_dim, true);
     if (st != W4A8_OK) return st;
     return finish(w4a8::launch_attn(c, q, ldq, kv, kv_scale, max_rows, q_heads, causal != 0, window,
                                     scale, out, ldo, lse, workspace, stream),
