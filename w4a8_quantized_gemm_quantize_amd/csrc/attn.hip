@@ -357,7 +357,7 @@ void attn_rows_kernel(AttnArgs a) {
     }
 }
 
-// ---- many rows: 32 a wavefront, 128 or 256 packed rows a workgroup ----
+// ---- many rows: 128 packed rows a workgroup, 32 a wavefront ----
 //
 // The wavefronts share 64 tokens at a time, converted once to halves in LDS in the order of
 // the operands of v_mfma_f32_32x32x16_f16 (A: lane l holds 8 of row l % 32, k = 8 (l / 32) ..;
@@ -373,17 +373,15 @@ __device__ __forceinline__ f32x16 mfma32(half8_t a, half8_t b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 constexpr int min_of(int a, int b) { return a < b ? a : b; }
-// Wavefronts of a workgroup, by registers: eight are two on a SIMD, four three (up to 64
-// elements a head) or one.
-constexpr int tile_waves(int dim) { return dim > 64 && dim <= 128 ? 8 : 4; }
-
-constexpr int tile_groups(int dim) { return dim <= 64 ? 3 : 1; }   // workgroups of a compute unit
+// Workgroups of a compute unit, by registers and LDS.  (Workgroups of eight wavefronts and 256
+// rows stage half as much each, and gain nothing: 671 us for 673 on 5124 and 3067 rows of 64
+// x 128, 8 us more on short prompts, which have too few of them.)
+constexpr int tile_groups(int dim) { return dim <= 64 ? 3 : dim <= 128 ? 2 : 1; }
+constexpr int kTileShift = 7;                    // packed rows of a tile: 128
 
 template <int C, bool HALF>
-__global__ __launch_bounds__(64 * tile_waves(64 * C + 32 * HALF), tile_waves(64 * C + 32 * HALF) / 4 * tile_groups(64 * C + 32 * HALF))
-void attn_tile_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_tile_kernel(AttnArgs a) {
     constexpr int kDim = 64 * C + (HALF ? 32 : 0), kSteps = kDim / 16, kBlocks = kDim / 32;
-    constexpr int kTW = tile_waves(kDim), kTileShift = kTW == 8 ? 8 : 7;
     constexpr int kSub = 16 * kDim;              // halves of 16 tokens
     __shared__ __attribute__((aligned(16))) _Float16 kbuf[2][4 * kSub], vbuf[2][4 * kSub];
     __shared__ f32x4 page[4][4];                 // of 16 tokens: page_terms
@@ -444,18 +442,14 @@ void attn_tile_kernel(AttnArgs a) {
         for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
     float m = -1e30f, l = 0.0f;
 
-    // A wavefront stages 16 tokens of each run of 64: their keys, their values (the upper
-    // four of eight wavefronts), or both.
-    const int sub = wave & 3;
-    const bool does_keys = kTW == 4 || wave < 4, does_values = kTW == 4 || wave >= 4;
-    // Lane x: of the tokens of run j_in + x the place of their keys and the page's terms, 64
+    // A wavefront stages 16 tokens of each run of 64.  Lane x: of the tokens of run j_in + x the place of their keys and the page's terms, 64
     // runs at a time (as in attn_rows_kernel).
     int j_in = j0;
     int64_t at_in = 0;
     f32x4 terms_in;
     auto look_up = [&](int j) {
         j_in = j;
-        const int64_t at = (int64_t)(j + lane) * 64 + sub * 16;
+        const int64_t at = (int64_t)(j + lane) * 64 + wave * 16;
         const int pg = j + lane < j1 && at < t.hi ? kv_page(a.b, t.s, at >> a.b.page_shift) : -1;
         at_in = 0;
         float sk = 0.0f, sv = -1.0f;
@@ -494,35 +488,30 @@ void attn_tile_kernel(AttnArgs a) {
                       lane_value(terms_in.z, j - j_in), 0.0f};
     };
     auto load_values = [&](int j) { load(part_of(j) + to_values, vraw); };
+    // What was loaded, as halves, in pieces: keys, then values.
+    constexpr int kKeyPieces = 2 * C + HALF, kValuePieces = 4 * C + 2 * HALF;
+    auto store_key = [&](int j, int n) {         // n: half a record
+        _Float16 *to = kbuf[j & 1] + wave * kSub + n * 512 + lane * 8;
+        const int c = n >> 1, x = 2 * (n & 1);
+        *(half8_t *)to = n < 2 * C ? codes8h(kraw.r[c < C ? c : 0][x], kraw.r[c < C ? c : 0][x + 1])
+                                   : codes8h(kraw.h.x, kraw.h.y);
+    };
+    _Float16 *const value_lane = vbuf[0] + wave * kSub + (lane >> 4 & 1) * 256 + (lane & 15) * 8 +
+                                 (lane >> 5) * 4;
+    auto store_value = [&](int j, int n) {       // n: 16 elements
+        uint32_t lo, hi;
+        codes4(n < 4 * C ? vraw.r[n < 4 * C ? n >> 2 : 0][n & 3] : vraw.h[n & 1], lo, hi);
+        *(u32x2 *)(value_lane + (j & 1) * (4 * kSub) + (n >> 1) * 512 + (n & 1) * 128) = u32x2{lo, hi};
+    };
+    auto store_terms = [&](int j) { page[j & 3][wave] = terms; };
     auto store_keys = [&](int j) {
-        _Float16 *kb = kbuf[j & 1] + sub * kSub;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            *(half8_t *)(kb + (c * 2) * 512 + lane * 8) = codes8h(kraw.r[c].x, kraw.r[c].y);
-            *(half8_t *)(kb + (c * 2 + 1) * 512 + lane * 8) = codes8h(kraw.r[c].z, kraw.r[c].w);
-        }
-        if constexpr (HALF) *(half8_t *)(kb + (C * 2) * 512 + lane * 8) = codes8h(kraw.h.x, kraw.h.y);
-        page[j & 3][sub] = terms;
+        for (int n = 0; n < kKeyPieces; ++n) store_key(j, n);
+        store_terms(j);
     };
     auto store_values = [&](int j) {
-        const int g = lane >> 4, e = lane & 15;
-        _Float16 *vl = vbuf[j & 1] + sub * kSub + (g & 1) * 256 + e * 8 + (g >> 1) * 4;
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                uint32_t lo, hi;
-                codes4(vraw.r[c][x], lo, hi);
-                *(u32x2 *)(vl + (c * 2 + (x >> 1)) * 512 + (x & 1) * 128) = u32x2{lo, hi};
-            }
-        if constexpr (HALF) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                uint32_t lo, hi;
-                codes4(vraw.h[x], lo, hi);
-                *(u32x2 *)(vl + C * 2 * 512 + x * 128) = u32x2{lo, hi};
-            }
-        }
+        for (int n = 0; n < kValuePieces; ++n) store_value(j, n);
     };
     const int sub_lane = (lane & 31) >> 4, rec = (h * 16 + (lane & 15)) * 8;
     auto key_operand = [&](int j, int half, int k) {
@@ -604,13 +593,20 @@ void attn_tile_kernel(AttnArgs a) {
                     }
                 }
             }
+            if (half) {
+                // and its share of the next tokens' halves
+                constexpr int kPieces = kKeyPieces + kValuePieces;
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i)
+                    if (i * kAll / kPieces == n) {
+                        if (i < kKeyPieces) store_key(j + 2, i);
+                        else store_value(j + 1, i - kKeyPieces);
+                    }
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
+        if (half) store_terms(j + 2);
         const float most = fmaxf(sum[0], sum[1]);
-        if (kTW == 4 && half) {
-            store_keys(j + 2);
-            store_values(j + 1);
-        }
         if (__any(!(most <= 0x1p14f))) {
             float best = -1e30f;
 #pragma unroll
@@ -631,21 +627,17 @@ void attn_tile_kernel(AttnArgs a) {
     half8_t p0[2], p1[2];
     if (j0 < j1) {
         look_up(j0);
-        if (does_keys) {
-            load_keys(j0);
-            store_keys(j0);
-            load_keys(j0 + 1);
-            store_keys(j0 + 1);
-            load_keys(j0 + 2);
-        }
-        if (does_values) {
-            load_values(j0);
-            store_values(j0);
-            // what the first step multiplies by 0
-            for (int x = lane; x < kSub / 8; x += 64)
-                *(u32x4 *)(vbuf[(j0 + 1) & 1] + sub * kSub + x * 8) = u32x4{0, 0, 0, 0};
-            load_values(j0 + 1);
-        }
+        load_keys(j0);
+        load_values(j0);
+        store_keys(j0);
+        store_values(j0);
+        // what the first step multiplies by 0
+        for (int x = lane; x < kSub / 8; x += 64)
+            *(u32x4 *)(vbuf[(j0 + 1) & 1] + wave * kSub + x * 8) = u32x4{0, 0, 0, 0};
+        load_keys(j0 + 1);
+        load_values(j0 + 1);
+        store_keys(j0 + 1);
+        load_keys(j0 + 2);
         __syncthreads();
 #pragma unroll
         for (int e = 0; e < 16; ++e) s0[e] = 0.0f;
@@ -656,21 +648,13 @@ void attn_tile_kernel(AttnArgs a) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) p1[x][e] = (_Float16)0.0f;
     }
-    auto load_next = [&](int j) {
-        if (does_values) load_values(j + 2);
-        if (j + 3 - j_in == 64) look_up(j + 3);
-        if (does_keys) load_keys(j + 3);
-    };
     for (int j = j0; j < j1; ++j) {
         step(j, 0, s0, s1, p1, p0);
         __syncthreads();
-        if (kTW == 8) {
-            if (does_keys) store_keys(j + 2);
-            else store_values(j + 1);
-            load_next(j);
-        }
         step(j, 1, s1, s0, p0, p1);
-        if (kTW == 4) load_next(j);
+        load_values(j + 2);
+        if (j + 3 - j_in == 64) look_up(j + 3);
+        load_keys(j + 3);
     }
     if (j0 < j1) {
 #pragma unroll
@@ -771,7 +755,7 @@ template <int C, bool HALF>
 void launch_dim(const AttnArgs &a, int shift, hipStream_t stream) {
     const dim3 grid((uint32_t)(a.items * a.heads * a.splits));
     if (shift == 4) attn_rows_kernel<C, HALF><<<grid, kWaves * 64, 0, stream>>>(a);
-    else attn_tile_kernel<C, HALF><<<grid, 64 * tile_waves(64 * C + 32 * HALF), 0, stream>>>(a);
+    else attn_tile_kernel<C, HALF><<<grid, 256, 0, stream>>>(a);
 }
 
 struct Plan {
@@ -795,7 +779,7 @@ Plan attn_plan(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows, int64_
     const int64_t group = q_heads / kv_heads;
     max_rows = !ragged ? 1 : max_rows < rows ? max_rows : rows;
     Plan p;
-    p.shift = max_rows * group <= 64 ? 4 : tile_waves(dim) == 8 ? 8 : 7;
+    p.shift = max_rows * group <= 64 ? 4 : kTileShift;
     const int64_t height = 1 << p.shift;
     const int64_t tiles = (max_rows * group + height - 1) / height;
     const int64_t loose = kv_tile_items(rows, seqs, group, p.shift);
