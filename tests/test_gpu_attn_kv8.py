@@ -121,6 +121,57 @@ def test_prompts(w, dim, rows):
     Case([0, 0, 1000], [rows, 77, rows // 2], 8, 2, dim, 16).check(w, max_rows=rows)
 
 
+def halves(w, c, max_rows):
+    """Whether the call takes the form that converts the cache first (by its workspace)."""
+    hq, hk, dim, page = c.sizes
+    blocks = c.table.shape[1]
+    need = w.attn_kv8_workspace_bytes(len(c.q), len(c.n), True, max_rows, blocks, hq, hk, dim, page)
+    return need >= len(c.n) * hk * ((blocks * page + 63) // 64) * 64 * dim * 4
+
+
+@pytest.mark.parametrize("dim", [32, 64, 96, 128, 160, 192, 224, 256])
+def test_long_prompts(w, dim):
+    """Many tiles over many tokens: from the cache converted once."""
+    print("CASE attn halves", dim, flush=True)
+    c = Case([8100, 0, 2500], [900, 1, 77], 32, 8, dim, [16, 32, 64, 128][dim // 32 % 4])
+    assert halves(w, c, 900) and not halves(w, Case([0], [200], 32, 8, dim, 16), 200)
+    c.check(w, max_rows=900)
+
+
+@pytest.mark.parametrize("kw", [dict(window=1000), dict(window=30), dict(causal=False),
+                                dict(causal=False, window=2000)])
+def test_long_prompts_seen_otherwise(w, kw):
+    c = Case([8100, 2500], [900, 77], 32, 8, 64, 16, seed=5)
+    assert halves(w, c, 900)
+    c.table[0, 7:9] = -1                                      # no pages
+    c.table[0, 200] = len(c.scales)
+    c.scales[c.table[0, 100:120], :, 1] *= np.float32(2.0 ** 12)
+    c.scales[c.table[0, 150], :, 1] = 0
+    c.check(w, max_rows=900, **kw)
+
+
+def test_long_prompts_by_graph(w):
+    """Captured, with other pages and lengths at each replay; the space between is reused."""
+    c = Case([8100, 2500], [900, 77], 32, 8, 64, 16, seed=6)
+    kvt, sc, t, lens, st = c.on_device()
+    need = w.attn_kv8_workspace_bytes(len(c.q), 2, True, 900, t.shape[1], 32, 8, 64, 16)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")     # halves are NaN
+    l, tt = lens.clone(), t.clone()
+    out, lse = torch.empty_like(c.q), torch.empty((len(c.q), 32), device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        w.attn_kv8(c.q, kvt, sc, tt, l, st, max_rows=900, out=out, lse=lse, workspace=ws)
+    for i in range(3):
+        l.copy_(lens - 450 * i)
+        tt[0, 5:50] = t[0, 5:50].flip(0) if i == 1 else t[0, 5:50]
+        graph.replay()
+        a = w.attn_kv8(c.q, kvt, sc, tt, l, st, max_rows=900, want_lse=True)
+        torch.cuda.synchronize()
+        assert torch.equal(out, a[0]) and torch.equal(lse, a[1])
+    c.lens = (lens - 900).cpu().numpy()
+    near(out, lse, *c.want(max_rows=900))
+
+
 def test_scales_far_apart(w):
     """Pages of values 2^40 apart, zero pages, the largest scale on a page of no weight."""
     c = Case([0, 200], [200, 3], 4, 1, 64, 16, seed=3, sharp=3.0)

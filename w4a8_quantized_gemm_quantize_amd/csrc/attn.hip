@@ -36,6 +36,9 @@ struct AttnArgs {
     const float *kv_scale;
     uint16_t *out;
     float *lse, *part;             // part: partial results of splits (null: none)
+    _Float16 *halves;              // the cache as halves (attn_halves_kernel; null: none)
+    f32x4 *halves_terms;
+    int runs;                      // of 64 tokens, that it has place for a sequence
     int64_t ldq, ldo;
     int heads, group, max_rows, causal, window;
     int splits, tiles;             // tiles: of a sequence, or 0 (items found by kv_find_seq)
@@ -378,8 +381,79 @@ constexpr int min_of(int a, int b) { return a < b ? a : b; }
 // x 128, 8 us more on short prompts, which have too few of them.)
 constexpr int tile_groups(int dim) { return dim <= 64 ? 3 : dim <= 128 ? 2 : 1; }
 constexpr int kTileShift = 7;                    // packed rows of a tile: 128
+constexpr int kWaitLoads = 0x0f70;               // s_waitcnt vmcnt(0)
 
+// A run of 64 tokens of a sequence and head as halves: keys, then values as they are in LDS.
+__device__ __forceinline__ int64_t halves_run(const AttnArgs &a, int s, int head, int run) {
+    return ((int64_t)s * a.heads + head) * a.runs + run;
+}
+// 16 bytes of keys, 4 of values of a record to their place in the run's image.
 template <int C, bool HALF>
+struct Halves {
+    static constexpr int kDim = 64 * C + (HALF ? 32 : 0), kSub = 16 * kDim;
+    static constexpr int kKeyPieces = 2 * C + HALF, kValuePieces = 4 * C + 2 * HALF;
+    u32x4 r[C ? C : 1];
+    u32x2 h;
+    __device__ __forceinline__ void load(const uint8_t *p, int lane) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) r[c] = *(const u32x4 *)(p + c * 1024 + lane * 16);
+        if constexpr (HALF) h = *(const u32x2 *)(p + C * 1024 + lane * 8);
+    }
+    // n: half a record; `to` the 16 tokens' keys
+    __device__ __forceinline__ void key(_Float16 *to, int lane, int n) const {
+        const int c = n >> 1, x = 2 * (n & 1);
+        *(half8_t *)(to + n * 512 + lane * 8) = n < 2 * C ? codes8h(r[c < C ? c : 0][x], r[c < C ? c : 0][x + 1])
+                                                          : codes8h(h.x, h.y);
+    }
+    static __device__ __forceinline__ int value_lane(int lane) {
+        return (lane >> 4 & 1) * 256 + (lane & 15) * 8 + (lane >> 5) * 4;
+    }
+    // n: 16 elements; `to` the 16 tokens' values and value_lane
+    __device__ __forceinline__ void value(_Float16 *to, int n) const {
+        uint32_t lo, hi;
+        codes4(n < 4 * C ? r[n < 4 * C ? n >> 2 : 0][n & 3] : h[n & 1], lo, hi);
+        *(u32x2 *)(to + (n >> 1) * 512 + (n & 1) * 128) = u32x2{lo, hi};
+    }
+};
+
+// The cache's tokens that the rows see as halves, once, where many tiles read each of them:
+// those then copy them straight to LDS.  Converting in every tile costs its wavefronts 77 of
+// 285 vector instructions a run, and the card, whose clock falls under this load, a fifth.
+template <int C, bool HALF>
+__global__ __launch_bounds__(256) void attn_halves_kernel(AttnArgs a) {
+    using H = Halves<C, HALF>;
+    const int head = blockIdx.x % a.heads;
+    const int64_t at = blockIdx.x / a.heads;
+    const int s = (int)(at / a.runs), run = (int)(at - (int64_t)s * a.runs);
+    const KvSeq q = kv_seq(a.b, s);
+    const int first = a.window ? max(0, q.len - q.n - a.window + 1) : 0;
+    if (q.n <= 0 || (int64_t)run * 64 >= q.len || run * 64 + 64 <= first) return;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int token = run * 64 + wave * 16;
+    const int page = token < q.len ? kv_page(a.b, s, token >> a.b.page_shift) : -1;
+    int64_t place = 0;                           // without a page the cache's first, weights 0
+    float sk = 0.0f, sv = -1.0f;
+    if (page >= 0) {
+        const int64_t ph = (int64_t)page * a.heads + head;
+        place = ((ph * 2 << a.b.page_shift) + (token & ((1 << a.b.page_shift) - 1))) * H::kDim;
+        sk = a.kv_scale[ph * 2];
+        sv = a.kv_scale[ph * 2 + 1];
+    }
+    H k, v;
+    k.load(a.kv + place, lane);
+    v.load(a.kv + place + ((int64_t)H::kDim << a.b.page_shift), lane);
+    const int64_t r = halves_run(a, s, head, run);
+    _Float16 *to = a.halves + r * (8 * H::kSub) + wave * H::kSub;
+#pragma unroll
+    for (int n = 0; n < H::kKeyPieces; ++n) k.key(to, lane, n);
+    to += 4 * H::kSub + H::value_lane(lane);
+#pragma unroll
+    for (int n = 0; n < H::kValuePieces; ++n) v.value(to, n);
+    if (lane == 0) a.halves_terms[r * 4 + wave] = page_terms(sk, sv);
+}
+
+// READY: from attn_halves_kernel's halves.
+template <int C, bool HALF, bool READY>
 __global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_tile_kernel(AttnArgs a) {
     constexpr int kDim = 64 * C + (HALF ? 32 : 0), kSteps = kDim / 16, kBlocks = kDim / 32;
     constexpr int kSub = 16 * kDim;              // halves of 16 tokens
@@ -466,43 +540,24 @@ __global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_til
         const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(at_in >> 32), j - j_in);
         return (int64_t)(((uint64_t)hi << 32) | lo);
     };
-    struct Raw {
-        u32x4 r[C ? C : 1];
-        u32x2 h;
-    };
-    Raw kraw, vraw;
+    using H = Halves<C, HALF>;
+    H kraw, vraw;
     f32x4 terms;
-    auto load = [&](int64_t at, Raw &x) {
-        const uint8_t *p = a.kv + at;
-#pragma unroll
-        for (int c = 0; c < C; ++c) x.r[c] = *(const u32x4 *)(p + c * 1024 + lane * 16);
-        if constexpr (HALF) x.h = *(const u32x2 *)(p + C * 1024 + lane * 8);
-    };
     auto lane_value = [](float v, int at) {
         return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), at));
     };
     const int64_t to_values = (int64_t)kDim << a.b.page_shift;
     auto load_keys = [&](int j) {
-        load(part_of(j), kraw);
+        kraw.load(a.kv + part_of(j), lane);
         terms = f32x4{lane_value(terms_in.x, j - j_in), lane_value(terms_in.y, j - j_in),
                       lane_value(terms_in.z, j - j_in), 0.0f};
     };
-    auto load_values = [&](int j) { load(part_of(j) + to_values, vraw); };
+    auto load_values = [&](int j) { vraw.load(a.kv + part_of(j) + to_values, lane); };
     // What was loaded, as halves, in pieces: keys, then values.
-    constexpr int kKeyPieces = 2 * C + HALF, kValuePieces = 4 * C + 2 * HALF;
-    auto store_key = [&](int j, int n) {         // n: half a record
-        _Float16 *to = kbuf[j & 1] + wave * kSub + n * 512 + lane * 8;
-        const int c = n >> 1, x = 2 * (n & 1);
-        *(half8_t *)to = n < 2 * C ? codes8h(kraw.r[c < C ? c : 0][x], kraw.r[c < C ? c : 0][x + 1])
-                                   : codes8h(kraw.h.x, kraw.h.y);
-    };
-    _Float16 *const value_lane = vbuf[0] + wave * kSub + (lane >> 4 & 1) * 256 + (lane & 15) * 8 +
-                                 (lane >> 5) * 4;
-    auto store_value = [&](int j, int n) {       // n: 16 elements
-        uint32_t lo, hi;
-        codes4(n < 4 * C ? vraw.r[n < 4 * C ? n >> 2 : 0][n & 3] : vraw.h[n & 1], lo, hi);
-        *(u32x2 *)(value_lane + (j & 1) * (4 * kSub) + (n >> 1) * 512 + (n & 1) * 128) = u32x2{lo, hi};
-    };
+    constexpr int kKeyPieces = H::kKeyPieces, kValuePieces = H::kValuePieces;
+    _Float16 *const value_lane = vbuf[0] + wave * kSub + H::value_lane(lane);
+    auto store_key = [&](int j, int n) { kraw.key(kbuf[j & 1] + wave * kSub, lane, n); };
+    auto store_value = [&](int j, int n) { vraw.value(value_lane + (j & 1) * (4 * kSub), n); };
     auto store_terms = [&](int j) { page[j & 3][wave] = terms; };
     auto store_keys = [&](int j) {
 #pragma unroll
@@ -512,6 +567,16 @@ __global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_til
     auto store_values = [&](int j) {
 #pragma unroll
         for (int n = 0; n < kValuePieces; ++n) store_value(j, n);
+    };
+    // The same from halves that are there: 16 bytes a lane straight to LDS (the wavefront
+    // waits for them before the barrier after the next half run).
+    auto copy = [&](int j, bool values) {
+        const int64_t r = halves_run(a, t.s, head, min(j, j1 - 1));
+        const _Float16 *from = a.halves + r * (8 * kSub) + (values ? 4 * kSub : 0) + wave * kSub;
+        _Float16 *to = (values ? vbuf[j & 1] : kbuf[j & 1]) + wave * kSub;
+#pragma unroll
+        for (int n = 0; n < kSub / 512; ++n) global_to_lds16(from + n * 512 + lane * 8, to + n * 512);
+        if (!values && wave == 0 && lane < 4) global_to_lds16(a.halves_terms + r * 4 + lane, &page[j & 3][0]);
     };
     const int sub_lane = (lane & 31) >> 4, rec = (h * 16 + (lane & 15)) * 8;
     auto key_operand = [&](int j, int half, int k) {
@@ -593,7 +658,7 @@ __global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_til
                     }
                 }
             }
-            if (half) {
+            if (half && !READY) {
                 // and its share of the next tokens' halves
                 constexpr int kPieces = kKeyPieces + kValuePieces;
 #pragma unroll
@@ -605,7 +670,7 @@ __global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_til
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        if (half) store_terms(j + 2);
+        if (half && !READY) store_terms(j + 2);
         const float most = fmaxf(sum[0], sum[1]);
         if (__any(!(most <= 0x1p14f))) {
             float best = -1e30f;
@@ -626,18 +691,25 @@ __global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_til
     f32x16 s0, s1;
     half8_t p0[2], p1[2];
     if (j0 < j1) {
-        look_up(j0);
-        load_keys(j0);
-        load_values(j0);
-        store_keys(j0);
-        store_values(j0);
         // what the first step multiplies by 0
         for (int x = lane; x < kSub / 8; x += 64)
             *(u32x4 *)(vbuf[(j0 + 1) & 1] + wave * kSub + x * 8) = u32x4{0, 0, 0, 0};
-        load_keys(j0 + 1);
-        load_values(j0 + 1);
-        store_keys(j0 + 1);
-        load_keys(j0 + 2);
+        if constexpr (READY) {
+            copy(j0, false);
+            copy(j0, true);
+            copy(j0 + 1, false);
+            __builtin_amdgcn_s_waitcnt(kWaitLoads);
+        } else {
+            look_up(j0);
+            load_keys(j0);
+            load_values(j0);
+            store_keys(j0);
+            store_values(j0);
+            load_keys(j0 + 1);
+            load_values(j0 + 1);
+            store_keys(j0 + 1);
+            load_keys(j0 + 2);
+        }
         __syncthreads();
 #pragma unroll
         for (int e = 0; e < 16; ++e) s0[e] = 0.0f;
@@ -650,12 +722,20 @@ __global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_til
     }
     for (int j = j0; j < j1; ++j) {
         step(j, 0, s0, s1, p1, p0);
+        if constexpr (READY) __builtin_amdgcn_s_waitcnt(kWaitLoads);
         __syncthreads();
+        if constexpr (READY) {
+            copy(j + 2, false);
+            copy(j + 1, true);
+        }
         step(j, 1, s1, s0, p0, p1);
-        load_values(j + 2);
-        if (j + 3 - j_in == 64) look_up(j + 3);
-        load_keys(j + 3);
+        if constexpr (!READY) {
+            load_values(j + 2);
+            if (j + 3 - j_in == 64) look_up(j + 3);
+            load_keys(j + 3);
+        }
     }
+    if constexpr (READY) __builtin_amdgcn_s_waitcnt(kWaitLoads);   // none outlives the wavefront
     if (j0 < j1) {
 #pragma unroll
         for (int x = 0; x < 2; ++x)
@@ -754,13 +834,22 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int dim, int
 template <int C, bool HALF>
 void launch_dim(const AttnArgs &a, int shift, hipStream_t stream) {
     const dim3 grid((uint32_t)(a.items * a.heads * a.splits));
-    if (shift == 4) attn_rows_kernel<C, HALF><<<grid, kWaves * 64, 0, stream>>>(a);
-    else attn_tile_kernel<C, HALF><<<grid, 256, 0, stream>>>(a);
+    if (shift == 4) {
+        attn_rows_kernel<C, HALF><<<grid, kWaves * 64, 0, stream>>>(a);
+    } else if (a.halves) {
+        attn_halves_kernel<C, HALF>
+            <<<dim3((uint32_t)((int64_t)a.b.seqs * a.runs * a.heads)), 256, 0, stream>>>(a);
+        attn_tile_kernel<C, HALF, true><<<grid, 256, 0, stream>>>(a);
+    } else {
+        attn_tile_kernel<C, HALF, false><<<grid, 256, 0, stream>>>(a);
+    }
 }
 
 struct Plan {
     int64_t items;
     int tiles, splits, shift;
+    int64_t runs;                  // of the cache as halves, a sequence; 0: none
+    size_t part_bytes, halves_bytes, terms_bytes;
 };
 // The kernel by the packed rows of a sequence: up to 64 go 16 a workgroup, that is, through
 // the cache up to four times, from the L2 after the first (32 x 4000 tokens, 8 heads of 128
@@ -774,10 +863,11 @@ struct Plan {
 // 5.5 ns a token (one sequence, 8 heads of 128: 8.0, 16.3 and 27.4 us for 500, 2000 and 4000
 // tokens), the join 3.5 us and 0.18 us a split (2000 tokens: 14.5, 12.2, 11.6, 12.3 and 15.5
 // us in 2, 4, 8, 16 and 32).
-Plan attn_plan(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows, int64_t max_tokens,
-               int q_heads, int kv_heads, int dim) {
+Plan attn_plan(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows, int64_t table_tokens,
+               int window, int q_heads, int kv_heads, int dim) {
     const int64_t group = q_heads / kv_heads;
     max_rows = !ragged ? 1 : max_rows < rows ? max_rows : rows;
+    int64_t max_tokens = table_tokens;
     Plan p;
     p.shift = max_rows * group <= 64 ? 4 : kTileShift;
     const int64_t height = 1 << p.shift;
@@ -785,6 +875,9 @@ Plan attn_plan(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows, int64_
     const int64_t loose = kv_tile_items(rows, seqs, group, p.shift);
     p.tiles = !ragged || seqs * tiles <= loose ? (int)tiles : 0;
     p.items = p.tiles ? seqs * tiles : loose;
+    // a tile sees its window and as many tokens more as it has rows
+    const int64_t seen = window + kv_min(max_rows, height / group + 2);
+    if (window && seen < max_tokens) max_tokens = seen;
     const int64_t work = p.items * kv_heads, most = (max_tokens + 127) / 128;
     const int64_t places = device_cu_count() * (p.shift == 4 ? 2 : tile_groups(dim));
     const double token = (p.shift == 4 ? 5.5e-3 : 3.0e-2) * dim / 128;
@@ -801,20 +894,32 @@ Plan attn_plan(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows, int64_
             p.splits = z;
         }
     }
+    p.part_bytes = p.splits > 1 ? ((size_t)work * p.splits << p.shift) * (dim + 4) * 4 : 0;
+    // The cache as halves: where at least eight tiles read a token and the call is long enough
+    // for the pass over the tokens (tiles x tokens x heads; 1.05 M: 66 us without, 70 with it,
+    // 1.3 M: 122 and 120, 3.1 M: 215 and 207, 3.4 M: 190 and 180, 20 M: 666 and 640), and the
+    // space for all tokens that the block tables could name is at most 1 GiB.
+    p.runs = (table_tokens + 63) / 64;
+    p.halves_bytes = (size_t)seqs * kv_heads * p.runs * 64 * dim * 4;
+    p.terms_bytes = (size_t)seqs * kv_heads * p.runs * 64;
+    const int64_t many = rows * group / height;
+    if (p.shift == 4 || many < 8 * seqs || (double)many * kv_heads * table_tokens < 2e6 ||
+        p.halves_bytes > (size_t)1 << 30 || seqs * kv_heads * p.runs >= (1 << 23))
+        p.runs = p.halves_bytes = p.terms_bytes = 0;
     return p;
 }
 
 }  // namespace
 
 size_t attn_workspace_bytes(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows,
-                            int64_t max_tokens, int q_heads, int kv_heads, int dim) {
-    const Plan p = attn_plan(rows, seqs, ragged, max_rows, max_tokens, q_heads, kv_heads, dim);
-    return p.splits > 1 ? ((size_t)p.items * kv_heads * p.splits << p.shift) * (dim + 4) * 4 : 0;
+                            int64_t table_tokens, int q_heads, int kv_heads, int dim) {
+    const Plan p = attn_plan(rows, seqs, ragged, max_rows, table_tokens, 0, q_heads, kv_heads, dim);
+    return p.part_bytes + p.halves_bytes + p.terms_bytes;
 }
 
-int64_t attn_grid(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows, int64_t max_tokens,
+int64_t attn_grid(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows, int64_t table_tokens,
                   int q_heads, int kv_heads, int dim) {
-    const Plan p = attn_plan(rows, seqs, ragged, max_rows, max_tokens, q_heads, kv_heads, dim);
+    const Plan p = attn_plan(rows, seqs, ragged, max_rows, table_tokens, 0, q_heads, kv_heads, dim);
     return p.items * kv_heads * (p.splits == 1 ? 1 : p.splits > 1 << p.shift ? p.splits : 1 << p.shift);
 }
 
@@ -822,8 +927,14 @@ hipError_t launch_attn(const KvCall &c, const uint16_t *q, int64_t ldq, const ui
                        const float *kv_scale, int64_t max_rows, int32_t q_heads, bool causal,
                        int32_t window, float scale, uint16_t *out, int64_t ldo, float *lse,
                        void *workspace, hipStream_t stream) {
-    const Plan p = attn_plan(c.rows, c.seqs, c.start != nullptr, max_rows,
-                             (int64_t)c.blocks * c.page, q_heads, c.kv_heads, c.dim);
+    const int64_t tokens = (int64_t)c.blocks * c.page;
+    Plan p = attn_plan(c.rows, c.seqs, c.start != nullptr, max_rows, tokens, 0, q_heads, c.kv_heads,
+                       c.dim);
+    if (window) {                                // the workspace knows no window: never more splits
+        const Plan w = attn_plan(c.rows, c.seqs, c.start != nullptr, max_rows, tokens, window, q_heads,
+                                 c.kv_heads, c.dim);
+        p.splits = w.splits < p.splits ? w.splits : p.splits;
+    }
     AttnArgs a;
     a.b = KvBatch{c.start, c.lens, c.table, c.ldb, c.seqs, c.blocks, c.pages, (int32_t)c.rows,
                   __builtin_ctz(c.page)};
@@ -833,6 +944,9 @@ hipError_t launch_attn(const KvCall &c, const uint16_t *q, int64_t ldq, const ui
     a.out = out;
     a.lse = lse;
     a.part = p.splits > 1 ? (float *)workspace : nullptr;
+    a.runs = (int)p.runs;
+    a.halves = p.runs ? (_Float16 *)((uint8_t *)workspace + p.part_bytes) : nullptr;
+    a.halves_terms = (f32x4 *)((uint8_t *)workspace + p.part_bytes + p.halves_bytes);
     a.ldq = ldq;
     a.ldo = ldo;
     a.heads = c.kv_heads;

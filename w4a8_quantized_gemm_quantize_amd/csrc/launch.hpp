@@ -156,8 +156,8 @@ hipError_t launch_kv8_write(const KvCall &c, const void *k, int64_t ldk, const v
 hipError_t launch_kv8_read(const KvCall &c, const uint8_t *kv, const float *scale, void *k,
                            int64_t ldk, void *v, int64_t ldv, bool bf16, hipStream_t stream);
 size_t attn_workspace_bytes(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows,
-                            int64_t max_tokens, int q_heads, int kv_heads, int dim);
-int64_t attn_grid(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows, int64_t max_tokens,
+                            int64_t table_tokens, int q_heads, int kv_heads, int dim);
+int64_t attn_grid(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows, int64_t table_tokens,
                   int q_heads, int kv_heads, int dim);
 hipError_t launch_attn(const KvCall &c, const uint16_t *q, int64_t ldq, const uint8_t *kv,
                        const float *kv_scale, int64_t max_rows, int32_t q_heads, bool causal,
