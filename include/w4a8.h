@@ -547,7 +547,7 @@ w4a8_status w4a8_lora_add(const uint16_t *x, int64_t ldx, const uint16_t *a, con
  * Common rules: head_dim a multiple of 32, kv_heads >= 1, blocks >= 0, ldb >= blocks,
  * ld at least a row and a multiple of 8 (bf16) or 4 (binary32) (W4A8_ERR_SHAPE);
  * head_dim <= 256, page 16, 32, 64 or 128, kv_heads <= 1024, rows, seqs and blocks * page
- * at most 2^30, pages below 2^31, and fewer than 2^24 workgroups (W4A8_ERR_UNSUPPORTED).
+ * at most 2^30, pages below 2^31, and fewer than 2^23 workgroups (W4A8_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------ */
 
 #define W4A8_KV_LAYOUT_V1 1

@@ -90,6 +90,18 @@ def test_single_tokens(w, hq, hk, lens):
     near(*b, *c.want())
 
 
+@pytest.mark.parametrize("dim", [32, 64, 96, 128, 160, 192, 224, 256])
+@pytest.mark.parametrize("hq,hk", [(8, 1), (16, 2), (14, 2), (5, 1)])
+@pytest.mark.parametrize("kw", [dict(), dict(window=20), dict(causal=False)])
+def test_few_rows(w, dim, hq, hk, kw):
+    """A few rows a sequence: 10 to 40 packed rows, one or two tiles of them."""
+    print("CASE attn few rows", dim, hq, hk, kw, flush=True)
+    c = Case([0, 100, 0, 33, 700], [5, 2, 1, 3, 5], hq, hk, dim, 16, seed=dim, sharp=2.0)
+    c.scales[c.table[4, :8], :, 1] *= np.float32(2.0 ** 10)
+    c.table[1, 2] = -1
+    c.check(w, max_rows=5, **kw)
+
+
 @pytest.mark.parametrize("window", [1, 2, 16, 33, 1000])
 @pytest.mark.parametrize("causal", [True, False])
 def test_windows(w, window, causal):

@@ -725,7 +725,7 @@ w4a8_status w4a8_kv8_write(const void *k, int64_t ldk, const void *v, int64_t ld
     if (st != W4A8_OK) return st;
     const bool bf16 = dtype == W4A8_BF16;
     if ((!bf16 && dtype != W4A8_F32) ||
-        w4a8::kv8_page_items(rows, seqs, row_start, page) * kv_heads >= kMaxGrid)
+        w4a8::kv8_page_items(rows, seqs, row_start, page) * kv_heads >= kMaxGrid / 2)
         return W4A8_ERR_UNSUPPORTED;
     if (!row_stride_ok(ldk, kv_heads, head_dim, bf16) ||
         !row_stride_ok(ldv, kv_heads, head_dim, bf16))
@@ -755,7 +755,7 @@ w4a8_status w4a8_kv8_read(const uint8_t *kv, const float *kv_scale, const int32_
     if (st != W4A8_OK) return st;
     const bool bf16 = dtype == W4A8_BF16;
     if ((!bf16 && dtype != W4A8_F32) ||
-        w4a8::kv8_page_items(rows, seqs, row_start, page) * kv_heads >= kMaxGrid)
+        w4a8::kv8_page_items(rows, seqs, row_start, page) * kv_heads >= kMaxGrid / 2)
         return W4A8_ERR_UNSUPPORTED;
     if (!row_stride_ok(ldk, kv_heads, head_dim, bf16) ||
         !row_stride_ok(ldv, kv_heads, head_dim, bf16))

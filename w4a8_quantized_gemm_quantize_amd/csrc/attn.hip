@@ -1,10 +1,10 @@
 // attn.hip -- attention of query rows over the paged 8-bit cache (w4a8_attn_kv8 in w4a8.h).
 //
 // The G = q_heads / kv_heads query heads of a cache head share its keys and values, so the
-// rows of a tile are (row i of the sequence, head g of the group), i G + g, 16 at a time:
-// the columns of the matrix products
+// rows of a tile are (row i of the sequence, head g of the group), i G + g: the columns of
+// the matrix products
 //   S [token][row] = K Q^T   and   O^T [element][row] += V^T P
-// with v_mfma_f32_16x16x32_f16.  K and V are bytes u = code + 128; the half 0x6400 | u is
+// with v_mfma_f32_16x16x32_f16 or _32x32x16_f16.  K and V are bytes u = code + 128; the half 0x6400 | u is
 // 1024 + u, so one byte permutation and one packed subtraction of 1152 make two exact
 // codes.  Q enters as halves too, each row scaled by a power of two that puts its largest
 // element just below 2^15: exact, but for elements under 2^-29 of that.  The products'
@@ -12,13 +12,16 @@
 //
 // Softmax in base 2 in one pass: with s_j = (scale log2 e) k_scale (q . k_j) of a token in a
 // page of value scale sv,
-//   t_j = s_j + log2 sv,   m >= max t_j - 8,   p_j = 2^(t_j - m)
-//   O = sum p_j codes_j,   l = sum p_j / sv,   out = O / l,   lse = ln 2 (m + log2 l)
-// so P needs no factor per page, is at most 2^8, and what its rounding to a half loses
-// (2^-11 of each p_j; below 2^-14 absolutely 2^-25) is measured against the largest product
-// p_j sv, not against p_j alone.  t, m, l and O are binary32.  m moves only when some t_j
-// exceeds it by more than 8, so most tiles rescale nothing.  Where a page's values are all 0
-// (sv = 0) any sv does: scales below 2^-100 count as that.
+//   t_j = s_j + log2 sv,   p_j = 2^(t_j - m),   O = sum p_j codes_j,   l = sum p_j / sv,
+//   out = O / l,   lse = ln 2 (m + log2 l)
+// so P needs no factor per page, and what its rounding to a half loses (2^-11 of a p_j, or
+// 2^-25 where it is below 2^-14) is measured against the largest product p_j sv, not against
+// p_j alone.  t, m, l and O are binary32.  m is no maximum but near one: it moves, to the
+// maximum less 4, only when some p_j come out so large that a lane's sum of them exceeds
+// 2^14, which a half still holds; so no maximum is taken while nothing overflows, and most
+// tiles rescale nothing.  Where a page's values are all 0 (sv = 0) any sv does: scales below
+// 2^-100 count as that; and a factor of scores below 1e-30 as 1e-30, so that hidden tokens'
+// -inf stays one where a page's keys are all 0.
 #include "device_common.hpp"
 #include "kv_index.hpp"
 #include "launch.hpp"
@@ -100,33 +103,42 @@ __device__ __forceinline__ f32x4 page_terms(float sk, float sv) {
 }
 
 constexpr int kWaves = 4;
+constexpr int kPairDim = 128;                    // 32 rows a wavefront up to here, by registers
 
-// A wavefront holds all 16 rows and takes every fourth run of 32 tokens of the workgroup's
+// ---- few rows: 16 MT packed rows a workgroup ----
+//
+// A wavefront holds all the rows and takes every fourth run of 32 tokens of the workgroup's
 // range; the four partial results are joined in LDS.  K and V go from memory straight to
-// the registers they are multiplied from, the next run's while this one is worked on.
-template <int C, bool HALF>                      // full chunks of 64 elements, and a half one
-__global__ __launch_bounds__(kWaves * 64, 64 * C + 32 * HALF <= 96 ? 4 : C == 2 && !HALF ? 3 : 2)
+// the registers they are multiplied from: the next run's keys as soon as this one's are
+// used, then its values.  Bound by HBM: 64 x 8192 tokens, 8 heads of 128, 180 us or 5.9
+// TB/s; with loads that also fill the L2 203 us, with both buffered twice (two wavefronts
+// on a SIMD for three) 288 us.
+template <int C, bool HALF, int MT>              // full chunks of 64 elements, and a half one
+__global__ __launch_bounds__(kWaves * 64, MT == 2 ? 2 : 64 * C + 32 * HALF <= 96 ? 4 : C == 2 && !HALF ? 3 : 2)
 void attn_rows_kernel(AttnArgs a) {
     constexpr int kDim = 64 * C + (HALF ? 32 : 0), kTiles = kDim / 16, kSteps = kDim / 32;
-    constexpr int kStride = kDim + 4;
-    __shared__ __attribute__((aligned(16))) float lds[kWaves * 16 * kStride];
-    __shared__ float lds_m[kWaves * 16], lds_l[kWaves * 16];
+    constexpr int kStride = kDim + 4, kRows = 16 * MT, kShift = MT == 2 ? 5 : 4;
+    __shared__ __attribute__((aligned(16))) float lds[kWaves * kRows * kStride];
+    __shared__ float lds_m[kWaves * kRows], lds_l[kWaves * kRows];
     const int split = blockIdx.x % a.splits;
     const int head = blockIdx.x / a.splits % a.heads;
     const int64_t item = blockIdx.x / a.splits / a.heads;
     KvTile t;
-    if (!find_tile(a, item, 4, t)) return;
+    if (!find_tile(a, item, kShift, t)) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int col = lane & 15, g = lane >> 4;
     const int from = t.seq.len - t.seq.n;
 
-    // this lane's row of Q, scaled
-    const int r = t.row0 + col;
-    const int i = r / a.group;
-    const bool live = col < t.rows;
-    half8_t q[kSteps];
-    float qfac;
-    {
+    // this lane's rows of Q, scaled, and the tokens they see, [see_lo, see_hi)
+    half8_t q[MT][kSteps];
+    float qfac[MT];
+    int see_hi[MT], see_lo[MT];
+#pragma unroll
+    for (int x = 0; x < MT; ++x) {
+        const int r = t.row0 + 16 * x + col, i = r / a.group, pos = from + i;
+        const bool live = 16 * x + col < t.rows;
+        see_hi[x] = a.causal ? min(t.hi, pos + 1) : t.hi;
+        see_lo[x] = a.window ? max(0, pos - a.window + 1) : 0;
         const uint16_t *p = a.q + (int64_t)(t.seq.first_row + i) * a.ldq +
                             (int64_t)(head * a.group + r - i * a.group) * kDim;
         u32x4 w[kSteps];
@@ -141,19 +153,16 @@ void attn_rows_kernel(AttnArgs a) {
         }
         top = max(top, (uint32_t)__shfl_xor((int)top, 16));
         top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-        const float up = row_scale(top, a.scale, qfac);
+        const float up = row_scale(top, a.scale, qfac[x]);
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
             float f[8];
             bf16x8_to_f32(w[k], f);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) q[k][x] = (_Float16)(f[x] * up);
+            for (int e = 0; e < 8; ++e) q[x][k][e] = (_Float16)(f[e] * up);
         }
     }
-    // tokens this row sees, [see_lo, see_hi), and those that every row sees
-    const int pos = from + i;
-    const int see_hi = a.causal ? min(t.hi, pos + 1) : t.hi;
-    const int see_lo = a.window ? max(0, pos - a.window + 1) : 0;
+    // tokens that every row sees
     const int all_hi = a.causal ? min(t.hi, from + t.row0 / a.group + 1) : t.hi;
     const int all_lo = a.window ? from + (t.row0 + t.rows - 1) / a.group - a.window + 1 : 0;
 
@@ -161,10 +170,15 @@ void attn_rows_kernel(AttnArgs a) {
     const int u0 = u_first + (int)((int64_t)u_all * split / a.splits) + wave;
     const int u1 = u_first + (int)((int64_t)u_all * (split + 1) / a.splits);
 
-    f32x4 o[kTiles];
+    f32x4 o[MT][kTiles];
+    float m[MT], l[MT];
 #pragma unroll
-    for (int d = 0; d < kTiles; ++d) o[d] = f32x4{0, 0, 0, 0};
-    float m = -1e30f, l = 0.0f;
+    for (int r = 0; r < MT; ++r) {
+#pragma unroll
+        for (int d = 0; d < kTiles; ++d) o[r][d] = f32x4{0, 0, 0, 0};
+        m[r] = -1e30f;
+        l[r] = 0.0f;
+    }
 
     // Lane x: of this wavefront's run n_in + x, for its two tiles of 16 tokens the place of
     // their keys and the page's terms, 64 runs at a time.  Without a page the place is the
@@ -231,72 +245,90 @@ void attn_rows_kernel(AttnArgs a) {
             inv_sv[h] = lane_value(terms_in[h].z, n - n_in);
         }
         // scores of two tiles of 16 tokens
-        f32x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        f32x4 s[MT][2];
+#pragma unroll
+        for (int r = 0; r < MT; ++r) s[r][0] = s[r][1] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    s[h] = mfma16(codes8h(x.k[h][c][2 * k], x.k[h][c][2 * k + 1]), q[2 * c + k], s[h]);
+                for (int h = 0; h < 2; ++h) {
+                    const half8_t key = codes8h(x.k[h][c][2 * k], x.k[h][c][2 * k + 1]);
+#pragma unroll
+                    for (int r = 0; r < MT; ++r) s[r][h] = mfma16(key, q[r][2 * c + k], s[r][h]);
+                }
         if constexpr (HALF) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) s[h] = mfma16(codes8h(x.kh[h].x, x.kh[h].y), q[2 * C], s[h]);
+            for (int h = 0; h < 2; ++h) {
+                const half8_t key = codes8h(x.kh[h].x, x.kh[h].y);
+#pragma unroll
+                for (int r = 0; r < MT; ++r) s[r][h] = mfma16(key, q[r][2 * C], s[r][h]);
+            }
         }
         if (n + 1 - n_in == 64) look_up(n + 1);
         load_keys(n + 1);
-        if (first + 32 > all_hi || first < all_lo) {
+        half8_t p[MT];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+        for (int r = 0; r < MT; ++r) {
+            if (first + 32 > all_hi || first < all_lo) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = first + h * 16 + 4 * g + e;
-                    if (j < see_lo || j >= see_hi) s[h][e] = -__builtin_inff();
-                }
-        }
-        float f[2], sum[2];
-        half8_t p;
-        auto weights = [&]() {
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                f[h] = fmaxf(qfac * sk[h], 1e-30f);
-                const float off = log_sv[h] - m;
-                sum[h] = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[h][e], f[h], off));
-                    sum[h] += w;
-                    p[4 * h + e] = (_Float16)w;
-                }
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = first + h * 16 + 4 * g + e;
+                        if (j < see_lo[r] || j >= see_hi[r]) s[r][h][e] = -__builtin_inff();
+                    }
             }
-        };
-        weights();
-        if (__any(!(fmaxf(sum[0], sum[1]) <= 0x1p14f))) {
-            float best = -1e30f;
+            float f[2], sum[2];
+            auto weights = [&]() {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < 2; ++h) {
+                    f[h] = fmaxf(qfac[r] * sk[h], 1e-30f);
+                    const float off = log_sv[h] - m[r];
+                    sum[h] = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    best = fmaxf(best, __builtin_fmaf(s[h][e], f[h], log_sv[h]));
-            const float top = fmaxf(m, quad_max(best) - 4.0f);
-            const float down = __builtin_amdgcn_exp2f(m - top);
-            m = top;
-            l *= down;
-#pragma unroll
-            for (int d = 0; d < kTiles; ++d) o[d] *= down;
+                    for (int e = 0; e < 4; ++e) {
+                        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][h][e], f[h], off));
+                        sum[h] += w;
+                        p[r][4 * h + e] = (_Float16)w;
+                    }
+                }
+            };
             weights();
-        }
+            if (__any(!(fmaxf(sum[0], sum[1]) <= 0x1p14f))) {
+                float best = -1e30f;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) l = __builtin_fmaf(sum[h], inv_sv[h], l);
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        best = fmaxf(best, __builtin_fmaf(s[r][h][e], f[h], log_sv[h]));
+                const float top = fmaxf(m[r], quad_max(best) - 4.0f);
+                const float down = __builtin_amdgcn_exp2f(m[r] - top);
+                m[r] = top;
+                l[r] *= down;
+#pragma unroll
+                for (int d = 0; d < kTiles; ++d) o[r][d] *= down;
+                weights();
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) l[r] = __builtin_fmaf(sum[h], inv_sv[h], l[r]);
+        }
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                o[4 * c + j] = mfma16(codes8h(x.v[0][c][j], x.v[1][c][j]), p, o[4 * c + j]);
+            for (int j = 0; j < 4; ++j) {
+                const half8_t value = codes8h(x.v[0][c][j], x.v[1][c][j]);
+#pragma unroll
+                for (int r = 0; r < MT; ++r) o[r][4 * c + j] = mfma16(value, p[r], o[r][4 * c + j]);
+            }
         if constexpr (HALF) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                o[4 * C + j] = mfma16(codes8h(x.vh[0][j], x.vh[1][j]), p, o[4 * C + j]);
+            for (int j = 0; j < 2; ++j) {
+                const half8_t value = codes8h(x.vh[0][j], x.vh[1][j]);
+#pragma unroll
+                for (int r = 0; r < MT; ++r) o[r][4 * C + j] = mfma16(value, p[r], o[r][4 * C + j]);
+            }
         }
         load_values(n + 1);
     };
@@ -308,54 +340,60 @@ void attn_rows_kernel(AttnArgs a) {
         load_values(0);
         for (int n = 0; n < runs; ++n) work(n);
     }
-    l = quad_sum(l);
 #pragma unroll
-    for (int d = 0; d < kTiles; ++d)
-        *(f32x4 *)(lds + (wave * 16 + col) * kStride + d * 16 + 4 * g) = o[d];
-    if (g == 0) {
-        lds_m[wave * 16 + col] = m;
-        lds_l[wave * 16 + col] = l;
+    for (int r = 0; r < MT; ++r) {
+        l[r] = quad_sum(l[r]);
+        const int row = wave * kRows + 16 * r + col;
+#pragma unroll
+        for (int d = 0; d < kTiles; ++d) *(f32x4 *)(lds + row * kStride + d * 16 + 4 * g) = o[r][d];
+        if (g == 0) {
+            lds_m[row] = m[r];
+            lds_l[row] = l[r];
+        }
     }
     __syncthreads();
     // 16 threads a row, 4 elements each at a time
-    const int row = threadIdx.x >> 4, at = (threadIdx.x & 15) * 4;
-    if (row >= t.rows) return;
-    float mm = lds_m[row];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) mm = fmaxf(mm, lds_m[w * 16 + row]);
-    float f[kWaves], ll = 0.0f;
+    for (int x16 = 0; x16 < MT; ++x16) {
+        const int row = 16 * x16 + (threadIdx.x >> 4), at = (threadIdx.x & 15) * 4;
+        if (row >= t.rows) return;
+        float mm = lds_m[row];
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        f[w] = __builtin_amdgcn_exp2f(lds_m[w * 16 + row] - mm);
-        ll = __builtin_fmaf(f[w], lds_l[w * 16 + row], ll);
-    }
-    const int rr = t.row0 + row, ri = rr / a.group, qh = head * a.group + rr - ri * a.group;
-    const int64_t orow = t.seq.first_row + ri;
-    const float by = a.part ? 1.0f : ll > 0.0f ? 1.0f / ll : 0.0f;
-    float *part = nullptr;
-    if (a.part) {
-        part = a.part + (((item * a.heads + head) * a.splits + split) * 16 + row) * (kDim + 4);
-        if (at == 0) {
-            part[kDim] = mm;
-            part[kDim + 1] = ll;
-        }
-    } else if (at == 0 && a.lse) {
-        a.lse[orow * a.heads * a.group + qh] =
-            ll > 0.0f ? kLn2 * (mm + __builtin_amdgcn_logf(ll)) : -__builtin_inff();
-    }
-    for (int d = at; d < kDim; d += 64) {
-        f32x4 sum = {0, 0, 0, 0};
+        for (int w = 1; w < kWaves; ++w) mm = fmaxf(mm, lds_m[w * kRows + row]);
+        float f[kWaves], ll = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            const f32x4 v = *(const f32x4 *)(lds + (w * 16 + row) * kStride + d);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(f[w], v[e], sum[e]);
+            f[w] = __builtin_amdgcn_exp2f(lds_m[w * kRows + row] - mm);
+            ll = __builtin_fmaf(f[w], lds_l[w * kRows + row], ll);
         }
+        const int rr = t.row0 + row, ri = rr / a.group, qh = head * a.group + rr - ri * a.group;
+        const int64_t orow = t.seq.first_row + ri;
+        const float by = ll > 0.0f ? 1.0f / ll : 0.0f;
+        float *part = nullptr;
         if (a.part) {
-            *(f32x4 *)(part + d) = sum;
-        } else {
-            *(u32x2 *)(a.out + orow * a.ldo + (int64_t)qh * kDim + d) =
-                u32x2{bf16x2_rne(sum[0] * by, sum[1] * by), bf16x2_rne(sum[2] * by, sum[3] * by)};
+            part = a.part + ((((item * a.heads + head) * a.splits + split) << kShift) + row) * (kDim + 4);
+            if (at == 0) {
+                part[kDim] = mm;
+                part[kDim + 1] = ll;
+            }
+        } else if (at == 0 && a.lse) {
+            a.lse[orow * a.heads * a.group + qh] =
+                ll > 0.0f ? kLn2 * (mm + __builtin_amdgcn_logf(ll)) : -__builtin_inff();
+        }
+        for (int d = at; d < kDim; d += 64) {
+            f32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                const f32x4 v = *(const f32x4 *)(lds + (w * kRows + row) * kStride + d);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(f[w], v[e], sum[e]);
+            }
+            if (a.part) {
+                *(f32x4 *)(part + d) = sum;
+            } else {
+                *(u32x2 *)(a.out + orow * a.ldo + (int64_t)qh * kDim + d) =
+                    u32x2{bf16x2_rne(sum[0] * by, sum[1] * by), bf16x2_rne(sum[2] * by, sum[3] * by)};
+            }
         }
     }
 }
@@ -835,7 +873,10 @@ template <int C, bool HALF>
 void launch_dim(const AttnArgs &a, int shift, hipStream_t stream) {
     const dim3 grid((uint32_t)(a.items * a.heads * a.splits));
     if (shift == 4) {
-        attn_rows_kernel<C, HALF><<<grid, kWaves * 64, 0, stream>>>(a);
+        attn_rows_kernel<C, HALF, 1><<<grid, kWaves * 64, 0, stream>>>(a);
+    } else if (shift == 5) {
+        if constexpr (64 * C + 32 * HALF <= kPairDim)
+            attn_rows_kernel<C, HALF, 2><<<grid, kWaves * 64, 0, stream>>>(a);
     } else if (a.halves) {
         attn_halves_kernel<C, HALF>
             <<<dim3((uint32_t)((int64_t)a.b.seqs * a.runs * a.heads)), 256, 0, stream>>>(a);
@@ -851,11 +892,12 @@ struct Plan {
     int64_t runs;                  // of the cache as halves, a sequence; 0: none
     size_t part_bytes, halves_bytes, terms_bytes;
 };
-// The kernel by the packed rows of a sequence: up to 64 go 16 a workgroup, that is, through
-// the cache up to four times, from the L2 after the first (32 x 4000 tokens, 8 heads of 128
-// with 32, 40, 64 and 80 rows: 67, 127, 132 and 200 us, where a 256-row tile takes 179, 181,
-// 183 and 185; 4 x 4000 tokens: 20, 23, 25 and 29 for 35, 36, 37 and 37).  Then over how many workgroups the tokens of a
-// tile are split: the least of a cost in microseconds,
+// The kernel by the packed rows of a sequence: up to 64 go 16 or 32 a workgroup, that is,
+// through the cache up to twice (four times past 128 elements a head), from the L2 after the
+// first time: 32 x 4000 tokens, 8 heads of 128 with 24, 40, 64 and 80 rows: 60, 79, 84 and
+// 165 us, 16 rows a workgroup 67, 127, 132 and 200, 128-row tiles 177, 181, 183 and 146.
+// Then over how many workgroups the tokens of a tile are split: the least of a cost in
+// microseconds,
 //   rounds of workgroups over the card x tokens each x what one takes a token
 //   + for more than one split its partial results and the second launch that joins them.
 // Few rows: two workgroups a compute unit draw all that memory gives (64 x 8192 tokens, 8
@@ -869,7 +911,8 @@ Plan attn_plan(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows, int64_
     max_rows = !ragged ? 1 : max_rows < rows ? max_rows : rows;
     int64_t max_tokens = table_tokens;
     Plan p;
-    p.shift = max_rows * group <= 64 ? 4 : kTileShift;
+    const int64_t packed = max_rows * group;
+    p.shift = packed > 64 ? kTileShift : packed > 16 && dim <= kPairDim ? 5 : 4;
     const int64_t height = 1 << p.shift;
     const int64_t tiles = (max_rows * group + height - 1) / height;
     const int64_t loose = kv_tile_items(rows, seqs, group, p.shift);
@@ -879,10 +922,10 @@ Plan attn_plan(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows, int64_
     const int64_t seen = window + kv_min(max_rows, height / group + 2);
     if (window && seen < max_tokens) max_tokens = seen;
     const int64_t work = p.items * kv_heads, most = (max_tokens + 127) / 128;
-    const int64_t places = device_cu_count() * (p.shift == 4 ? 2 : tile_groups(dim));
-    const double token = (p.shift == 4 ? 5.5e-3 : 3.0e-2) * dim / 128;
+    const int64_t places = device_cu_count() * (p.shift != kTileShift ? 2 : tile_groups(dim));
+    const double token = (p.shift != kTileShift ? 5.5e-3 : 3.0e-2) * dim / 128;
     // partial results are written and read at about 4 TB/s
-    const double join = p.shift == 4 ? 3.5 : 9.0;
+    const double join = p.shift != kTileShift ? 3.5 : 9.0;
     const double each = 0.18 + 2e-6 * (double)(work << p.shift) * (dim + 4);
     double best = 0;
     p.splits = 1;
@@ -903,7 +946,7 @@ Plan attn_plan(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows, int64_
     p.halves_bytes = (size_t)seqs * kv_heads * p.runs * 64 * dim * 4;
     p.terms_bytes = (size_t)seqs * kv_heads * p.runs * 64;
     const int64_t many = rows * group / height;
-    if (p.shift == 4 || many < 8 * seqs || (double)many * kv_heads * table_tokens < 2e6 ||
+    if (p.shift != kTileShift || many < 8 * seqs || (double)many * kv_heads * table_tokens < 2e6 ||
         p.halves_bytes > (size_t)1 << 30 || seqs * kv_heads * p.runs >= (1 << 23))
         p.runs = p.halves_bytes = p.terms_bytes = 0;
     return p;
