@@ -326,6 +326,7 @@ hipError_t launch_kv8_write(const KvCall &c, const void *k, int64_t ldk, const v
     const int64_t most = (mean < c.page ? mean : c.page) * c.dim / 8;
     if (most <= 64) launch_write<64, 1>(a, bf16, grid, lds, stream);
     else if (most <= 512) launch_write<256, 2>(a, bf16, grid, lds, stream);
+    else if (most <= 1024) launch_write<256, 4>(a, bf16, grid, lds, stream);
     else launch_write<512, 4>(a, bf16, grid, lds, stream);
     return hipGetLastError();
 }
