@@ -138,9 +138,16 @@ def attention(q, codes, scales, table, lens, starts, causal=True, window=0, scal
         block = torch.cat([blocks, torch.full((length // page + 1,), -1, device=dev)])[at // page]
         have = (block >= 0) & (block < pages)
         block = torch.where(have, block, 0)
+        p = length - n + torch.arange(m, device=dev)
+        see = have[None].expand(m, -1).clone()
+        if causal:
+            see &= at[None] <= p[:, None]
+        if window:
+            see &= at[None] > p[:, None] - window
         if pages:
             kv = codes[:, block, :, at % page].to(f8).permute(1, 2, 0, 3)    # 2, heads, tokens, dim
-            sc = torch.where(have[:, None, None], scales[block].to(f8), 0.0).permute(2, 1, 0)
+            # what no row sees may hold anything
+            sc = torch.where(see.any(0)[:, None, None], scales[block].to(f8), 0.0).permute(2, 1, 0)
             kv = kv * sc[..., None]
         else:
             kv = torch.zeros((2, heads, length, dim), dtype=f8, device=dev)
@@ -149,12 +156,6 @@ def attention(q, codes, scales, table, lens, starts, causal=True, window=0, scal
         x = x.reshape(heads, group * m, dim)
         score = torch.matmul(x, kv[0].transpose(1, 2)) * scale
         mass = torch.matmul(x.abs(), kv[0].abs().transpose(1, 2)) * abs(scale)
-        p = length - n + torch.arange(m, device=dev)
-        see = have[None].expand(m, -1).clone()
-        if causal:
-            see &= at[None] <= p[:, None]
-        if window:
-            see &= at[None] > p[:, None] - window
         see = see[None, None].expand(heads, group, m, length).reshape(heads, group * m, length)
         score = score.masked_fill(~see, float("-inf"))
         l = torch.logsumexp(score, 2) if length else \

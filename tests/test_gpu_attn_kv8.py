@@ -109,6 +109,18 @@ def test_windows(w, window, causal):
                                                                        causal=causal)
 
 
+@pytest.mark.parametrize("n", [1, 4, 60])
+def test_behind_the_window(w, n):
+    """Pages that slid out of the window may be gone or hold anything."""
+    c = Case([500, 330], [n, n], 4, 2, 64, 16, seed=n)
+    for s, length in enumerate(c.lens):
+        out = max(0, int(length) - n - 100 + 1) // 16           # wholly before every row's window
+        for b in range(out):
+            c.scales[c.table[s, b]] = [np.nan, np.inf, -np.inf, 0.0][b % 4]
+        c.table[s, 0:out:5] = -1
+    c.check(w, window=100, max_rows=n)
+
+
 def test_not_causal(w):
     Case([0, 90, 300], [70, 1, 33], 6, 2, 128, 16).check(w, causal=False)
 
@@ -335,6 +347,47 @@ def test_streams_workspaces_graphs(w):
         b = w.attn_kv8(q, kvt, sc, t, l2, window=100)
         torch.cuda.synchronize()
         assert torch.equal(out, a[0]) and torch.equal(lse, a[1]) and torch.equal(out2, b)
+
+
+def test_graphs_that_share_a_workspace(w):
+    """Two graphs, replayed in turn on one stream, with eager calls between them."""
+    c = Case([2500, 800], [2, 2], 8, 2, 128, 16, seed=3)
+    kvt, sc, t, lens, st = c.on_device()
+    need = w.attn_kv8_workspace_bytes(4, 2, True, 2, t.shape[1], 8, 2, 128, 16)
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    outs, graphs = [torch.empty_like(c.q) for _ in range(2)], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            w.attn_kv8(c.q, kvt, sc, t, lens, st, max_rows=2, window=700 * i, out=outs[i], workspace=ws)
+        graphs.append(g)
+    want = [w.attn_kv8(c.q, kvt, sc, t, lens, st, max_rows=2, window=700 * i) for i in range(2)]
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        graphs[0].replay()
+        graphs[1].replay()
+        eager = w.attn_kv8(c.q, kvt, sc, t, lens, st, max_rows=2, workspace=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+        assert torch.equal(eager, want[0])
+
+
+def test_two_streams_at_once(w):
+    c, d = Case([6000], [3], 8, 2, 128, 16, seed=4), Case([300], [200], 8, 2, 64, 32, seed=5)
+    want = c.run(w), d.run(w)
+    args = [(x.q, *x.on_device()) for x in (c, d)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i in range(2):
+            got[i].append(w.attn_kv8(*args[i], want_lse=True, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out, lse in got[i]:
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
 
 
 def test_empty(w):

@@ -95,9 +95,10 @@ __device__ __forceinline__ float row_scale(uint32_t top, float scale, float &fac
     return copysignf(__uint_as_float((uint32_t)(127 + e) << 23), scale);
 }
 // Of a page: key scale, log2 of the value scale, its inverse.  Without one (sv < 0) log2 is
-// -inf, so that every weight is 0.
+// -inf, so that every weight is 0; where the scale is no number either, so that what a
+// hidden token's page holds shows nowhere.
 __device__ __forceinline__ f32x4 page_terms(float sk, float sv) {
-    if (!(sv >= 0.0f)) return f32x4{0.0f, -__builtin_inff(), 0.0f, 0.0f};
+    if (!(sv >= 0.0f && sv <= 3.40282347e38f)) return f32x4{0.0f, -__builtin_inff(), 0.0f, 0.0f};
     sv = fmaxf(sv, 0x1p-100f);
     return f32x4{sk, __builtin_amdgcn_logf(sv), __builtin_amdgcn_rcpf(sv), 0.0f};
 }
