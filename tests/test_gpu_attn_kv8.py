@@ -140,6 +140,24 @@ def test_long(w, rows):
     c.check(w, max_rows=rows)
 
 
+@pytest.mark.parametrize("dim", [32, 64, 96, 128, 160, 192, 224, 256])
+@pytest.mark.parametrize("past,few", [(1200, True), (3000, False)])
+def test_tiles_in_parts(w, dim, past, few):
+    """Tiles over few and over many parts of the tokens, which two kernels join: a sequence
+    shorter than a part, one without rows, and one row that sees nothing."""
+    if dim == 32:
+        past *= 2                                             # parts of it are longer
+    print("CASE attn parts", dim, past, flush=True)
+    c = Case([past, 5, 40, 0], [33, 7, 0, 90], 8, 2, dim, 16, seed=dim)
+    c.lens[1] = 6                                             # seven rows, six tokens
+    need = w.attn_kv8_workspace_bytes(130, 4, True, 90, c.table.shape[1], 8, 2, dim, 16)
+    tiles = 130 * 4 // 128 + 4
+    parts = need // (tiles * 2 * 128 * (dim + 4) * 4)
+    assert 1 < parts <= 8 if few else parts > 8
+    out, lse = c.check(w, max_rows=90)
+    assert (lse[33] == float("-inf")).all() and (out[33] == 0).all()
+
+
 @pytest.mark.parametrize("dim,rows", [(64, 700), (128, 500), (256, 300), (96, 333)])
 def test_prompts(w, dim, rows):
     Case([0, 0, 1000], [rows, 77, rows // 2], 8, 2, dim, 16).check(w, max_rows=rows)

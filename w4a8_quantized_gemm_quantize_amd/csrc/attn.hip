@@ -870,6 +870,54 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int dim, int
         u32x2{bf16x2_rne(all[0] * by, all[1] * by), bf16x2_rne(all[2] * by, all[3] * by)};
 }
 
+// The same for few splits of tiles' many rows: 16 lanes a row and all its loads at once.  The
+// whole call with a wavefront a row and with this, 8 x 64 rows of 32 heads by 4 splits: 92 and
+// 85 us; 512 rows by 4: 65 and 60, by 8: 75.2 and 75.7, by 12: 91 and 99.  The join alone of
+// 500 rows of 28 heads of 64 by 6: 10.5 and 6.1 us.
+constexpr int kFewSplits = 8;
+__global__ __launch_bounds__(256) void attn_join_few_kernel(AttnArgs a, int dim, int shift) {
+    const int64_t at = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);    // item, head, row
+    const int row = (int)(at & ((1 << shift) - 1)), d0 = (threadIdx.x & 15) * 4;
+    // one item for the workgroup: tiles have 16 rows or more
+    const int64_t slot = (int64_t)blockIdx.x * 16 >> shift, item = slot / a.heads;
+    const int head = (int)(slot - item * a.heads);
+    KvTile t;
+    if (!find_tile(a, item, shift, t) || row >= t.rows) return;
+    const int64_t step = (int64_t)(dim + 4) << shift;
+    const float *p = a.part + slot * a.splits * step + row * (dim + 4);
+    float f[kFewSplits], l[kFewSplits], mm = -1e30f, ll = 0.0f;
+#pragma unroll
+    for (int z = 0; z < kFewSplits; ++z) {
+        f[z] = z < a.splits ? p[z * step + dim] : -1e30f;
+        l[z] = z < a.splits ? p[z * step + dim + 1] : 0.0f;
+    }
+#pragma unroll
+    for (int z = 0; z < kFewSplits; ++z) mm = fmaxf(mm, f[z]);
+#pragma unroll
+    for (int z = 0; z < kFewSplits; ++z) {
+        f[z] = __builtin_amdgcn_exp2f(f[z] - mm);
+        ll = __builtin_fmaf(f[z], l[z], ll);
+    }
+    const float by = ll > 0.0f ? 1.0f / ll : 0.0f;
+    const int rr = t.row0 + row, ri = rr / a.group, qh = head * a.group + rr - ri * a.group;
+    const int64_t orow = t.seq.first_row + ri;
+    if (d0 == 0 && a.lse)
+        a.lse[orow * a.heads * a.group + qh] =
+            ll > 0.0f ? kLn2 * (mm + __builtin_amdgcn_logf(ll)) : -__builtin_inff();
+    for (int d = d0; d < dim; d += 64) {
+        f32x4 v[kFewSplits], sum = {0, 0, 0, 0};
+#pragma unroll
+        for (int z = 0; z < kFewSplits; ++z)
+            v[z] = z < a.splits ? *(const f32x4 *)(p + z * step + d) : f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int z = 0; z < kFewSplits; ++z)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(f[z], v[z][e], sum[e]);
+        *(u32x2 *)(a.out + orow * a.ldo + (int64_t)qh * dim + d) =
+            u32x2{bf16x2_rne(sum[0] * by, sum[1] * by), bf16x2_rne(sum[2] * by, sum[3] * by)};
+    }
+}
+
 template <int C, bool HALF>
 void launch_dim(const AttnArgs &a, int shift, hipStream_t stream) {
     const dim3 grid((uint32_t)(a.items * a.heads * a.splits));
@@ -925,8 +973,9 @@ Plan attn_plan(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows, int64_
     const int64_t work = p.items * kv_heads, most = (max_tokens + 127) / 128;
     const int64_t places = device_cu_count() * (p.shift != kTileShift ? 2 : tile_groups(dim));
     const double token = (p.shift != kTileShift ? 5.5e-3 : 3.0e-2) * dim / 128;
-    // partial results are written and read at about 4 TB/s
-    const double join = p.shift != kTileShift ? 3.5 : 9.0;
+    // partial results are written and read at about 4 TB/s (tiles: 512 rows of 4 heads of 96 in
+    // 4 parts 14.2 us, unsplit 16.0; 256 rows 12.5 and 11.8)
+    const double join = p.shift != kTileShift ? 3.5 : 6.0;
     const double each = 0.18 + 2e-6 * (double)(work << p.shift) * (dim + 4);
     double best = 0;
     p.splits = 1;
@@ -1014,8 +1063,11 @@ hipError_t launch_attn(const KvCall &c, const uint16_t *q, int64_t ldq, const ui
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    const int64_t joins = (p.items * c.kv_heads << p.shift) / 4;
-    attn_join_kernel<<<dim3((uint32_t)joins), 256, 0, stream>>>(a, c.dim, p.shift);
+    const int64_t joins = p.items * c.kv_heads << p.shift;               // rows
+    if (p.splits <= kFewSplits && p.shift == kTileShift)
+        attn_join_few_kernel<<<dim3((uint32_t)(joins / 16)), 256, 0, stream>>>(a, c.dim, p.shift);
+    else
+        attn_join_kernel<<<dim3((uint32_t)(joins / 4)), 256, 0, stream>>>(a, c.dim, p.shift);
     return hipGetLastError();
 }
 
