@@ -591,8 +591,10 @@ w4a8_status w4a8_qk_norm_rope(const void *q, int64_t ldq, const void *k, int64_t
  *   new codes clamp(round_half_even(x * inv), -127, 127), inv = 1 / scale (0 where the
  *   scale is 0), each operation rounded to binary32.
  * A page's older tokens lose at most half a step of its scale each time that grows.
- * Tokens behind the last are left as they were.  A page must not be written for two
- * sequences in one call (a shared page that is not full is the caller's to copy).
+ * Tokens behind the last are left as they were.  A page must not be written twice in one
+ * call, for two sequences (a shared page that is not full is the caller's to copy) or for
+ * one whose table names it again.  k and v must be finite: an infinity makes the page's scale
+ * one, a NaN counts in no maximum and its code is not specified.
  */
 w4a8_status w4a8_kv8_write(const void *k, int64_t ldk, const void *v, int64_t ldv,
                            w4a8_dtype dtype, const int32_t *block_table, int64_t ldb,
@@ -637,7 +639,9 @@ size_t w4a8_attn_kv8_workspace_bytes(int64_t rows, int64_t seqs, int32_t ragged,
  * k_j and v_j are code * scale.  Products are exact and summed in binary32 (elements of q
  * below 2^-29 of their row's largest lose bits), exp(S_j) enters the sum over v_j rounded
  * to 11 bits, the statistics are binary32, and out is rounded once.  Value scales below
- * 2^-100 count as 2^-100.  The result does not depend on timing, but on the sizes of the
+ * 2^-100 count as 2^-100.  A row that sees a token of a page with a scale that is negative
+ * or no finite number gives NaN, out and lse; of pages it does not see they may be
+ * anything.  The result does not depend on timing, but on the sizes of the
  * batch, which set the order of the sums.
  * max_rows bounds a sequence's rows: of one with more only the first max_rows are
  * computed, the rest left as they were, like rows behind the last sequence.

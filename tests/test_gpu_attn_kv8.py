@@ -121,6 +121,47 @@ def test_behind_the_window(w, n):
     c.check(w, window=100, max_rows=n)
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -1.0])
+@pytest.mark.parametrize("part", [0, 1])
+@pytest.mark.parametrize("past,n", [(300, 1), (30000, 3), (300, 10), (300, 90), (6000, 90),
+                                    (8100, 900)])
+def test_scales_that_are_no_numbers(w, past, n, part, bad):
+    """Rows that see such a page say so, the others are as they were."""
+    print("CASE attn scales", past, n, part, bad, flush=True)
+    c = Case([past, 200], [n, n], 8, 2, 32, 16, seed=n)
+    if past == 8100:
+        c = Case([past, 200], [n, n], 32, 8, 32, 16, seed=n)
+        assert halves(w, c, n)
+    o, l, eo, el = c.want()
+    at = past + n // 2                                        # in the middle of the rows
+    c.scales[c.table[0, at // 16], 1, part] = bad
+    out, lse = c.run(w, max_rows=n)
+    hit = torch.zeros(lse.shape, dtype=torch.bool, device="cuda")
+    hit[max(0, at // 16 * 16 - past):n, 4:8] = True
+    assert hit.any() and torch.isnan(lse[hit]).all() and torch.isnan(out[hit]).all()
+    near(out[~hit], lse[~hit], o[~hit], l[~hit], eo[~hit], el[~hit])
+
+
+def test_queries_that_are_no_numbers(w):
+    """In their own rows only."""
+    c = Case([50, 400], [3, 90], 8, 2, 64, 16)
+    o, l, eo, el = c.want()
+    c.q[1, 2, 5] = c.q[40, 7, 63] = float("nan")
+    out, lse = c.run(w, max_rows=90)
+    hit = torch.zeros(lse.shape, dtype=torch.bool, device="cuda")
+    hit[1, 2] = hit[40, 7] = True
+    assert torch.isnan(lse[hit]).all() and torch.isnan(out[hit]).all()
+    near(out[~hit], lse[~hit], o[~hit], l[~hit], eo[~hit], el[~hit])
+
+
+def test_windows_that_32_bits_do_not_hold(w):
+    c = Case([50], [3], 8, 2, 64, 16)
+    for window in (-1, (1 << 30) + 1, (1 << 32) + 5, -(1 << 32) + 5):
+        with pytest.raises(w.W4A8Error):
+            c.run(w, window=window)
+    c.check(w, window=1 << 30)
+
+
 def test_not_causal(w):
     Case([0, 90, 300], [70, 1, 33], 6, 2, 128, 16).check(w, causal=False)
 
@@ -178,6 +219,16 @@ def test_long_prompts(w, dim):
     c = Case([8100, 0, 2500], [900, 1, 77], 32, 8, dim, [16, 32, 64, 128][dim // 32 % 4])
     assert halves(w, c, 900) and not halves(w, Case([0], [200], 32, 8, dim, 16), 200)
     c.check(w, max_rows=900)
+
+
+@pytest.mark.parametrize("kw", [dict(window=3000), dict(causal=False, window=4000)])
+def test_long_prompts_in_windows(w, kw):
+    """Windows of many tiles: the halves of what they see."""
+    c = Case([8100, 5], [1800, 77], 64, 16, 32, 16, seed=6)
+    assert halves(w, c, 1800)
+    # behind the window of every row: the first sees tokens from 8101 - window on
+    c.scales[c.table[0, :(8101 - kw["window"]) // 16]] = np.nan
+    c.check(w, max_rows=1800, **kw)
 
 
 @pytest.mark.parametrize("kw", [dict(window=1000), dict(window=30), dict(causal=False),

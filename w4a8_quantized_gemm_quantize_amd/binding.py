@@ -948,6 +948,8 @@ def attn_kv8_workspace_bytes(rows: int, seqs: int, ragged: bool, max_rows: int, 
                              q_heads: int, kv_heads: int, head_dim: int, page: int) -> int:
     """Workspace of attn_kv8 for `rows` query rows of `seqs` sequences (at most max_rows each,
     `ragged`: with row_start) whose block tables hold `blocks` pages; 0: none."""
+    if max(blocks, q_heads, kv_heads, head_dim, page) > 0x7fffffff:
+        return 0                             # refused
     return int(_lib.w4a8_attn_kv8_workspace_bytes(rows, seqs, 1 if ragged else 0, max_rows, blocks,
                                                   q_heads, kv_heads, head_dim, page))
 
@@ -985,6 +987,8 @@ def attn_kv8(q, kv, kv_scale, block_table, lens, row_start=None, max_rows=None,
             workspace = _workspace(stream, need, q.device)
     else:
         _flat(fn, workspace, torch.uint8, 0, "workspace", dev)
+    if not 0 <= window <= 1 << 30:           # refused, also where 32 bits would not hold it
+        window = -1 if window < 0 else 0x7fffffff
     status = _lib.w4a8_attn_kv8(
         q.data_ptr(), ldq, kv.data_ptr(), kv_scale.data_ptr(), block_table.data_ptr(), ldb, blocks,
         lens.data_ptr(), _addr(row_start), seqs, rows, max_rows, q_heads, kv_heads, dim, page, pages,

@@ -94,13 +94,22 @@ __device__ __forceinline__ float row_scale(uint32_t top, float scale, float &fac
     fac = fabsf(scale) * __uint_as_float((uint32_t)(127 - e) << 23);
     return copysignf(__uint_as_float((uint32_t)(127 + e) << 23), scale);
 }
-// Of a page: key scale, log2 of the value scale, its inverse.  Without one (sv < 0) log2 is
-// -inf, so that every weight is 0; where the scale is no number either, so that what a
-// hidden token's page holds shows nowhere.
-__device__ __forceinline__ f32x4 page_terms(float sk, float sv) {
-    if (!(sv >= 0.0f && sv <= 3.40282347e38f)) return f32x4{0.0f, -__builtin_inff(), 0.0f, 0.0f};
+// Of a page: key scale, log2 of the value scale, its inverse.  Without one log2 is -inf, so
+// that every weight is 0.  A scale that is negative or no finite number must show in the rows
+// that see the page and in no other, so it takes neither a product nor an infinity, which
+// hidden tokens' -inf would turn into NaN, but a log2 that no weights have: m rises to it.
+constexpr float kBadScale = 3e38f;
+__device__ __forceinline__ f32x4 page_terms(bool have, float sk, float sv) {
+    if (!have) return f32x4{0.0f, -__builtin_inff(), 0.0f, 0.0f};
+    if (!(fminf(sk, sv) >= 0.0f && sk + sv < __builtin_inff())) return f32x4{0.0f, kBadScale, 0.0f, 0.0f};
     sv = fmaxf(sv, 0x1p-100f);
     return f32x4{sk, __builtin_amdgcn_logf(sv), __builtin_amdgcn_rcpf(sv), 0.0f};
+}
+// What a row's sum of products is multiplied by, and its lse.
+__device__ __forceinline__ float row_end(float m, float l, float &lse) {
+    if (m >= 1e38f) l = __builtin_nanf("");
+    lse = l == 0.0f ? -__builtin_inff() : kLn2 * (m + __builtin_amdgcn_logf(l));
+    return l == 0.0f ? 0.0f : 1.0f / l;
 }
 
 constexpr int kWaves = 4;
@@ -195,14 +204,14 @@ void attn_rows_kernel(AttnArgs a) {
             const int64_t at = u * 32 + h * 16;
             const int page = u < u1 && at < t.hi ? kv_page(a.b, t.s, at >> a.b.page_shift) : -1;
             at_in[h] = 0;
-            float sk = 0.0f, sv = -1.0f;
+            float sk = 0.0f, sv = 0.0f;
             if (page >= 0) {
                 const int64_t ph = (int64_t)page * a.heads + head;
                 at_in[h] = ((ph * 2 << a.b.page_shift) + (at & ((1 << a.b.page_shift) - 1))) * kDim;
                 sk = a.kv_scale[ph * 2];
                 sv = a.kv_scale[ph * 2 + 1];
             }
-            terms_in[h] = page_terms(sk, sv);
+            terms_in[h] = page_terms(page >= 0, sk, sv);
         }
     };
     const int64_t to_values = (int64_t)kDim << a.b.page_shift;
@@ -369,8 +378,8 @@ void attn_rows_kernel(AttnArgs a) {
         }
         const int rr = t.row0 + row, ri = rr / a.group, qh = head * a.group + rr - ri * a.group;
         const int64_t orow = t.seq.first_row + ri;
-        const float by = ll > 0.0f ? 1.0f / ll : 0.0f;
-        float *part = nullptr;
+        float lse, *part = nullptr;
+        const float by = row_end(mm, ll, lse);
         if (a.part) {
             part = a.part + ((((item * a.heads + head) * a.splits + split) << kShift) + row) * (kDim + 4);
             if (at == 0) {
@@ -378,8 +387,7 @@ void attn_rows_kernel(AttnArgs a) {
                 part[kDim + 1] = ll;
             }
         } else if (at == 0 && a.lse) {
-            a.lse[orow * a.heads * a.group + qh] =
-                ll > 0.0f ? kLn2 * (mm + __builtin_amdgcn_logf(ll)) : -__builtin_inff();
+            a.lse[orow * a.heads * a.group + qh] = lse;
         }
         for (int d = at; d < kDim; d += 64) {
             f32x4 sum = {0, 0, 0, 0};
@@ -471,7 +479,7 @@ __global__ __launch_bounds__(256) void attn_halves_kernel(AttnArgs a) {
     const int token = run * 64 + wave * 16;
     const int page = token < q.len ? kv_page(a.b, s, token >> a.b.page_shift) : -1;
     int64_t place = 0;                           // without a page the cache's first, weights 0
-    float sk = 0.0f, sv = -1.0f;
+    float sk = 0.0f, sv = 0.0f;
     if (page >= 0) {
         const int64_t ph = (int64_t)page * a.heads + head;
         place = ((ph * 2 << a.b.page_shift) + (token & ((1 << a.b.page_shift) - 1))) * H::kDim;
@@ -488,7 +496,7 @@ __global__ __launch_bounds__(256) void attn_halves_kernel(AttnArgs a) {
     to += 4 * H::kSub + H::value_lane(lane);
 #pragma unroll
     for (int n = 0; n < H::kValuePieces; ++n) v.value(to, n);
-    if (lane == 0) a.halves_terms[r * 4 + wave] = page_terms(sk, sv);
+    if (lane == 0) a.halves_terms[r * 4 + wave] = page_terms(page >= 0, sk, sv);
 }
 
 // READY: from attn_halves_kernel's halves.
@@ -565,14 +573,14 @@ __global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_til
         const int64_t at = (int64_t)(j + lane) * 64 + wave * 16;
         const int pg = j + lane < j1 && at < t.hi ? kv_page(a.b, t.s, at >> a.b.page_shift) : -1;
         at_in = 0;
-        float sk = 0.0f, sv = -1.0f;
+        float sk = 0.0f, sv = 0.0f;
         if (pg >= 0) {
             const int64_t ph = (int64_t)pg * a.heads + head;
             at_in = ((ph * 2 << a.b.page_shift) + (at & ((1 << a.b.page_shift) - 1))) * kDim;
             sk = a.kv_scale[ph * 2];
             sv = a.kv_scale[ph * 2 + 1];
         }
-        terms_in = page_terms(sk, sv);
+        terms_in = page_terms(pg >= 0, sk, sv);
     };
     auto part_of = [&](int j) -> int64_t {
         const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)at_in, j - j_in);
@@ -800,11 +808,10 @@ __global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_til
                     f32x4{o[d][4 * x], o[d][4 * x + 1], o[d][4 * x + 2], o[d][4 * x + 3]};
         return;
     }
-    if (live && h == 0 && a.lse)
-        a.lse[orow * a.heads * a.group + qh] =
-            l > 0.0f ? kLn2 * (m + __builtin_amdgcn_logf(l)) : -__builtin_inff();
-    const float by = l > 0.0f ? 1.0f / l : 0.0f;
     if (!live) return;
+    float lse;
+    const float by = row_end(m, l, lse);
+    if (h == 0 && a.lse) a.lse[orow * a.heads * a.group + qh] = lse;
     uint16_t *out = a.out + orow * a.ldo + (int64_t)qh * kDim;
 #pragma unroll
     for (int d = 0; d < kBlocks; ++d)
@@ -844,9 +851,9 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int dim, int
     for (int x = 1; x < 64; x <<= 1) ll += __shfl_xor(ll, x);
     const int rr = t.row0 + row, ri = rr / a.group, qh = head * a.group + rr - ri * a.group;
     const int64_t orow = t.seq.first_row + ri;
-    if (lane == 0 && a.lse)
-        a.lse[orow * a.heads * a.group + qh] =
-            ll > 0.0f ? kLn2 * (mm + __builtin_amdgcn_logf(ll)) : -__builtin_inff();
+    float lse;
+    const float by = row_end(mm, ll, lse);
+    if (lane == 0 && a.lse) a.lse[orow * a.heads * a.group + qh] = lse;
     const int cols = dim >> 2, groups = 64 / cols, g = lane / cols, d = (lane - g * cols) * 4;
     f32x4 sum = {0, 0, 0, 0};
     for (int z0 = 0; z0 < a.splits; z0 += groups) {
@@ -865,7 +872,6 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int dim, int
 #pragma unroll
         for (int e = 0; e < 4; ++e) all[e] += __shfl(sum[e], (lane + x * cols) & 63);
     if (g > 0) return;
-    const float by = ll > 0.0f ? 1.0f / ll : 0.0f;
     *(u32x2 *)(a.out + orow * a.ldo + (int64_t)qh * dim + d) =
         u32x2{bf16x2_rne(all[0] * by, all[1] * by), bf16x2_rne(all[2] * by, all[3] * by)};
 }
@@ -898,12 +904,11 @@ __global__ __launch_bounds__(256) void attn_join_few_kernel(AttnArgs a, int dim,
         f[z] = __builtin_amdgcn_exp2f(f[z] - mm);
         ll = __builtin_fmaf(f[z], l[z], ll);
     }
-    const float by = ll > 0.0f ? 1.0f / ll : 0.0f;
+    float lse;
+    const float by = row_end(mm, ll, lse);
     const int rr = t.row0 + row, ri = rr / a.group, qh = head * a.group + rr - ri * a.group;
     const int64_t orow = t.seq.first_row + ri;
-    if (d0 == 0 && a.lse)
-        a.lse[orow * a.heads * a.group + qh] =
-            ll > 0.0f ? kLn2 * (mm + __builtin_amdgcn_logf(ll)) : -__builtin_inff();
+    if (d0 == 0 && a.lse) a.lse[orow * a.heads * a.group + qh] = lse;
     for (int d = d0; d < dim; d += 64) {
         f32x4 v[kFewSplits], sum = {0, 0, 0, 0};
 #pragma unroll
@@ -995,8 +1000,12 @@ Plan attn_plan(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows, int64_
     p.runs = (table_tokens + 63) / 64;
     p.halves_bytes = (size_t)seqs * kv_heads * p.runs * 64 * dim * 4;
     p.terms_bytes = (size_t)seqs * kv_heads * p.runs * 64;
+    // Of a windowed call a tile sees max_tokens, and a token is seen by so many tiles (5124 and
+    // 3067 rows of 64 x 128, window 30: 137 us with it, 131 without, 128: 156 and 146; 500 rows
+    // of 28 x 64, 512: 19.4 and 18.1; 5124 and 3067 again, 1024: 346 and 345).
     const int64_t many = rows * group / height;
-    if (p.shift != kTileShift || many < 8 * seqs || (double)many * kv_heads * table_tokens < 2e6 ||
+    const int64_t readers = window ? kv_min(many, seqs * (window * group / height + 1)) : many;
+    if (p.shift != kTileShift || readers < 8 * seqs || (double)many * kv_heads * max_tokens < 2e6 ||
         p.halves_bytes > (size_t)1 << 30 || seqs * kv_heads * p.runs >= (1 << 23))
         p.runs = p.halves_bytes = p.terms_bytes = 0;
     return p;
@@ -1023,10 +1032,11 @@ hipError_t launch_attn(const KvCall &c, const uint16_t *q, int64_t ldq, const ui
     const int64_t tokens = (int64_t)c.blocks * c.page;
     Plan p = attn_plan(c.rows, c.seqs, c.start != nullptr, max_rows, tokens, 0, q_heads, c.kv_heads,
                        c.dim);
-    if (window) {                                // the workspace knows no window: never more splits
+    if (window) {                                // the workspace knows no window: never more of it
         const Plan w = attn_plan(c.rows, c.seqs, c.start != nullptr, max_rows, tokens, window, q_heads,
                                  c.kv_heads, c.dim);
         p.splits = w.splits < p.splits ? w.splits : p.splits;
+        p.runs = w.runs < p.runs ? w.runs : p.runs;
     }
     AttnArgs a;
     a.b = KvBatch{c.start, c.lens, c.table, c.ldb, c.seqs, c.blocks, c.pages, (int32_t)c.rows,
