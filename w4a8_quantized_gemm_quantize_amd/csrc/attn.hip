@@ -473,8 +473,7 @@ __global__ __launch_bounds__(256) void attn_halves_kernel(AttnArgs a) {
     const int64_t at = blockIdx.x / a.heads;
     const int s = (int)(at / a.runs), run = (int)(at - (int64_t)s * a.runs);
     const KvSeq q = kv_seq(a.b, s);
-    const int first = a.window ? max(0, q.len - q.n - a.window + 1) : 0;
-    if (q.n <= 0 || (int64_t)run * 64 >= q.len || run * 64 + 64 <= first) return;
+    if (!kv_run_seen(a.b, q, run, a.window)) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int token = run * 64 + wave * 16;
     const int page = token < q.len ? kv_page(a.b, s, token >> a.b.page_shift) : -1;

@@ -178,4 +178,11 @@ KV_INLINE bool kv_tile(const KvBatch &b, int64_t item, int tiles, int group, int
     return true;
 }
 
+// Whether rows of sequence q see any of the 64 tokens from `run` * 64 on, so that bytes may be
+// read for them: without a page not even the cache's first is there.
+KV_INLINE bool kv_run_seen(const KvBatch &b, const KvSeq &q, int run, int window) {
+    const int64_t first = window ? (int64_t)q.len - q.n - window + 1 : 0, at = (int64_t)run * 64;
+    return b.pages > 0 && q.n > 0 && at < q.len && at + 64 > first;
+}
+
 }  // namespace w4a8
