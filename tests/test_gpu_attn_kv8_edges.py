@@ -1,6 +1,8 @@
 """Attention over the 8-bit cache at the edges of what its entry point takes: caches without a
-page in every form."""
+page in every form, value scales of any size."""
+import numpy as np
 import pytest
+import torch
 
 from test_gpu_attn_kv8 import Case, halves, w  # noqa: F401
 
@@ -19,3 +21,59 @@ def test_no_pages(w, n):
     for kw in (dict(), dict(causal=False), dict(window=3000)):
         out, lse = w.attn_kv8(c.q, none, nsc, t, lens, st, max_rows=n, want_lse=True, **kw)
         assert (out == 0).all() and (lse == float("-inf")).all()
+
+
+# forms: few rows in one part, in parts and joined, 32 rows a wavefront, tiles, tiles in few and
+# in many parts, tiles over the cache converted first
+FORMS = [([40, 3], [1, 1], 4, 1), ([9000, 3], [1, 1], 4, 1), ([200, 3], [5, 3], 8, 2),
+         ([200, 3], [40, 1], 8, 2), ([1200, 5], [33, 7], 8, 2), ([9000, 5], [33, 7], 8, 2),
+         ([8100, 40], [900, 77], 32, 8)]
+
+
+def spread(c, rows_of_pages):
+    """Value scales of the used pages, times what each sequence's pages are given in turn."""
+    for s in range(len(c.lens)):
+        used = c.table[s][c.table[s] >= 0]
+        for i, f in enumerate(rows_of_pages):
+            at = used[i::len(rows_of_pages)]
+            c.scales[at, :, 1] = (c.scales[at, :, 1].astype(np.float64) * f).astype(np.float32)
+
+
+@pytest.mark.parametrize("past,n,hq,hk", FORMS)
+@pytest.mark.parametrize("scales", [(0.0, 2.0 ** 45), (2.0 ** 45, 0.0), (2.0 ** -60, 2.0 ** 60, 1.0),
+                                    (2.0 ** 120, 2.0 ** -120, 0.0), (2.0 ** -130, 1.0),
+                                    (2.0 ** 120,), (2.0 ** -125,), (0.0,), (1.0, 1.0, 0.0)])
+def test_value_scales_of_any_size(w, past, n, hq, hk, scales):
+    """A token weighs the same in the softmax's sum whatever its page's value scale is: pages
+    of zeros, scales far apart, at both ends of what binary32 holds."""
+    print("CASE attn value scales", past, n, hq, hk, scales, flush=True)
+    c = Case(past, n, hq, hk, 32 if n[0] == 900 else 64, 16, seed=len(scales))
+    if n[0] == 900:
+        assert halves(w, c, 900)
+    spread(c, scales)
+    used = c.table[c.table >= 0]
+    assert np.isfinite(c.scales[used]).all()
+    for kw in (dict(), dict(window=70)) if n[0] < 100 else (dict(),):
+        out, lse = c.check(w, max_rows=max(n), **kw)
+        assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+
+
+def test_equal_scores_beside_zeros(w):
+    """Sixteen tokens of zeros and sixteen ones at equal scores: half of one's value, ln 32."""
+    c = Case([31], [1], 4, 1, 64, 16)
+    c.q.zero_()
+    c.codes[1] = 1
+    for big in (2.0 ** 29, 2.0 ** 40, 2.0 ** 127):
+        c.scales[c.table[0, :2], 0, 1] = 0.0, big
+        out, lse = c.run(w)
+        assert torch.equal(out, torch.full_like(out, big / 2))
+        assert (lse - np.log(32)).abs().max() < 1e-6
+
+
+def test_many_tokens_of_zeros(w):
+    """Enough of them that their number times a factor for their scale would leave binary32."""
+    c = Case([150000, 7], [1, 1], 1, 1, 32, 128)
+    c.q.zero_()
+    c.scales[c.table[0], :, 1] = 0.0
+    out, lse = c.run(w)
+    assert (out[0] == 0).all() and abs(lse[0, 0].item() - np.log(150001)) < 1e-5

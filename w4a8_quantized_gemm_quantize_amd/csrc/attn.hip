@@ -19,9 +19,18 @@
 // p_j alone.  t, m, l and O are binary32.  m is no maximum but near one: it moves, to the
 // maximum less 4, only when some p_j come out so large that a lane's sum of them exceeds
 // 2^14, which a half still holds; so no maximum is taken while nothing overflows, and most
-// tiles rescale nothing.  Where a page's values are all 0 (sv = 0) any sv does: scales below
-// 2^-100 count as that; and a factor of scores below 1e-30 as 1e-30, so that hidden tokens'
-// -inf stays one where a page's keys are all 0.
+// tiles rescale nothing.  A factor of scores below 1e-30 counts as 1e-30, so that hidden
+// tokens' -inf stays one where a page's keys are all 0.
+//
+// Taking l from the p_j holds while scales lie between 2^-40 and 2^20: then p_j counts in l
+// only from 2^-110 on, where exp2 still has it, and l stays in 2^-16 .. 2^84 (2^30 tokens).
+// From the first page on that a row of the wavefront sees and whose scale lies outside, zero
+// among them, the wavefront takes l's weights by themselves, against a reference of their own:
+//   l = sum 2^(s_j - ml),   out = O 2^(m - ml) / l,   lse = ln 2 (ml + log2 l),
+// with ml = m before.  Such a page has a log2 sv that makes any weight overflow, so that it is
+// found without a test per page, and from there on every sum of weights counts as too large.
+// (Values of 1e-10 to 1e8 never get there, and pay nothing up to 128 elements a head; prompts
+// of 3000 rows, 32 heads of 192 and 256: 102 -> 105 and 135 -> 140 us, by registers.)
 #include "device_common.hpp"
 #include "kv_index.hpp"
 #include "launch.hpp"
@@ -95,23 +104,37 @@ __device__ __forceinline__ float row_scale(uint32_t top, float scale, float &fac
     return copysignf(__uint_as_float((uint32_t)(127 + e) << 23), scale);
 }
 // Of a page: key scale, log2 of the value scale, its inverse.  Without one log2 is -inf, so
-// that every weight is 0.  A scale that is negative or no finite number must show in the rows
-// that see the page and in no other, so it takes neither a product nor an infinity, which
-// hidden tokens' -inf would turn into NaN, but a log2 that no weights have: m rises to it.
-constexpr float kBadScale = 3e38f;
+// that every weight is 0.  For scales that l cannot be taken from p by (see above) log2 is
+// kOdd, and the third term what it really is (finite, as weights of 0 are multiplied by it
+// where the page is hidden; a scale of 0 has one that no weight survives).  A scale that is
+// negative or no finite number must show in the rows that see the page and in no other, so it
+// takes neither a product nor an infinity, which hidden tokens' -inf would turn into NaN, but
+// a log2 that no weights have: m rises to it.
+constexpr float kOdd = 3e38f, kBadScale = 3e38f;
 __device__ __forceinline__ f32x4 page_terms(bool have, float sk, float sv) {
     if (!have) return f32x4{0.0f, -__builtin_inff(), 0.0f, 0.0f};
-    if (!(fminf(sk, sv) >= 0.0f && sk + sv < __builtin_inff())) return f32x4{0.0f, kBadScale, 0.0f, 0.0f};
-    sv = fmaxf(sv, 0x1p-100f);
-    return f32x4{sk, __builtin_amdgcn_logf(sv), __builtin_amdgcn_rcpf(sv), 0.0f};
+    if (!(fminf(sk, sv) >= 0.0f && sk < __builtin_inff() && sv < __builtin_inff()))
+        return f32x4{0.0f, kOdd, kBadScale, 0.0f};
+    if (sv >= 0x1p-40f && sv <= 0x1p20f)
+        return f32x4{sk, __builtin_amdgcn_logf(sv), __builtin_amdgcn_rcpf(sv), 0.0f};
+    // the instruction takes subnormal numbers for 0
+    const float log_sv = sv < 1.0f ? __builtin_amdgcn_logf(sv * 0x1p32f) - 32.0f : __builtin_amdgcn_logf(sv);
+    return f32x4{sk, kOdd, fmaxf(log_sv, -kOdd), 0.0f};
 }
-// What a row's sum of products is multiplied by, and its lse.
-__device__ __forceinline__ float row_end(float m, float l, float &lse) {
+// A row's results from its statistics: x times the factors by and up, which together may be
+// out of binary32's range, and its lse.
+struct RowEnd {
+    float by, up, lse;
+    __device__ __forceinline__ float operator()(float x) const { return x * by * up; }
+};
+__device__ __forceinline__ RowEnd row_end(float m, float ml, float l) {
     if (m >= 1e38f) l = __builtin_nanf("");
-    lse = l == 0.0f ? -__builtin_inff() : kLn2 * (m + __builtin_amdgcn_logf(l));
-    return l == 0.0f ? 0.0f : 1.0f / l;
+    if (l == 0.0f) return RowEnd{0.0f, 0.0f, -__builtin_inff()};
+    const float up = __builtin_amdgcn_exp2f(0.5f * (m - ml));
+    return RowEnd{1.0f / l * up, up, kLn2 * (ml + __builtin_amdgcn_logf(l))};
 }
 
+constexpr float kLimit = 0x1p14f;                // of a lane's sum of weights
 constexpr int kWaves = 4;
 constexpr int kPairDim = 128;                    // 32 rows a wavefront up to here, by registers
 
@@ -129,7 +152,7 @@ void attn_rows_kernel(AttnArgs a) {
     constexpr int kDim = 64 * C + (HALF ? 32 : 0), kTiles = kDim / 16, kSteps = kDim / 32;
     constexpr int kStride = kDim + 4, kRows = 16 * MT, kShift = MT == 2 ? 5 : 4;
     __shared__ __attribute__((aligned(16))) float lds[kWaves * kRows * kStride];
-    __shared__ float lds_m[kWaves * kRows], lds_l[kWaves * kRows];
+    __shared__ float lds_m[kWaves * kRows], lds_l[kWaves * kRows], lds_ml[kWaves * kRows];
     const int split = blockIdx.x % a.splits;
     const int head = blockIdx.x / a.splits % a.heads;
     const int64_t item = blockIdx.x / a.splits / a.heads;
@@ -181,12 +204,13 @@ void attn_rows_kernel(AttnArgs a) {
     const int u1 = u_first + (int)((int64_t)u_all * (split + 1) / a.splits);
 
     f32x4 o[MT][kTiles];
-    float m[MT], l[MT];
+    float m[MT], ml[MT], l[MT];
+    float limit = kLimit;                        // below 0: l's weights by themselves
 #pragma unroll
     for (int r = 0; r < MT; ++r) {
 #pragma unroll
         for (int d = 0; d < kTiles; ++d) o[r][d] = f32x4{0, 0, 0, 0};
-        m[r] = -1e30f;
+        m[r] = ml[r] = -1e30f;
         l[r] = 0.0f;
     }
 
@@ -306,20 +330,50 @@ void attn_rows_kernel(AttnArgs a) {
                 }
             };
             weights();
-            if (__any(!(fmaxf(sum[0], sum[1]) <= 0x1p14f))) {
-                float best = -1e30f;
+            if (__any(!(fmaxf(sum[0], sum[1]) <= limit))) {
+                const bool odd = limit < 0.0f || log_sv[0] == kOdd || log_sv[1] == kOdd;
+                if (odd) limit = -1.0f;
+                float log_v[2] = {log_sv[0], log_sv[1]}, best = -1e30f, best_l = -1e30f;
+                if (odd) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (log_sv[h] == kOdd) log_v[h] = inv_sv[h];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (log_sv[h] == -__builtin_inff()) s[r][h][e] = -__builtin_inff();   // no page
+                            best_l = fmaxf(best_l, s[r][h][e] * f[h]);
+                        }
+                    }
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        best = fmaxf(best, __builtin_fmaf(s[r][h][e], f[h], log_sv[h]));
+                        best = fmaxf(best, __builtin_fmaf(s[r][h][e], f[h], log_v[h]));
                 const float top = fmaxf(m[r], quad_max(best) - 4.0f);
                 const float down = __builtin_amdgcn_exp2f(m[r] - top);
                 m[r] = top;
-                l[r] *= down;
+                if (!odd) {
+                    ml[r] = top;
+                    l[r] *= down;
+                    weights();
+                } else {
+                    const float top_l = fmaxf(ml[r], quad_max(best_l) - 4.0f);
+                    l[r] *= __builtin_amdgcn_exp2f(ml[r] - top_l);
+                    ml[r] = top_l;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float off = log_v[h] - top;
+                        sum[h] = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            p[r][4 * h + e] = (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(s[r][h][e], f[h], off));
+                            l[r] += __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][h][e], f[h], -top_l));
+                        }
+                    }
+                }
 #pragma unroll
                 for (int d = 0; d < kTiles; ++d) o[r][d] *= down;
-                weights();
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) l[r] = __builtin_fmaf(sum[h], inv_sv[h], l[r]);
@@ -358,6 +412,7 @@ void attn_rows_kernel(AttnArgs a) {
         for (int d = 0; d < kTiles; ++d) *(f32x4 *)(lds + row * kStride + d * 16 + 4 * g) = o[r][d];
         if (g == 0) {
             lds_m[row] = m[r];
+            lds_ml[row] = ml[r];
             lds_l[row] = l[r];
         }
     }
@@ -367,27 +422,32 @@ void attn_rows_kernel(AttnArgs a) {
     for (int x16 = 0; x16 < MT; ++x16) {
         const int row = 16 * x16 + (threadIdx.x >> 4), at = (threadIdx.x & 15) * 4;
         if (row >= t.rows) return;
-        float mm = lds_m[row];
+        float mm = lds_m[row], mml = lds_ml[row];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) mm = fmaxf(mm, lds_m[w * kRows + row]);
+        for (int w = 1; w < kWaves; ++w) {
+            mm = fmaxf(mm, lds_m[w * kRows + row]);
+            mml = fmaxf(mml, lds_ml[w * kRows + row]);
+        }
         float f[kWaves], ll = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
             f[w] = __builtin_amdgcn_exp2f(lds_m[w * kRows + row] - mm);
-            ll = __builtin_fmaf(f[w], lds_l[w * kRows + row], ll);
+            ll = __builtin_fmaf(__builtin_amdgcn_exp2f(lds_ml[w * kRows + row] - mml),
+                                lds_l[w * kRows + row], ll);
         }
         const int rr = t.row0 + row, ri = rr / a.group, qh = head * a.group + rr - ri * a.group;
         const int64_t orow = t.seq.first_row + ri;
-        float lse, *part = nullptr;
-        const float by = row_end(mm, ll, lse);
+        float *part = nullptr;
+        const RowEnd end = row_end(mm, mml, ll);
         if (a.part) {
             part = a.part + ((((item * a.heads + head) * a.splits + split) << kShift) + row) * (kDim + 4);
             if (at == 0) {
                 part[kDim] = mm;
                 part[kDim + 1] = ll;
+                part[kDim + 2] = mml;
             }
         } else if (at == 0 && a.lse) {
-            a.lse[orow * a.heads * a.group + qh] = lse;
+            a.lse[orow * a.heads * a.group + qh] = end.lse;
         }
         for (int d = at; d < kDim; d += 64) {
             f32x4 sum = {0, 0, 0, 0};
@@ -401,7 +461,7 @@ void attn_rows_kernel(AttnArgs a) {
                 *(f32x4 *)(part + d) = sum;
             } else {
                 *(u32x2 *)(a.out + orow * a.ldo + (int64_t)qh * kDim + d) =
-                    u32x2{bf16x2_rne(sum[0] * by, sum[1] * by), bf16x2_rne(sum[2] * by, sum[3] * by)};
+                    u32x2{bf16x2_rne(end(sum[0]), end(sum[1])), bf16x2_rne(end(sum[2]), end(sum[3]))};
             }
         }
     }
@@ -560,10 +620,11 @@ __global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_til
     for (int d = 0; d < kBlocks; ++d)
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
-    float m = -1e30f, l = 0.0f;
+    float m = -1e30f, ml = -1e30f, l = 0.0f;
+    float limit = kLimit;                        // below 0: l's weights by themselves
 
-    // A wavefront stages 16 tokens of each run of 64.  Lane x: of the tokens of run j_in + x the place of their keys and the page's terms, 64
-    // runs at a time (as in attn_rows_kernel).
+    // A wavefront stages 16 tokens of each run of 64.  Lane x: of the tokens of run j_in + x
+    // the place of their keys and the page's terms, 64 runs at a time (as in attn_rows_kernel).
     int j_in = j0;
     int64_t at_in = 0;
     f32x4 terms_in;
@@ -718,17 +779,47 @@ __global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_til
         }
         if (half && !READY) store_terms(j + 2);
         const float most = fmaxf(sum[0], sum[1]);
-        if (__any(!(most <= 0x1p14f))) {
-            float best = -1e30f;
+        if (__builtin_expect(__any(!(most <= limit)), 0)) {
+            const bool odd = limit < 0.0f || __any(pt[0].y == kOdd || pt[1].y == kOdd);
+            if (odd) limit = -1.0f;
+            float log_v[2] = {pt[0].y, pt[1].y}, best = -1e30f, best_l = -1e30f;
+            if (odd) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) best = fmaxf(best, __builtin_fmaf(s[e], f[e >> 3], pt[e >> 3].y));
+                for (int x = 0; x < 2; ++x)
+                    if (pt[x].y == kOdd) log_v[x] = pt[x].z;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    if (pt[e >> 3].y == -__builtin_inff()) s[e] = -__builtin_inff();  // no page
+                    best_l = fmaxf(best_l, s[e] * f[e >> 3]);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) best = fmaxf(best, __builtin_fmaf(s[e], f[e >> 3], log_v[e >> 3]));
             const float n = fmaxf(m, fmaxf(best, __shfl_xor(best, 32)) - 4.0f);
             const float down = __builtin_amdgcn_exp2f(m - n);
             m = n;
-            l *= down;
 #pragma unroll
             for (int d = 0; d < kBlocks; ++d) o[d] *= down;
-            weights();
+            if (!odd) {
+                ml = n;
+                l *= down;
+                weights();
+            } else {
+                const float nl = fmaxf(ml, fmaxf(best_l, __shfl_xor(best_l, 32)) - 4.0f);
+                l *= __builtin_amdgcn_exp2f(ml - nl);
+                ml = nl;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float off = log_v[x] - n;
+                    sum[x] = 0.0f;
+                    pt[x].z = 1.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        p[x][e] = (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(s[8 * x + e], f[x], off));
+                        sum[x] += __builtin_amdgcn_exp2f(__builtin_fmaf(s[8 * x + e], f[x], -nl));
+                    }
+                }
+            }
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) l = __builtin_fmaf(sum[x], pt[x].z, l);
@@ -798,6 +889,7 @@ __global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_til
         if (h == 0) {
             part[kDim] = m;
             part[kDim + 1] = l;
+            part[kDim + 2] = ml;
         }
 #pragma unroll
         for (int d = 0; d < kBlocks; ++d)
@@ -808,17 +900,16 @@ __global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_til
         return;
     }
     if (!live) return;
-    float lse;
-    const float by = row_end(m, l, lse);
-    if (h == 0 && a.lse) a.lse[orow * a.heads * a.group + qh] = lse;
+    const RowEnd end = row_end(m, ml, l);
+    if (h == 0 && a.lse) a.lse[orow * a.heads * a.group + qh] = end.lse;
     uint16_t *out = a.out + orow * a.ldo + (int64_t)qh * kDim;
 #pragma unroll
     for (int d = 0; d < kBlocks; ++d)
 #pragma unroll
         for (int x = 0; x < 4; ++x)
             *(u32x2 *)(out + d * 32 + 8 * x + 4 * h) =
-                u32x2{bf16x2_rne(o[d][4 * x] * by, o[d][4 * x + 1] * by),
-                      bf16x2_rne(o[d][4 * x + 2] * by, o[d][4 * x + 3] * by)};
+                u32x2{bf16x2_rne(end(o[d][4 * x]), end(o[d][4 * x + 1])),
+                      bf16x2_rne(end(o[d][4 * x + 2]), end(o[d][4 * x + 3]))};
 }
 
 // Joins the splits of a tile, one wavefront a row: lane z holds the factors of splits z and
@@ -834,25 +925,29 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int dim, int
     if (item >= a.items || !find_tile(a, item, shift, t) || row >= t.rows) return;
     const int64_t step = (int64_t)(dim + 4) << shift;
     const float *p = a.part + slot * a.splits * step + row * (dim + 4);
-    float m[2], l[2];
+    float m[2], l[2], ml[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const int z = lane + 64 * x;
         m[x] = z < a.splits ? p[z * step + dim] : -1e30f;
         l[x] = z < a.splits ? p[z * step + dim + 1] : 0.0f;
+        ml[x] = z < a.splits ? p[z * step + dim + 2] : -1e30f;
     }
-    float mm = fmaxf(m[0], m[1]);
+    float mm = fmaxf(m[0], m[1]), mml = fmaxf(ml[0], ml[1]);
 #pragma unroll
-    for (int x = 1; x < 64; x <<= 1) mm = fmaxf(mm, __shfl_xor(mm, x));
+    for (int x = 1; x < 64; x <<= 1) {
+        mm = fmaxf(mm, __shfl_xor(mm, x));
+        mml = fmaxf(mml, __shfl_xor(mml, x));
+    }
     const float f0 = __builtin_amdgcn_exp2f(m[0] - mm), f1 = __builtin_amdgcn_exp2f(m[1] - mm);
-    float ll = __builtin_fmaf(f0, l[0], f1 * l[1]);
+    float ll = __builtin_fmaf(__builtin_amdgcn_exp2f(ml[0] - mml), l[0],
+                              __builtin_amdgcn_exp2f(ml[1] - mml) * l[1]);
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) ll += __shfl_xor(ll, x);
     const int rr = t.row0 + row, ri = rr / a.group, qh = head * a.group + rr - ri * a.group;
     const int64_t orow = t.seq.first_row + ri;
-    float lse;
-    const float by = row_end(mm, ll, lse);
-    if (lane == 0 && a.lse) a.lse[orow * a.heads * a.group + qh] = lse;
+    const RowEnd end = row_end(mm, mml, ll);
+    if (lane == 0 && a.lse) a.lse[orow * a.heads * a.group + qh] = end.lse;
     const int cols = dim >> 2, groups = 64 / cols, g = lane / cols, d = (lane - g * cols) * 4;
     f32x4 sum = {0, 0, 0, 0};
     for (int z0 = 0; z0 < a.splits; z0 += groups) {
@@ -872,7 +967,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int dim, int
         for (int e = 0; e < 4; ++e) all[e] += __shfl(sum[e], (lane + x * cols) & 63);
     if (g > 0) return;
     *(u32x2 *)(a.out + orow * a.ldo + (int64_t)qh * dim + d) =
-        u32x2{bf16x2_rne(all[0] * by, all[1] * by), bf16x2_rne(all[2] * by, all[3] * by)};
+        u32x2{bf16x2_rne(end(all[0]), end(all[1])), bf16x2_rne(end(all[2]), end(all[3]))};
 }
 
 // The same for few splits of tiles' many rows: 16 lanes a row and all its loads at once.  The
@@ -890,24 +985,27 @@ __global__ __launch_bounds__(256) void attn_join_few_kernel(AttnArgs a, int dim,
     if (!find_tile(a, item, shift, t) || row >= t.rows) return;
     const int64_t step = (int64_t)(dim + 4) << shift;
     const float *p = a.part + slot * a.splits * step + row * (dim + 4);
-    float f[kFewSplits], l[kFewSplits], mm = -1e30f, ll = 0.0f;
+    float f[kFewSplits], l[kFewSplits], ml[kFewSplits], mm = -1e30f, mml = -1e30f, ll = 0.0f;
 #pragma unroll
     for (int z = 0; z < kFewSplits; ++z) {
         f[z] = z < a.splits ? p[z * step + dim] : -1e30f;
         l[z] = z < a.splits ? p[z * step + dim + 1] : 0.0f;
+        ml[z] = z < a.splits ? p[z * step + dim + 2] : -1e30f;
     }
 #pragma unroll
-    for (int z = 0; z < kFewSplits; ++z) mm = fmaxf(mm, f[z]);
+    for (int z = 0; z < kFewSplits; ++z) {
+        mm = fmaxf(mm, f[z]);
+        mml = fmaxf(mml, ml[z]);
+    }
 #pragma unroll
     for (int z = 0; z < kFewSplits; ++z) {
         f[z] = __builtin_amdgcn_exp2f(f[z] - mm);
-        ll = __builtin_fmaf(f[z], l[z], ll);
+        ll = __builtin_fmaf(__builtin_amdgcn_exp2f(ml[z] - mml), l[z], ll);
     }
-    float lse;
-    const float by = row_end(mm, ll, lse);
+    const RowEnd end = row_end(mm, mml, ll);
     const int rr = t.row0 + row, ri = rr / a.group, qh = head * a.group + rr - ri * a.group;
     const int64_t orow = t.seq.first_row + ri;
-    if (d0 == 0 && a.lse) a.lse[orow * a.heads * a.group + qh] = lse;
+    if (d0 == 0 && a.lse) a.lse[orow * a.heads * a.group + qh] = end.lse;
     for (int d = d0; d < dim; d += 64) {
         f32x4 v[kFewSplits], sum = {0, 0, 0, 0};
 #pragma unroll
@@ -918,7 +1016,7 @@ __global__ __launch_bounds__(256) void attn_join_few_kernel(AttnArgs a, int dim,
 #pragma unroll
             for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(f[z], v[z][e], sum[e]);
         *(u32x2 *)(a.out + orow * a.ldo + (int64_t)qh * dim + d) =
-            u32x2{bf16x2_rne(sum[0] * by, sum[1] * by), bf16x2_rne(sum[2] * by, sum[3] * by)};
+            u32x2{bf16x2_rne(end(sum[0]), end(sum[1])), bf16x2_rne(end(sum[2]), end(sum[3]))};
     }
 }
 
