@@ -1,10 +1,10 @@
 """Attention over the 8-bit cache at the edges of what its entry point takes: caches without a
-page in every form, value scales of any size."""
+page in every form, value scales of any size, queries that are no finite numbers."""
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_attn_kv8 import Case, halves, w  # noqa: F401
+from test_gpu_attn_kv8 import Case, halves, near, w  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +77,40 @@ def test_many_tokens_of_zeros(w):
     c.scales[c.table[0], :, 1] = 0.0
     out, lse = c.run(w)
     assert (out[0] == 0).all() and abs(lse[0, 0].item() - np.log(150001)) < 1e-5
+
+
+@pytest.mark.parametrize("past,n,hq,hk", FORMS)
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_queries_that_are_not_finite(w, past, n, hq, hk, bad):
+    """NaN in the rows that hold one and see a token, whatever the signs of what they see; a row
+    that sees nothing gives 0 and -inf, and the others are as they were."""
+    print("CASE attn queries", past, n, hq, hk, bad, flush=True)
+    c = Case(past, n, hq, hk, 32 if n[0] == 900 else 64, 16)
+    if past[0] == 200:
+        c.lens[0] = n[0] - 1                                # its first row sees nothing
+    if past[0] == 1200:
+        c.table[0] = -1                                     # no row of it does
+    c.codes[0] = np.where(c.codes[0] == 0, 1, c.codes[0])   # no 0 that an infinity makes NaN
+    o, l, eo, el = c.want(max_rows=max(n))
+    hit = torch.zeros(l.shape, dtype=torch.bool, device="cuda")
+    for row, head in ((0, 0), (0, hq - 1), (n[0] // 2, 1), (n[0], 2)):
+        if row < len(c.q):
+            c.q[row, head, 5] = bad
+            hit[row, head] = l[row, head] > float("-inf")
+    out, lse = c.run(w, max_rows=max(n))
+    assert torch.isnan(lse[hit]).all() and torch.isnan(out[hit]).all()
+    near(out[~hit], lse[~hit], o[~hit], l[~hit], eo[~hit], el[~hit])
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf")])
+def test_one_token_of_either_sign(w, bad):
+    """One sign decides in the first row of a prompt: a score of -inf is NaN too."""
+    for sign in (1, -1):
+        c = Case([0], [3], 4, 1, 64, 16)
+        c.codes[0] = sign * 3
+        c.q[0, 1, 7] = bad
+        out, lse = c.run(w, scale=sign * 0.1)
+        assert torch.isnan(out[0, 1]).all() and torch.isnan(lse[0, 1])
+        assert torch.isfinite(out[1:]).all() and torch.isfinite(lse[0, 2:]).all()
+        out, lse = c.run(w)
+        assert torch.isnan(out[0, 1]).all() and torch.isnan(lse[0, 1])

@@ -96,13 +96,30 @@ __device__ __forceinline__ bool find_tile(const AttnArgs &a, int64_t item, int s
     return kv_tile(a.b, item, a.tiles, a.group, shift, a.max_rows, a.causal, a.window, t);
 }
 
+// The bits of the largest of eight bf16 without its sign, as binary32; NaN above infinity.
+__device__ __forceinline__ uint32_t top_bits(const u32x4 &w) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, max(w[i] << 16 & 0x7fff0000u, w[i] & 0x7fff0000u));
+    return top;
+}
 // 2^e that brings a row of Q whose largest element has the bits `top` to [2^14, 2^15), with
-// the sign of the scale; fac = |scale| / 2^e.
+// the sign of the scale; fac = |scale| / 2^e.  A row with an element that is no finite number
+// counts as zeros and has the factor NaN, which no weight sees (a factor is at least 1e-30)
+// and which makes NaN of the sum in the end, where it saw anything (row_sum).
 __device__ __forceinline__ float row_scale(uint32_t top, float scale, float &fac) {
+    if (top >= 0x7f800000u) {
+        fac = __builtin_nanf("");
+        return 0.0f;
+    }
     const int e = min(100, 14 + 127 - (int)(top >> 23));
     fac = fabsf(scale) * __uint_as_float((uint32_t)(127 - e) << 23);
     return copysignf(__uint_as_float((uint32_t)(127 + e) << 23), scale);
 }
+__device__ __forceinline__ _Float16 row_value(float f, float up) {
+    return up == 0.0f ? (_Float16)0.0f : (_Float16)(f * up);
+}
+__device__ __forceinline__ float row_sum(float l, float fac) { return l > 0.0f && fac != fac ? fac : l; }
 // Of a page: key scale, log2 of the value scale, its inverse.  Without one log2 is -inf, so
 // that every weight is 0.  For scales that l cannot be taken from p by (see above) log2 is
 // kOdd, and the third term what it really is (finite, as weights of 0 are multiplied by it
@@ -180,9 +197,7 @@ void attn_rows_kernel(AttnArgs a) {
         for (int k = 0; k < kSteps; ++k) {
             const int d = k < 2 * C ? (k >> 1) * 64 + 16 * g + 8 * (k & 1) : C * 64 + 8 * g;
             w[k] = live ? *(const u32x4 *)(p + d) : u32x4{0, 0, 0, 0};
-            float f[8];
-            bf16x8_to_f32(w[k], f);
-            top = max(top, __float_as_uint(absmax_f32x8(f)));
+            top = max(top, top_bits(w[k]));
         }
         top = max(top, (uint32_t)__shfl_xor((int)top, 16));
         top = max(top, (uint32_t)__shfl_xor((int)top, 32));
@@ -192,7 +207,7 @@ void attn_rows_kernel(AttnArgs a) {
             float f[8];
             bf16x8_to_f32(w[k], f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) q[x][k][e] = (_Float16)(f[e] * up);
+            for (int e = 0; e < 8; ++e) q[x][k][e] = row_value(f[e], up);
         }
     }
     // tokens that every row sees
@@ -406,7 +421,7 @@ void attn_rows_kernel(AttnArgs a) {
     }
 #pragma unroll
     for (int r = 0; r < MT; ++r) {
-        l[r] = quad_sum(l[r]);
+        l[r] = row_sum(quad_sum(l[r]), qfac[r]);
         const int row = wave * kRows + 16 * r + col;
 #pragma unroll
         for (int d = 0; d < kTiles; ++d) *(f32x4 *)(lds + row * kStride + d * 16 + 4 * g) = o[r][d];
@@ -589,9 +604,7 @@ __global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_til
             const int d = k < 4 * C ? (k >> 2) * 64 + 16 * (2 * (k >> 1 & 1) + h) + 8 * (k & 1)
                                     : C * 64 + 8 * (2 * (k & 1) + h);
             w[k] = live ? *(const u32x4 *)(p + d) : u32x4{0, 0, 0, 0};
-            float f[8];
-            bf16x8_to_f32(w[k], f);
-            top = max(top, __float_as_uint(absmax_f32x8(f)));
+            top = max(top, top_bits(w[k]));
         }
         top = max(top, (uint32_t)__shfl_xor((int)top, 32));
         const float up = row_scale(top, a.scale, qfac);
@@ -600,7 +613,7 @@ __global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_til
             float f[8];
             bf16x8_to_f32(w[k], f);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) q[k][x] = (_Float16)(f[x] * up);
+            for (int x = 0; x < 8; ++x) q[k][x] = row_value(f[x], up);
         }
     }
     const int pos = from + i;
@@ -879,7 +892,7 @@ __global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_til
 #pragma unroll
             for (int d = 0; d < kBlocks; ++d) o[d] = mfma32(value_operand(j1 - 1, 2 + x, d), p1[x], o[d]);
     }
-    l += __shfl_xor(l, 32);
+    l = row_sum(l + __shfl_xor(l, 32), qfac);
     const int qh = head * a.group + r - i * a.group;
     const int64_t orow = t.seq.first_row + i;
     if (a.part) {
