@@ -642,8 +642,9 @@ size_t w4a8_attn_kv8_workspace_bytes(int64_t rows, int64_t seqs, int32_t ragged,
  * numbers from 0 on, side by side too (value scales outside 2^-40 .. 2^20, zero among them,
  * take a slower path for the sum of exp(S_j)).  A row that sees a token of a page with a
  * scale that is negative or no finite number, or a score past 1e38, or that sees any and whose
- * query has an element that is no finite number, gives NaN, out and lse; of pages it does not
- * see scales may be anything.  The result does not depend on timing, but on
+ * query has an element that is no finite number, gives NaN, out and lse (with a `scale` that is
+ * none, or past 2e38, every row that sees any); of pages it does not see scales may be anything.
+ * The result does not depend on timing, but on
  * the sizes of the batch, which set the order of the sums.
  * max_rows bounds a sequence's rows: of one with more only the first max_rows are
  * computed, the rest left as they were, like rows behind the last sequence.

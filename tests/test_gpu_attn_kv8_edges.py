@@ -114,3 +114,18 @@ def test_one_token_of_either_sign(w, bad):
         assert torch.isfinite(out[1:]).all() and torch.isfinite(lse[0, 2:]).all()
         out, lse = c.run(w)
         assert torch.isnan(out[0, 1]).all() and torch.isnan(lse[0, 1])
+
+
+@pytest.mark.parametrize("past,n,hq,hk", FORMS)
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), float("-inf")])
+def test_scales_of_scores_that_are_not_finite(w, past, n, hq, hk, scale):
+    """NaN in every row that sees a token, 0 and -inf in the others."""
+    print("CASE attn scale", past, n, hq, hk, scale, flush=True)
+    c = Case(past, n, hq, hk, 32 if n[0] == 900 else 64, 16)
+    c.lens[1] = n[1] - 1
+    c.q[0] = 0.0
+    out, lse = c.run(w, max_rows=max(n), scale=scale)
+    none = n[0]                                             # that row sees nothing
+    assert (lse[none] == float("-inf")).all() and (out[none] == 0).all()
+    some = torch.arange(len(c.q), device="cuda") != none
+    assert torch.isnan(lse[some]).all() and torch.isnan(out[some]).all()

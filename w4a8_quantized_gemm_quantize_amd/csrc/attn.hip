@@ -106,9 +106,10 @@ __device__ __forceinline__ uint32_t top_bits(const u32x4 &w) {
 // 2^e that brings a row of Q whose largest element has the bits `top` to [2^14, 2^15), with
 // the sign of the scale; fac = |scale| / 2^e.  A row with an element that is no finite number
 // counts as zeros and has the factor NaN, which no weight sees (a factor is at least 1e-30)
-// and which makes NaN of the sum in the end, where it saw anything (row_sum).
+// and which makes NaN of the sum in the end, where it saw anything (row_sum); so does every
+// row where the scale is no finite number.
 __device__ __forceinline__ float row_scale(uint32_t top, float scale, float &fac) {
-    if (top >= 0x7f800000u) {
+    if (top >= 0x7f800000u || !(fabsf(scale) < __builtin_inff())) {
         fac = __builtin_nanf("");
         return 0.0f;
     }
