@@ -7,6 +7,7 @@ import torch
 from test_gpu_attn_kv8 import Case, halves, near, w  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
 
 
 @pytest.mark.parametrize("n", [1, 4, 33, 900])
@@ -129,3 +130,19 @@ def test_scales_of_scores_that_are_not_finite(w, past, n, hq, hk, scale):
     assert (lse[none] == float("-inf")).all() and (out[none] == 0).all()
     some = torch.arange(len(c.q), device="cuda") != none
     assert torch.isnan(lse[some]).all() and torch.isnan(out[some]).all()
+
+
+@pytest.mark.parametrize("past,n,hq,hk", FORMS)
+@pytest.mark.parametrize("size,scale", [(2.0 ** -115, 2.0 ** 112), (2.0 ** -125, 2.0 ** 122),
+                                        (2.0 ** -131, 2.0 ** 126)])
+def test_tiny_queries(w, past, n, hq, hk, size, scale):
+    """Down to subnormal bf16, with a scale that brings the scores back: no element loses bits
+    (all are multiples of 2^-133), the smallest of a row neither."""
+    print("CASE attn tiny queries", past, n, hq, hk, size, flush=True)
+    c = Case(past, n, hq, hk, 32 if n[0] == 900 else 64, 16, sharp=2.0)
+    c.q[..., ::2] *= 2.0 ** -10
+    c.q = (c.q.float() * size).to(BF)
+    assert (c.q != 0).any()
+    c.check(w, max_rows=max(n), scale=scale)
+    c.q[..., 1::2] = 0                                      # what a row's largest would hide
+    c.check(w, max_rows=max(n), scale=scale)

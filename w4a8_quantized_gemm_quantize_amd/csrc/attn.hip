@@ -113,7 +113,9 @@ __device__ __forceinline__ float row_scale(uint32_t top, float scale, float &fac
         fac = __builtin_nanf("");
         return 0.0f;
     }
-    const int e = min(100, 14 + 127 - (int)(top >> 23));
+    // 110 at most, so that fac keeps its bits: of smaller rows every element is then a multiple of
+    // 2^(110 - 133), which a half holds, and no bit is lost
+    const int e = min(110, 14 + 127 - (int)(top >> 23));
     fac = fabsf(scale) * __uint_as_float((uint32_t)(127 - e) << 23);
     return copysignf(__uint_as_float((uint32_t)(127 + e) << 23), scale);
 }
