@@ -41,7 +41,8 @@
  *     before launching, a call synchronizes its stream, copies its floating
  *     point inputs (bf16 activations or weights, binary32 scales or partial
  *     sums) to host memory and returns W4A8_ERR_NONFINITE, writing nothing, if
- *     any element is NaN or infinite; after launching it synchronizes again and
+ *     any element is NaN or infinite (of rotations and of the calls on the 8-bit
+ *     cache: any in a row that the call uses); after launching it synchronizes again and
  *     reports execution errors as W4A8_ERR_HIP.  Debug mode is slow (host
  *     scans) and meant for development only.
  */

@@ -7,9 +7,11 @@
 
 #include <atomic>
 #include <initializer_list>
+#include <new>
 #include <vector>
 
 #include "w4a8.h"
+#include "kv_index.hpp"
 #include "launch.hpp"
 
 namespace w4a8 {
@@ -219,13 +221,73 @@ w4a8_status check_kv_pointers(const w4a8::KvCall &c, const void *kv, const void 
         return W4A8_ERR_MISALIGNED;
     return W4A8_OK;
 }
-// Debug mode: the rows of a strided tensor.
-w4a8_status debug_check_rows(hipStream_t stream, const void *p, int64_t rows, int64_t ld,
-                             int64_t cols, bool bf16) {
+// Debug mode: rows first .. last - 1 of a strided tensor.
+w4a8_status debug_check_rows(hipStream_t stream, const void *p, int64_t first, int64_t last,
+                             int64_t ld, int64_t cols, bool bf16) {
     w4a8_status st = W4A8_OK;
-    for (int64_t t = 0; t < rows && st == W4A8_OK; ++t)
+    for (int64_t t = first; t < last && st == W4A8_OK; ++t)
         st = debug_check_inputs(
             stream, {{(const uint8_t *)p + t * ld * (bf16 ? 2 : 4), (size_t)cols, bf16}});
+    return st;
+}
+// Debug mode: device arrays on the host, so that only rows are checked that the call uses.
+bool debug_copy(hipStream_t stream, std::vector<int32_t> &to, const int32_t *from, int64_t rows,
+                int64_t cols, int64_t ld) {
+    try {
+        to.resize((size_t)(rows * cols) + 1);
+    } catch (const std::bad_alloc &) {
+        return false;
+    }
+    if (hipStreamSynchronize(stream) != hipSuccess) return false;
+    return rows * cols == 0 ||
+           hipMemcpy2D(to.data(), cols * 4, from, ld * 4, cols * 4, rows, hipMemcpyDeviceToHost) == hipSuccess;
+}
+struct DebugBatch {
+    std::vector<int32_t> start, lens, table;
+    w4a8::KvBatch b;
+    bool copy(const w4a8::KvCall &c, hipStream_t stream) {
+        if (!debug_copy(stream, lens, c.lens, 1, c.seqs, c.seqs) ||
+            (c.start && !debug_copy(stream, start, c.start, 1, (int64_t)c.seqs + 1, (int64_t)c.seqs + 1)) ||
+            !debug_copy(stream, table, c.table, c.seqs, c.blocks, c.ldb))
+            return false;
+        b = w4a8::KvBatch{c.start ? start.data() : nullptr, lens.data(), table.data(), c.blocks, c.seqs,
+                          c.blocks, c.pages, (int32_t)c.rows, __builtin_ctz(c.page)};
+        return true;
+    }
+};
+w4a8_status debug_check_written(hipStream_t stream, const w4a8::KvCall &c, const void *k, int64_t ldk,
+                                const void *v, int64_t ldv, bool bf16) {
+    DebugBatch d;
+    if (!d.copy(c, stream)) return W4A8_ERR_HIP;
+    const int64_t items = w4a8::kv_page_items(c.rows, c.seqs, c.start != nullptr, c.page);
+    const int64_t cols = (int64_t)c.kv_heads * c.dim;
+    w4a8_status st = W4A8_OK;
+    for (int64_t i = 0; i < items && st == W4A8_OK; ++i) {
+        const w4a8::KvPageItem it = w4a8::kv_page_item(d.b, i);
+        if (it.page < 0) continue;
+        const int64_t last = it.row + (it.last - it.first);
+        st = debug_check_rows(stream, k, it.row, last, ldk, cols, bf16);
+        if (st == W4A8_OK) st = debug_check_rows(stream, v, it.row, last, ldv, cols, bf16);
+    }
+    return st;
+}
+w4a8_status debug_check_queries(hipStream_t stream, const w4a8::KvCall &c, const void *q, int64_t ldq,
+                                int64_t cols, int64_t max_rows, bool causal, int32_t window) {
+    DebugBatch d;
+    if (!d.copy(c, stream)) return W4A8_ERR_HIP;
+    w4a8_status st = W4A8_OK;
+    for (int32_t s = 0; s < c.seqs; ++s) {
+        const w4a8::KvSeq r = w4a8::kv_seq(d.b, s);
+        for (int64_t i = 0; i < r.n && i < max_rows && st == W4A8_OK; ++i) {
+            const int64_t at = (int64_t)r.len - r.n + i;
+            const int64_t hi = causal && at + 1 < r.len ? at + 1 : r.len;
+            const int64_t lo = window && at - window + 1 > 0 ? at - window + 1 : 0;
+            bool seen = false;
+            for (int64_t b = lo / c.page; b < c.blocks && b * c.page < hi && !seen; ++b)
+                seen = w4a8::kv_page(d.b, s, b) >= 0;
+            if (seen) st = debug_check_rows(stream, q, r.first_row + i, r.first_row + i + 1, ldq, cols, true);
+        }
+    }
     return st;
 }
 
@@ -700,10 +762,16 @@ w4a8_status w4a8_qk_norm_rope(const void *q, int64_t ldq, const void *k, int64_t
     if (debug_sync_enabled()) {
         w4a8_status st = debug_check_inputs(stream, {{q_weight, (size_t)head_dim, false},
                                                      {k_weight, (size_t)head_dim, false}});
-        if (st == W4A8_OK && q_heads)
-            st = debug_check_rows(stream, q, tokens, ldq, (int64_t)q_heads * head_dim, in);
-        if (st == W4A8_OK && kv_heads)
-            st = debug_check_rows(stream, k, tokens, ldk, (int64_t)kv_heads * head_dim, in);
+        std::vector<int32_t> pos;
+        if (st == W4A8_OK && rot && !debug_copy(stream, pos, positions, 1, tokens, tokens))
+            st = W4A8_ERR_HIP;
+        for (int64_t t = 0; t < tokens && st == W4A8_OK; ++t) {
+            if (rot && (pos[t] < 0 || pos[t] >= max_pos)) continue;          // left as it is
+            if (q_heads)
+                st = debug_check_rows(stream, q, t, t + 1, ldq, (int64_t)q_heads * head_dim, in);
+            if (st == W4A8_OK && kv_heads)
+                st = debug_check_rows(stream, k, t, t + 1, ldk, (int64_t)kv_heads * head_dim, in);
+        }
         if (st != W4A8_OK) return st;
     }
     return finish(w4a8::launch_qk_norm_rope(q, ldq, k, ldk, in, q_weight, k_weight, eps, cos_sin,
@@ -734,11 +802,8 @@ w4a8_status w4a8_kv8_write(const void *k, int64_t ldk, const void *v, int64_t ld
     if (!k || !v) return W4A8_ERR_NULL;
     if (!aligned16(k) || !aligned16(v)) return W4A8_ERR_MISALIGNED;
     st = check_kv_pointers(c, kv, kv_scale);
-    if (st == W4A8_OK && debug_sync_enabled()) {
-        st = debug_check_rows(stream, k, rows, ldk, (int64_t)kv_heads * head_dim, bf16);
-        if (st == W4A8_OK)
-            st = debug_check_rows(stream, v, rows, ldv, (int64_t)kv_heads * head_dim, bf16);
-    }
+    if (st == W4A8_OK && debug_sync_enabled())
+        st = debug_check_written(stream, c, k, ldk, v, ldv, bf16);
     if (st != W4A8_OK) return st;
     return finish(w4a8::launch_kv8_write(c, k, ldk, v, ldv, bf16, kv, kv_scale, stream), stream);
 }
@@ -809,7 +874,8 @@ w4a8_status w4a8_attn_kv8(const uint16_t *q, int64_t ldq, const uint8_t *kv,
     if (ws_bytes < need) return W4A8_ERR_SHAPE;
     st = check_kv_pointers(c, kv, kv_scale);
     if (st == W4A8_OK && debug_sync_enabled())
-        st = debug_check_rows(stream, q, rows, ldq, (int64_t)q_heads * head_dim, true);
+        st = debug_check_queries(stream, c, q, ldq, (int64_t)q_heads * head_dim, max_rows, causal != 0,
+                                 window);
     if (st != W4A8_OK) return st;
     return finish(w4a8::launch_attn(c, q, ldq, kv, kv_scale, max_rows, q_heads, causal != 0, window,
                                     scale, out, ldo, lse, workspace, stream),

@@ -19,6 +19,7 @@
 #include <stdint.h>
 
 #ifdef __HIPCC__
+#include <hip/hip_runtime.h>
 #define KV_INLINE __host__ __device__ __forceinline__
 #else
 #define KV_INLINE inline
