@@ -134,7 +134,10 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(RopeArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(x[n][i], x[n][i], sum);
             sum = group_sum<LANES>(sum);
-            const float r = __builtin_amdgcn_rsqf(sum * a.inv_dim + a.eps);
+            const float mean = sum * a.inv_dim + a.eps;
+            // the instruction takes subnormal numbers for 0
+            const float r = mean < 0x1p-126f ? __builtin_amdgcn_rsqf(mean * 0x1p32f) * 0x1p16f
+                                             : __builtin_amdgcn_rsqf(mean);
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[n][i] = x[n][i] * r * (is_q ? w[0][i] : w[1][i]);
         }
