@@ -880,7 +880,8 @@ def _kv_args(fn, kv, kv_scale, block_table, lens, row_start, dev):
             ldb = blocks
     if row_start is not None:
         _flat(fn, row_start, torch.int32, seqs + 1, "row_start", dev)
-    return (pages, kv_heads, page, dim), ldb, blocks, seqs
+    # the library counts them in 32 bits, and refuses the most that these hold
+    return (pages, kv_heads, page, dim), ldb, min(blocks, 0x7fffffff), seqs
 
 
 def kv8_write(k, v, kv, kv_scale, block_table, lens, row_start=None, stream=None):
