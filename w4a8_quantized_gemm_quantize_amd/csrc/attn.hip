@@ -500,7 +500,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 __device__ __forceinline__ f32x16 mfma32(half8_t a, half8_t b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
-constexpr int min_of(int a, int b) { return a < b ? a : b; }
 // Workgroups of a compute unit, by registers and LDS.  (Workgroups of eight wavefronts and 256
 // rows stage half as much each, and gain nothing: 671 us for 673 on 5124 and 3067 rows of 64
 // x 128, 8 us more on short prompts, which have too few of them.)
@@ -743,12 +742,11 @@ __global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_til
         };
         // One product at a time with its share of the weights' steps, in this order: the
         // scheduler left to itself puts the products first and the weights behind them.
-        constexpr int kProducts = 2 * kBlocks, kAll = kSteps + kProducts, kAhead = 4;
+        constexpr int kAll = 2 * kSteps, kAhead = 4;        // as many sums' as scores': kDim / 16
         auto operand = [&](int n) {              // products in turn: a score's, a sum's
-            const bool score = n < 2 * min_of(kSteps, kProducts) ? n % 2 == 0 : kSteps > kProducts;
-            const int k = n < 2 * min_of(kSteps, kProducts) ? n / 2 : n - min_of(kSteps, kProducts);
-            return score ? key_operand(j + half, 1 - half, k)
-                         : value_operand(j - 1 + half, 2 * (1 - half) + k / kBlocks, k % kBlocks);
+            const int k = n / 2;
+            return n % 2 == 0 ? key_operand(j + half, 1 - half, k)
+                              : value_operand(j - 1 + half, 2 * (1 - half) + k / kBlocks, k % kBlocks);
         };
         half8_t ring[kAhead];
 #pragma unroll
@@ -762,9 +760,8 @@ __global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_til
 #pragma unroll
         for (int n = 0; n < kAll + 2; ++n) {
             if (n < kAll) {
-                const bool score = n < 2 * min_of(kSteps, kProducts) ? n % 2 == 0 : kSteps > kProducts;
-                const int k = n < 2 * min_of(kSteps, kProducts) ? n / 2 : n - min_of(kSteps, kProducts);
-                if (score) next = mfma32(ring[n % kAhead], q[k], next);
+                const int k = n / 2;
+                if (n % 2 == 0) next = mfma32(ring[n % kAhead], q[k], next);
                 else o[k % kBlocks] = mfma32(ring[n % kAhead], before[k / kBlocks], o[k % kBlocks]);
                 if (n + kAhead < kAll) ring[n % kAhead] = operand(n + kAhead);
             }
