@@ -793,7 +793,8 @@ __global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_til
         if (half && !READY) store_terms(j + 2);
         const float most = fmaxf(sum[0], sum[1]);
         if (__builtin_expect(__any(!(most <= limit)), 0)) {
-            const bool odd = limit < 0.0f || __any(pt[0].y == kOdd || pt[1].y == kOdd);
+            const bool odd_page = __any(pt[0].y == kOdd || pt[1].y == kOdd);
+            const bool odd = limit < 0.0f || odd_page;
             if (odd) limit = -1.0f;
             float log_v[2] = {pt[0].y, pt[1].y}, best = -1e30f, best_l = -1e30f;
             if (odd) {
@@ -831,6 +832,17 @@ __global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_til
                         p[x][e] = (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(s[8 * x + e], f[x], off));
                         sum[x] += __builtin_amdgcn_exp2f(__builtin_fmaf(s[8 * x + e], f[x], -nl));
                     }
+                }
+                // Where m and ml are as close as scales between 2^-40 and 2^4 leave them, for
+                // all rows, l is taken from p again (a first page of zeros, 5124 and 3067 rows
+                // of 64 x 128: 995 us without).
+                const float apart = nl - n;
+                if (!odd_page && __all(apart >= -4.0f && apart <= 40.0f)) {
+                    const float by = __builtin_amdgcn_exp2f(apart);
+                    l *= by;
+                    ml = n;
+                    pt[0].z = pt[1].z = by;
+                    limit = kLimit;
                 }
             }
         }
