@@ -96,31 +96,31 @@ __device__ __forceinline__ bool find_tile(const AttnArgs &a, int64_t item, int s
     return kv_tile(a.b, item, a.tiles, a.group, shift, a.max_rows, a.causal, a.window, t);
 }
 
-// The bits of the largest of eight bf16 without its sign, as binary32; NaN above infinity.
-__device__ __forceinline__ uint32_t top_bits(const u32x4 &w) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) top = max(top, max(w[i] << 16 & 0x7fff0000u, w[i] & 0x7fff0000u));
-    return top;
+// The largest of a row's bf16 by their bits without the sign, NaN above infinity: even and odd
+// elements apart, then of both as binary32.
+__device__ __forceinline__ uint32_t max_bits(uint32_t top, uint32_t w) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(v2u16, top),
+                                                                  __builtin_bit_cast(v2u16, w & 0x7fff7fffu)));
 }
+__device__ __forceinline__ uint32_t top_bits(uint32_t top) { return max(top << 16, top & 0xffff0000u); }
 // 2^e that brings a row of Q whose largest element has the bits `top` to [2^14, 2^15), with
 // the sign of the scale; fac = |scale| / 2^e.  A row with an element that is no finite number
-// counts as zeros and has the factor NaN, which no weight sees (a factor is at least 1e-30)
-// and which makes NaN of the sum in the end, where it saw anything (row_sum); so does every
-// row where the scale is no finite number.
+// has the factor NaN, and so has every row where the scale is none; such rows count as zeros
+// (row_words).  No weight sees that factor (one is at least 1e-30); it makes NaN of the sum
+// in the end, where the row saw anything (row_sum).
 __device__ __forceinline__ float row_scale(uint32_t top, float scale, float &fac) {
-    if (top >= 0x7f800000u || !(fabsf(scale) < __builtin_inff())) {
-        fac = __builtin_nanf("");
-        return 0.0f;
-    }
+    const bool none = top >= 0x7f800000u || !(fabsf(scale) < __builtin_inff());
     // 110 at most, so that fac keeps its bits: of smaller rows every element is then a multiple of
     // 2^(110 - 133), which a half holds, and no bit is lost
     const int e = min(110, 14 + 127 - (int)(top >> 23));
-    fac = fabsf(scale) * __uint_as_float((uint32_t)(127 - e) << 23);
+    fac = none ? __builtin_nanf("") : fabsf(scale) * __uint_as_float((uint32_t)(127 - e) << 23);
     return copysignf(__uint_as_float((uint32_t)(127 + e) << 23), scale);
 }
-__device__ __forceinline__ _Float16 row_value(float f, float up) {
-    return up == 0.0f ? (_Float16)0.0f : (_Float16)(f * up);
+template <int N>
+__device__ __forceinline__ void row_words(u32x4 (&w)[N], float fac) {
+    if (!__any(fac != fac)) return;
+#pragma unroll
+    for (int k = 0; k < N; ++k) w[k] = fac != fac ? u32x4{0, 0, 0, 0} : w[k];
 }
 __device__ __forceinline__ float row_sum(float l, float fac) { return l > 0.0f && fac != fac ? fac : l; }
 // Of a page: key scale, log2 of the value scale, its inverse.  Without one log2 is -inf, so
@@ -200,17 +200,20 @@ void attn_rows_kernel(AttnArgs a) {
         for (int k = 0; k < kSteps; ++k) {
             const int d = k < 2 * C ? (k >> 1) * 64 + 16 * g + 8 * (k & 1) : C * 64 + 8 * g;
             w[k] = live ? *(const u32x4 *)(p + d) : u32x4{0, 0, 0, 0};
-            top = max(top, top_bits(w[k]));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = max_bits(top, w[k][i]);
         }
+        top = top_bits(top);
         top = max(top, (uint32_t)__shfl_xor((int)top, 16));
         top = max(top, (uint32_t)__shfl_xor((int)top, 32));
         const float up = row_scale(top, a.scale, qfac[x]);
+        row_words(w, qfac[x]);
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
             float f[8];
             bf16x8_to_f32(w[k], f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) q[x][k][e] = row_value(f[e], up);
+            for (int e = 0; e < 8; ++e) q[x][k][e] = (_Float16)(f[e] * up);
         }
     }
     // tokens that every row sees
@@ -606,16 +609,19 @@ __global__ __launch_bounds__(256, tile_groups(64 * C + 32 * HALF)) void attn_til
             const int d = k < 4 * C ? (k >> 2) * 64 + 16 * (2 * (k >> 1 & 1) + h) + 8 * (k & 1)
                                     : C * 64 + 8 * (2 * (k & 1) + h);
             w[k] = live ? *(const u32x4 *)(p + d) : u32x4{0, 0, 0, 0};
-            top = max(top, top_bits(w[k]));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = max_bits(top, w[k][i]);
         }
+        top = top_bits(top);
         top = max(top, (uint32_t)__shfl_xor((int)top, 32));
         const float up = row_scale(top, a.scale, qfac);
+        row_words(w, qfac);
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
             float f[8];
             bf16x8_to_f32(w[k], f);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) q[k][x] = row_value(f[x], up);
+            for (int x = 0; x < 8; ++x) q[k][x] = (_Float16)(f[x] * up);
         }
     }
     const int pos = from + i;
