@@ -639,9 +639,10 @@ size_t w4a8_attn_kv8_workspace_bytes(int64_t rows, int64_t seqs, int32_t ragged,
  *   lse = ln sum_j exp(S_j);  a row that sees nothing: out 0, lse -inf.
  * k_j and v_j are code * scale.  Products are exact and summed in binary32 (elements of q
  * below 2^-29 of their row's largest lose bits), exp(S_j) enters the sum over v_j rounded
- * to 11 bits, the statistics are binary32, and out is rounded once.  Scales may be any finite
- * numbers from 0 on, side by side too (value scales outside 2^-40 .. 2^20, zero among them,
- * take a slower path for the sum of exp(S_j)).  A row that sees a token of a page with a
+ * to 11 bits, or 22 where a sequence has at most 16 rows times q_heads / kv_heads (64 past a
+ * head_dim of 128), the statistics are binary32, and out is rounded once.  Scales may be any
+ * finite numbers from 0 on, side by side too (value scales outside 2^-40 .. 2^20, zero among
+ * them, take a slower path for the sum of exp(S_j)).  A row that sees a token of a page with a
  * scale that is negative or no finite number, or a score past 1e38, or that sees any and whose
  * query has an element that is no finite number, gives NaN, out and lse (with a `scale` that is
  * none, or past 2e38, every row that sees any); of pages it does not see scales may be anything.

@@ -146,3 +146,45 @@ def test_tiny_queries(w, past, n, hq, hk, size, scale):
     c.check(w, max_rows=max(n), scale=scale)
     c.q[..., 1::2] = 0                                      # what a row's largest would hide
     c.check(w, max_rows=max(n), scale=scale)
+
+
+@pytest.mark.parametrize("dim,hq,rows", [(32, 8, 1), (96, 5, 1), (128, 4, 1), (128, 8, 2), (192, 8, 4), (256, 4, 3)])
+@pytest.mark.parametrize("past", [3, 4000])
+def test_weights_of_few_rows_keep_22_bits(w, dim, hq, rows, past):
+    """Up to 16 packed rows (64 past 128 elements a head) the weights enter the sum over the values
+    with 22 bits: out is the right one rounded to bf16, but for what the other steps may be off by.
+    Few tokens of large weight, each with a query of one element, so that those are small:
+      score   one product: 4 u (|s| + |lse| + 128) for the factors and the exponent's sum (as in
+              kv8_util.attention, whose first term is the sum of dim products)
+      weight  exp2 2^-22, two halves 2^-22, or below 2^-14 of a reference that is at most a 16th of
+              the largest weight 2^-25 of that
+    A half alone may be off by 2^-12."""
+    print("CASE attn 22 bits", dim, hq, rows, past, flush=True)
+    c = Case([past] * 40, [rows] * 40, hq, 1, dim, 16, seed=dim + past)
+    c.scales[:, :, 0] *= 16.0
+    g = torch.Generator(device="cuda").manual_seed(past)
+    at = torch.randint(0, dim, (len(c.q), hq, 1), generator=g, device="cuda")
+    c.q = torch.zeros_like(c.q).scatter_(2, at, torch.randn(at.shape, generator=g, device="cuda").to(BF) + 1)
+    if past > 100:                                          # few tokens with a weight among many
+        c.codes[0, :, :, 1:] = np.clip(c.codes[0, :, :, 1:], -20, 20)
+    out, lse = c.run(w, max_rows=rows, scale=0.25)
+    u = 2.0 ** -24
+    for s in range(40):
+        n = past + rows
+        page = torch.from_numpy(c.table[s][np.arange(n) // 16]).cuda().long()
+        slot = torch.arange(n, device="cuda") % 16
+        k, v = (torch.from_numpy(c.codes[i]).cuda()[page, 0, slot].double() *
+                torch.from_numpy(c.scales).cuda()[page, 0, i, None].double() for i in range(2))
+        sv = torch.from_numpy(c.scales).cuda()[page, 0, 1].double()
+        for i in range(rows):
+            r, m = s * rows + i, past + i + 1               # tokens seen
+            score = 0.25 * torch.matmul(c.q[r].double(), k[:m].T.contiguous())
+            l = torch.logsumexp(score, 1, keepdim=True)
+            p = torch.exp(score - l)
+            o, a = torch.matmul(p, v[:m]), torch.matmul(p, v[:m].abs())
+            ds = 4 * u * (score.abs().amax(1, keepdim=True) + l.abs() + 128)
+            unit = (p * sv[:m]).amax(1, keepdim=True)
+            bound = (2 * ds + 2.0 ** -21 + 2.0 ** -21 + 2 * u * (m + 64)) * a + m * 2.0 ** -29 * 127 * unit
+            half = torch.exp2(torch.floor(torch.log2(o.abs().clamp_min(2.0 ** -120))) - 8)   # of a step
+            off = (out[r].double() - o).abs()
+            assert (off <= half + bound * (1 + 2.0 ** -7)).all(), (off / (half + bound)).max().item()

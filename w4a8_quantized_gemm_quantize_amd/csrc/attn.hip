@@ -14,9 +14,10 @@
 // page of value scale sv,
 //   t_j = s_j + log2 sv,   p_j = 2^(t_j - m),   O = sum p_j codes_j,   l = sum p_j / sv,
 //   out = O / l,   lse = ln 2 (m + log2 l)
-// so P needs no factor per page, and what its rounding to a half loses (2^-11 of a p_j, or
+// so P needs no factor per page, and what its rounding to a half loses (2^-12 of a p_j, or
 // 2^-25 where it is below 2^-14) is measured against the largest product p_j sv, not against
-// p_j alone.  t, m, l and O are binary32.  m is no maximum but near one: it moves, to the
+// p_j alone.  Few rows, which memory bounds, take what the half leaves of p_j through a second
+// product (kLow); prompts, which the products bound, would need half as many again.  t, m, l and O are binary32.  m is no maximum but near one: it moves, to the
 // maximum less 4, only when some p_j come out so large that a lane's sum of them exceeds
 // 2^14, which a half still holds; so no maximum is taken while nothing overflows, and most
 // tiles rescale nothing.  A factor of scores below 1e-30 counts as 1e-30, so that hidden
@@ -167,10 +168,14 @@ constexpr int kPairDim = 128;                    // 32 rows a wavefront up to he
 // TB/s; with loads that also fill the L2 203 us, with both buffered twice (two wavefronts
 // on a SIMD for three) 288 us.
 template <int C, bool HALF, int MT>              // full chunks of 64 elements, and a half one
-__global__ __launch_bounds__(kWaves * 64, MT == 2 ? 2 : 64 * C + 32 * HALF <= 96 ? 4 : C == 2 && !HALF ? 3 : 2)
+__global__ __launch_bounds__(kWaves * 64, MT == 2 ? 2 : 64 * C + 32 * HALF <= 64 ? 4 : 64 * C + 32 * HALF <= 128 ? 3 : 2)
 void attn_rows_kernel(AttnArgs a) {
     constexpr int kDim = 64 * C + (HALF ? 32 : 0), kTiles = kDim / 16, kSteps = kDim / 32;
     constexpr int kStride = kDim + 4, kRows = 16 * MT, kShift = MT == 2 ? 5 : 4;
+    // Weights as two halves, 22 bits: free for 16 rows (64 x 8192 tokens 181 us for 182, heads of
+    // 96 with three wavefronts a SIMD for four); 24, 40 and 64 rows of the other form would pay
+    // 60 -> 63, 75 -> 86 and 74 -> 87 us.
+    constexpr bool kLow = MT == 1;
     __shared__ __attribute__((aligned(16))) float lds[kWaves * kRows * kStride];
     __shared__ float lds_m[kWaves * kRows], lds_l[kWaves * kRows], lds_ml[kWaves * kRows];
     const int split = blockIdx.x % a.splits;
@@ -323,7 +328,11 @@ void attn_rows_kernel(AttnArgs a) {
         }
         if (n + 1 - n_in == 64) look_up(n + 1);
         load_keys(n + 1);
-        half8_t p[MT];
+        half8_t p[MT], low;
+        auto weight = [&](float w, int r, int at) {
+            p[r][at] = (_Float16)w;
+            if constexpr (kLow) low[at] = (_Float16)(w - (float)p[r][at]);
+        };
 #pragma unroll
         for (int r = 0; r < MT; ++r) {
             if (first + 32 > all_hi || first < all_lo) {
@@ -346,7 +355,7 @@ void attn_rows_kernel(AttnArgs a) {
                     for (int e = 0; e < 4; ++e) {
                         const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][h][e], f[h], off));
                         sum[h] += w;
-                        p[r][4 * h + e] = (_Float16)w;
+                        weight(w, r, 4 * h + e);
                     }
                 }
             };
@@ -388,7 +397,7 @@ void attn_rows_kernel(AttnArgs a) {
                         sum[h] = 0.0f;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            p[r][4 * h + e] = (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(s[r][h][e], f[h], off));
+                            weight(__builtin_amdgcn_exp2f(__builtin_fmaf(s[r][h][e], f[h], off)), r, 4 * h + e);
                             l[r] += __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][h][e], f[h], -top_l));
                         }
                     }
@@ -406,6 +415,7 @@ void attn_rows_kernel(AttnArgs a) {
                 const half8_t value = codes8h(x.v[0][c][j], x.v[1][c][j]);
 #pragma unroll
                 for (int r = 0; r < MT; ++r) o[r][4 * c + j] = mfma16(value, p[r], o[r][4 * c + j]);
+                if constexpr (kLow) o[0][4 * c + j] = mfma16(value, low, o[0][4 * c + j]);
             }
         if constexpr (HALF) {
 #pragma unroll
@@ -413,6 +423,7 @@ void attn_rows_kernel(AttnArgs a) {
                 const half8_t value = codes8h(x.vh[0][j], x.vh[1][j]);
 #pragma unroll
                 for (int r = 0; r < MT; ++r) o[r][4 * C + j] = mfma16(value, p[r], o[r][4 * C + j]);
+                if constexpr (kLow) o[0][4 * C + j] = mfma16(value, low, o[0][4 * C + j]);
             }
         }
         load_values(n + 1);
@@ -504,8 +515,8 @@ __device__ __forceinline__ f32x16 mfma32(half8_t a, half8_t b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 // Workgroups of a compute unit, by registers and LDS.  (Workgroups of eight wavefronts and 256
-// rows stage half as much each, and gain nothing: 671 us for 673 on 5124 and 3067 rows of 64
-// x 128, 8 us more on short prompts, which have too few of them.)
+// rows stage half as much each, and gained nothing while every tile converted its tokens: 671
+// us for 673 on 5124 and 3067 rows of 64 x 128, 8 us more on short prompts, which have too few.)
 constexpr int tile_groups(int dim) { return dim <= 64 ? 3 : dim <= 128 ? 2 : 1; }
 constexpr int kTileShift = 7;                    // packed rows of a tile: 128
 constexpr int kWaitLoads = 0x0f70;               // s_waitcnt vmcnt(0)
