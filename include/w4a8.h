@@ -621,8 +621,9 @@ w4a8_status w4a8_kv8_read(const uint8_t *kv, const float *kv_scale, const int32_
 /* Bytes of workspace w4a8_attn_kv8 needs for these sizes (0: none, or sizes it refuses);
  * `ragged` is whether row_start is given.  It holds partial results where few rows see many
  * tokens, and where many rows do the tokens that the block tables can name converted to
- * halves (only where those take at most 1 GiB: a table no wider than its longest sequence
- * lets long prompts run 4 to 6 % faster). */
+ * halves (only where those take at most 1 GiB).  Both follow the tables' width, not the
+ * lengths: a table no wider than its longest sequence lets long prompts run 4 to 6 % faster,
+ * and a single short sequence twice as fast as in a table of 131072 tokens. */
 size_t w4a8_attn_kv8_workspace_bytes(int64_t rows, int64_t seqs, int32_t ragged,
                                      int64_t max_rows, int32_t blocks, int32_t q_heads,
                                      int32_t kv_heads, int32_t head_dim, int32_t page);
@@ -639,15 +640,15 @@ size_t w4a8_attn_kv8_workspace_bytes(int64_t rows, int64_t seqs, int32_t ragged,
  *   lse = ln sum_j exp(S_j);  a row that sees nothing: out 0, lse -inf.
  * k_j and v_j are code * scale.  Products are exact and summed in binary32 (elements of q
  * below 2^-29 of their row's largest lose bits), exp(S_j) enters the sum over v_j rounded
- * to 11 bits, or 22 where a sequence has at most 16 rows times q_heads / kv_heads (64 past a
- * head_dim of 128), the statistics are binary32, and out is rounded once.  Scales may be any
- * finite numbers from 0 on, side by side too (value scales outside 2^-40 .. 2^20, zero among
- * them, take a slower path for the sum of exp(S_j)).  A row that sees a token of a page with a
- * scale that is negative or no finite number, or a score past 1e38, or that sees any and whose
- * query has an element that is no finite number, gives NaN, out and lse (with a `scale` that is
- * none, or past 2e38, every row that sees any); of pages it does not see scales may be anything.
- * The result does not depend on timing, but on
- * the sizes of the batch, which set the order of the sums.
+ * to 11 bits, or to 22 where max_rows (1 without row_start) times q_heads / kv_heads is at
+ * most 16 (64 past a head_dim of 128), the statistics are binary32, and out is rounded once.
+ * Scales may be any finite numbers from 0 on, side by side too (value scales outside 2^-40 ..
+ * 2^20, zero among them, take a slower path for the sum of exp(S_j)).  NaN, out and lse, is
+ * what a row gives that sees a token of a page with a scale that is negative or no finite
+ * number, or a score past 1e38, or that sees any token and has an element in its query that
+ * is no finite number, or a `scale` that is none or past 2e38; of pages that it does not see
+ * scales may be anything.  The result does not depend on timing, but on the sizes of the
+ * batch, which set the order of the sums.
  * max_rows bounds a sequence's rows: of one with more only the first max_rows are
  * computed, the rest left as they were, like rows behind the last sequence.
  * Requires q_heads a positive multiple of kv_heads, max_rows >= 1, window >= 0

@@ -1140,8 +1140,8 @@ Plan attn_plan(int64_t rows, int64_t seqs, bool ragged, int64_t max_rows, int64_
     p.halves_bytes = (size_t)seqs * kv_heads * p.runs * 64 * dim * 4;
     p.terms_bytes = (size_t)seqs * kv_heads * p.runs * 64;
     // Of a windowed call a tile sees max_tokens, and a token is seen by so many tiles (5124 and
-    // 3067 rows of 64 x 128, window 30: 137 us with it, 131 without, 128: 156 and 146; 500 rows
-    // of 28 x 64, 512: 19.4 and 18.1; 5124 and 3067 again, 1024: 346 and 345).
+    // 3067 rows of 64 x 128, window 30: 132 us with it, 124 without, 128: 140 and 129, 1024: 308
+    // and 311; 500 rows of 28 x 64, 512: 19.2 and 17.7).
     const int64_t many = rows * group / height;
     const int64_t readers = window ? kv_min(many, seqs * (window * group / height + 1)) : many;
     if (p.shift != kTileShift || readers < 8 * seqs || (double)many * kv_heads * max_tokens < 2e6 ||
