@@ -239,8 +239,10 @@ bool debug_copy(hipStream_t stream, std::vector<int32_t> &to, const int32_t *fro
         return false;
     }
     if (hipStreamSynchronize(stream) != hipSuccess) return false;
-    return rows * cols == 0 ||
-           hipMemcpy2D(to.data(), cols * 4, from, ld * 4, cols * 4, rows, hipMemcpyDeviceToHost) == hipSuccess;
+    if (rows * cols == 0) return true;
+    if (rows == 1 || ld == cols)                 // a pitch has a limit
+        return hipMemcpy(to.data(), from, (size_t)(rows * cols) * 4, hipMemcpyDeviceToHost) == hipSuccess;
+    return hipMemcpy2D(to.data(), cols * 4, from, ld * 4, cols * 4, rows, hipMemcpyDeviceToHost) == hipSuccess;
 }
 struct DebugBatch {
     std::vector<int32_t> start, lens, table;
